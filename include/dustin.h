@@ -60,9 +60,15 @@ typedef enum dustin_status {
 #define DUSTIN_DEVFLAG_PAGE_RANGE 0x2u  /* page id < 0 or >= num_pages      */
 #define DUSTIN_DEVFLAG_WAIT_TIMEOUT 0x4u /* a pipeline wait gave up (~1 s);
                                             the outputs of that call are void */
+#define DUSTIN_DEVFLAG_NO_PAGES 0x8u     /* a sequence could not grow        */
+#define DUSTIN_DEVFLAG_INDEX_ORDER 0x10u /* compaction in place over indices
+                                            that do not ascend strictly      */
 
 #define DUSTIN_NORM_NONE 0 /* hybrid mix of the raw score vectors          */
 #define DUSTIN_NORM_L1 1   /* each score vector divided by its own sum     */
+
+#define DUSTIN_DTYPE_F32 0  /* IEEE binary32                                */
+#define DUSTIN_DTYPE_BF16 1 /* bfloat16 bit patterns                        */
 
 /*
  * One layer's KV cache for one (layer) of the target or the draft.
@@ -340,6 +346,119 @@ int dustin_full_verify_attn_window(int b, int h_q, int h_kv, int d, int w, int n
                                    const dustin_kv* win, float scale, void* o,
                                    float* lse, void* ws, size_t ws_bytes,
                                    unsigned flags, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Verification of drafted tokens (speculative sampling), the step that
+ * follows the target's pass over its w verification rows.  Not an API of the
+ * paper.
+ *
+ * Sequence i has g = n_draft[i] drafted tokens x_0 .. x_{g-1} (g <= w - 1;
+ * n_draft NULL: w - 1 each; values outside [0, w - 1] are clamped), the
+ * draft model's distribution q_t over the vocabulary each was drawn from,
+ * and the target's distributions p_0 .. p_g.  Draft t is accepted while
+ *   u_accept[i][t] * q_t(x_t) < p_t(x_t)      (products compared exactly),
+ * up to the first that is not.  With a drafts accepted, one more token is
+ * drawn by inversion: the first j with C_j > u_sample[i] * C_last, where C
+ * is the running sum, over ascending tokens, of
+ *   max(p_a(j) - q_a(j), 0)   if a < g (a draft was rejected),
+ *   p_a(j)                    if a == g, or if that residual has no mass.
+ * So the tokens follow the target's distribution if u_accept and u_sample
+ * are independent uniforms in [0, 1).  With p_draft NULL the drafts are
+ * taken as certain (q is 1 at the draft, 0 elsewhere), as for drafts found
+ * by lookup.  Entries that are negative, NaN or infinite have no mass.  The
+ * sums carry about 48 bits.  u_sample <= 0 or NaN counts as 0, >= 1 as the
+ * last token with mass; a NaN in u_accept rejects.  A draft outside
+ * [0, vocab) is rejected and raises DUSTIN_DEVFLAG_INDEX_RANGE.
+ *
+ *   p_target   [b][w][vocab] of `dtype` (DUSTIN_DTYPE_*), device; row (i, t)
+ *              at element i*stride_tb + t*stride_tw, entries contiguous
+ *   p_draft    [b][w-1][vocab] of the same type, row strides stride_db,
+ *              stride_dw; may be NULL
+ *   draft      int32 [b][w-1];  n_draft int32 [b] or NULL
+ *   u_accept   fp32 [b][w-1];   u_sample fp32 [b]
+ *   tokens     int32 [b][w]: the a accepted drafts, the drawn token (-1 if
+ *              the target's row has no mass at all), then -1
+ *   n_accepted int32 [b]: a
+ * draft and u_accept may be NULL when w == 1.  Rows may start at any
+ * element; rows that start on 16-byte boundaries are read fastest.
+ * b == 0 is a no-op.  Limits: vocab >= 1, b <= 2^27.  No workspace. */
+int dustin_verify_tokens(int b, int w, int vocab, int dtype, const void* p_target,
+                         int64_t stride_tb, int64_t stride_tw, const void* p_draft,
+                         int64_t stride_db, int64_t stride_dw, const int32_t* draft,
+                         const int32_t* n_draft, const float* u_accept,
+                         const float* u_sample, int32_t* tokens, int32_t* n_accepted,
+                         void* stream);
+
+/* ------------------------------------------------------------------------
+ * Compaction of a KV cache to an index set (for example the one of
+ * dustin_hybrid_topk, or the accepted path of a token tree): for every
+ * layer l, kv head and i < k_len[b],
+ *   row i of sequence b in dst[l] = row idx[b][i] of sequence b in src[l],
+ * K and V.  Rows from k_len[b] on are left as they were.
+ *
+ *   src, dst  host arrays [n_layers]; contiguous or paged, each on its own
+ *             (all layers of a side alike); src holds n positions, dst at
+ *             least k
+ *   idx       int32 [b][k], device; entries outside [0, n) raise
+ *             DUSTIN_DEVFLAG_INDEX_RANGE and leave their row as it was, and
+ *             so do pages outside the pool (DUSTIN_DEVFLAG_PAGE_RANGE)
+ *   k_len     int32 [b], device, or NULL (k each); clamped to [0, k]
+ * In place (dst[l] and src[l] have the same base and page table) the
+ * entries of a row ascend strictly; rows that stay where they are are not
+ * written (so a shared prefix that is kept whole may lie on shared pages).
+ * Otherwise (DUSTIN_DEVFLAG_INDEX_ORDER) that sequence's rows are
+ * unspecified.  Out of place, src and dst rows must not overlap, and an
+ * index may repeat.  Limits: d in {64, 128}; k <= n in place. */
+int dustin_kv_compact(int n_layers, int b, int h_kv, int d, int n, int k,
+                      const dustin_kv* src, const dustin_kv* dst, const int32_t* idx,
+                      const int32_t* k_len, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Pages shared between sequences.  The state is three device arrays of the
+ * caller: page_table int32 [n_seqs][pages_per_seq], seq_len int32 [n_seqs]
+ * (positions held), and refcount int32 [num_pages], the number of table
+ * entries that name a page (0: free).  Entries at or beyond
+ * ceil(seq_len / page_size) are not part of a sequence.
+ *
+ * dustin_kv_fork: sequence child[f] becomes a copy of sequence parent[f] by
+ * sharing all its pages (the last, partly full one too: see dustin_kv_resize).  A fork
+ * whose child is not empty (seq_len 0), is named earlier in the call, or is
+ * its own parent, whose parent is a child of the call, or with an id outside
+ * [0, n_seqs), is left out and raises DUSTIN_DEVFLAG_INDEX_RANGE.
+ *
+ * dustin_kv_resize: sequence seqs[i] gets the length new_len[i] (NULL: 0 for
+ * all, the sequences are freed).
+ *   - First, every sequence that shrinks gives up its pages behind the new
+ *     end: refcount - 1 each, entries set to -1.
+ *   - Then sequences that grow get pages, in list order, the free pages of
+ *     the lowest numbers first.  A partly full last page that other entries
+ *     name too is replaced by a copy of its own: copies[i] = {old page, new
+ *     page} (otherwise {-1, -1}), refcount of the old page - 1; that page
+ *     comes first, then the pages of the new positions.  (If all sharers of
+ *     a page grow in one call, each gets a copy and the page becomes free.)
+ *   - A sequence for which the free pages do not suffice, and those behind
+ *     it in the list that need pages, are left as they were and raise
+ *     DUSTIN_DEVFLAG_NO_PAGES.
+ *   - The copied pages' rows follow for the n_layers caches in kv (all
+ *     paged, with this page size and pool; page_table of the descriptors is
+ *     not read).  With n_layers == 0 the caller copies.
+ * An entry named before, an id or a length out of range (0 ..
+ * pages_per_seq * page_size) leaves that entry out and raises
+ * DUSTIN_DEVFLAG_INDEX_RANGE; a page id outside the pool is skipped and
+ * raises DUSTIN_DEVFLAG_PAGE_RANGE.
+ *   copies  int32 [n_list][2], device, fully overwritten
+ * Limits: n_list <= 1024, num_pages <= 2^22, pages_per_seq * page_size and
+ * n_seqs * pages_per_seq < 2^31; page_size as in dustin_kv.  Calls on one
+ * state are ordered by the stream; none may overlap another. */
+int dustin_kv_fork(int n_seqs, int pages_per_seq, int page_size, int num_pages,
+                   int n_forks, const int32_t* parent, const int32_t* child,
+                   int32_t* page_table, int32_t* seq_len, int32_t* refcount,
+                   void* stream);
+int dustin_kv_resize(int n_seqs, int pages_per_seq, int page_size, int num_pages,
+                     int n_list, const int32_t* seqs, const int32_t* new_len,
+                     int32_t* page_table, int32_t* seq_len, int32_t* refcount,
+                     int32_t* copies, int n_layers, int h_kv, int d,
+                     const dustin_kv* kv, void* stream);
 
 #ifdef __cplusplus
 }

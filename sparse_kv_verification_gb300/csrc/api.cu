@@ -459,7 +459,7 @@ const char* dustin_status_string(int status) {
 
 const char* dustin_last_error(void) { return g_err; }
 
-int dustin_version(void) { return 100; }
+int dustin_version(void) { return 200; }
 
 uint64_t dustin_launch_count(void) { return g_launches.load(); }
 
@@ -515,6 +515,8 @@ int dustin_device_status(uint32_t* flags) {
       (e = take_attn_dense_flags(&f)) != cudaSuccess ||
       (e = take_attn_ml_flags(&f)) != cudaSuccess ||
       (e = take_quest_flags(&f)) != cudaSuccess ||
+      (e = take_tokens_flags(&f)) != cudaSuccess ||
+      (e = take_pages_flags(&f)) != cudaSuccess ||
       (e = take_score_flags(&f)) != cudaSuccess)
     return cuda_fail(e, "dustin_device_status");
   if (flags) *flags = f;
@@ -806,6 +808,202 @@ int dustin_full_verify_attn_window(int b, int h_q, int h_kv, int d, int w, int n
   if (!win) return fail(DUSTIN_ERR_INVALID_ARG, "dustin_full_verify_attn_window: win is NULL");
   return run_attn(true, b, h_q, h_kv, d, w, n, n, q, kv, nullptr, win, scale, o, lse,
                   ws, ws_bytes, flags, stream);
+}
+
+int dustin_verify_tokens(int b, int w, int vocab, int dtype, const void* p_target,
+                         int64_t stride_tb, int64_t stride_tw, const void* p_draft,
+                         int64_t stride_db, int64_t stride_dw, const int32_t* draft,
+                         const int32_t* n_draft, const float* u_accept,
+                         const float* u_sample, int32_t* tokens, int32_t* n_accepted,
+                         void* stream) {
+  const char* what = "dustin_verify_tokens";
+  if (b < 0 || w < 1 || vocab < 1 || b > (1 << 27))
+    return fail(DUSTIN_ERR_SHAPE, "%s: b=%d w=%d vocab=%d", what, b, w, vocab);
+  if (dtype != DUSTIN_DTYPE_F32 && dtype != DUSTIN_DTYPE_BF16)
+    return fail(DUSTIN_ERR_INVALID_ARG, "%s: dtype=%d", what, dtype);
+  if (b == 0) return DUSTIN_OK;
+  if (!p_target || !u_sample || !tokens || !n_accepted || (w > 1 && (!draft || !u_accept)))
+    return fail(DUSTIN_ERR_INVALID_ARG,
+                "%s: p_target, u_sample, tokens, n_accepted and, with drafts, draft and "
+                "u_accept are required", what);
+  if (stride_tb < 0 || stride_tw < 0 || (p_draft && (stride_db < 0 || stride_dw < 0)))
+    return fail(DUSTIN_ERR_SHAPE, "%s: negative stride", what);
+  const uintptr_t at = dtype == DUSTIN_DTYPE_F32 ? 3u : 1u;
+  if (((reinterpret_cast<uintptr_t>(p_target) | reinterpret_cast<uintptr_t>(p_draft)) & at) ||
+      ((reinterpret_cast<uintptr_t>(draft) | reinterpret_cast<uintptr_t>(n_draft) |
+        reinterpret_cast<uintptr_t>(u_accept) | reinterpret_cast<uintptr_t>(u_sample) |
+        reinterpret_cast<uintptr_t>(tokens) | reinterpret_cast<uintptr_t>(n_accepted)) & 3u))
+    return fail(DUSTIN_ERR_ALIGNMENT, "%s: an array is not aligned to its elements", what);
+  TokenArgs a;
+  a.p = p_target;
+  a.q = w > 1 ? p_draft : nullptr;
+  a.stride_tb = stride_tb;
+  a.stride_tw = stride_tw;
+  a.stride_db = stride_db;
+  a.stride_dw = stride_dw;
+  a.draft = draft;
+  a.n_draft = n_draft;
+  a.u_accept = u_accept;
+  a.u_sample = u_sample;
+  a.tokens = tokens;
+  a.n_accepted = n_accepted;
+  a.b = b;
+  a.w = w;
+  a.vocab = vocab;
+  cudaError_t e = launch_tokens(a, dtype == DUSTIN_DTYPE_BF16, sm_count(), (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  return DUSTIN_OK;
+}
+
+int dustin_kv_compact(int n_layers, int b, int h_kv, int d, int n, int k,
+                      const dustin_kv* src, const dustin_kv* dst, const int32_t* idx,
+                      const int32_t* k_len, void* stream) {
+  const char* what = "dustin_kv_compact";
+  if (n_layers < 0 || b < 0 || h_kv < 1 || n < 0 || k < 0)
+    return fail(DUSTIN_ERR_SHAPE, "%s: n_layers=%d b=%d h_kv=%d n=%d k=%d", what, n_layers, b,
+                h_kv, n, k);
+  if (d != 64 && d != 128)
+    return fail(DUSTIN_ERR_UNSUPPORTED, "%s: d=%d (64 or 128)", what, d);
+  if (n_layers == 0 || b == 0 || k == 0) return DUSTIN_OK;
+  if (!src || !dst || !idx)
+    return fail(DUSTIN_ERR_INVALID_ARG, "%s: src, dst and idx are required", what);
+  if ((reinterpret_cast<uintptr_t>(idx) | reinterpret_cast<uintptr_t>(k_len)) & 3u)
+    return fail(DUSTIN_ERR_ALIGNMENT, "%s: idx and k_len need 4-byte alignment", what);
+  // Units of one launch, times the ranges a unit may be cut into.
+  if ((long long)b * h_kv * std::min(n_layers, kCompactMaxLayers) > (1LL << 24))
+    return fail(DUSTIN_ERR_SHAPE, "%s: problem too large", what);
+  const bool in_place = src[0].k == dst[0].k && src[0].page_table == dst[0].page_table;
+  if (in_place && k > n)
+    return fail(DUSTIN_ERR_SHAPE, "%s: k=%d > n=%d in place", what, k, n);
+  for (int l = 0; l < n_layers; ++l) {
+    int rc = check_kv(&src[l], b, n, d, true, what);
+    if (rc || (rc = check_kv(&dst[l], b, k, d, true, what))) return rc;
+    if ((src[l].page_table != nullptr) != (src[0].page_table != nullptr) ||
+        (dst[l].page_table != nullptr) != (dst[0].page_table != nullptr))
+      return fail(DUSTIN_ERR_INVALID_ARG, "%s: layers mix paged and contiguous caches", what);
+    const bool same_table = src[l].page_table == dst[l].page_table;
+    if ((src[l].k == dst[l].k && same_table) != in_place ||
+        (src[l].v == dst[l].v && same_table) != in_place)
+      return fail(DUSTIN_ERR_INVALID_ARG, "%s: layer %d: all of K and V in place, or none", what, l);
+    if (in_place && (src[l].stride_b != dst[l].stride_b || src[l].stride_h != dst[l].stride_h ||
+                     src[l].stride_n != dst[l].stride_n || src[l].page_size != dst[l].page_size ||
+                     src[l].num_pages != dst[l].num_pages))
+      return fail(DUSTIN_ERR_INVALID_ARG, "%s: layer %d: one cache in two layouts", what, l);
+  }
+  CompactArgs a;
+  a.idx = idx;
+  a.k_len = k_len;
+  a.b = b;
+  a.hkv = h_kv;
+  a.n = n;
+  a.k = k;
+  a.in_place = in_place ? 1 : 0;
+  a.splits = 1;
+  for (int l0 = 0; l0 < n_layers; l0 += kCompactMaxLayers) {
+    a.layers = std::min(kCompactMaxLayers, n_layers - l0);
+    for (int l = 0; l < a.layers; ++l) {
+      a.layer[l].src = to_view(src[l0 + l]);
+      a.layer[l].dst = to_view(dst[l0 + l]);
+    }
+    cudaError_t e = launch_compact(a, d, sm_count(), (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, what);
+  }
+  return DUSTIN_OK;
+}
+
+static int check_pages(int n_seqs, int pages_per_seq, int page_size, int num_pages,
+                       const void* page_table, const void* seq_len, const void* refcount,
+                       const char* what) {
+  if (n_seqs < 1 || pages_per_seq < 1 || num_pages < 1)
+    return fail(DUSTIN_ERR_SHAPE, "%s: n_seqs=%d pages_per_seq=%d num_pages=%d", what, n_seqs,
+                pages_per_seq, num_pages);
+  if (page_size < 16 || page_size % 16)
+    return fail(DUSTIN_ERR_UNSUPPORTED, "%s: page_size %d (must be a positive multiple of 16)",
+                what, page_size);
+  if ((long long)pages_per_seq * page_size > 0x7fffffffLL ||
+      (long long)n_seqs * pages_per_seq > 0x7fffffffLL)
+    return fail(DUSTIN_ERR_SHAPE, "%s: problem too large", what);
+  if (num_pages > kResizeMaxPages)
+    return fail(DUSTIN_ERR_UNSUPPORTED, "%s: num_pages=%d > %d", what, num_pages,
+                kResizeMaxPages);
+  if (!page_table || !seq_len || !refcount)
+    return fail(DUSTIN_ERR_INVALID_ARG, "%s: page_table, seq_len and refcount are required", what);
+  if ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(seq_len) |
+       reinterpret_cast<uintptr_t>(refcount)) & 3u)
+    return fail(DUSTIN_ERR_ALIGNMENT, "%s: an array is not 4-byte aligned", what);
+  return DUSTIN_OK;
+}
+
+int dustin_kv_fork(int n_seqs, int pages_per_seq, int page_size, int num_pages,
+                   int n_forks, const int32_t* parent, const int32_t* child,
+                   int32_t* page_table, int32_t* seq_len, int32_t* refcount,
+                   void* stream) {
+  const char* what = "dustin_kv_fork";
+  if (n_forks < 0) return fail(DUSTIN_ERR_SHAPE, "%s: n_forks=%d", what, n_forks);
+  if (n_forks == 0) return DUSTIN_OK;
+  int rc = check_pages(n_seqs, pages_per_seq, page_size, num_pages, page_table, seq_len,
+                       refcount, what);
+  if (rc) return rc;
+  if (!parent || !child)
+    return fail(DUSTIN_ERR_INVALID_ARG, "%s: parent and child are required", what);
+  if ((reinterpret_cast<uintptr_t>(parent) | reinterpret_cast<uintptr_t>(child)) & 3u)
+    return fail(DUSTIN_ERR_ALIGNMENT, "%s: an array is not 4-byte aligned", what);
+  ForkArgs a{parent, child, page_table, seq_len, refcount, n_seqs, pages_per_seq, page_size,
+             num_pages, n_forks};
+  cudaError_t e = launch_fork(a, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  return DUSTIN_OK;
+}
+
+int dustin_kv_resize(int n_seqs, int pages_per_seq, int page_size, int num_pages,
+                     int n_list, const int32_t* seqs, const int32_t* new_len,
+                     int32_t* page_table, int32_t* seq_len, int32_t* refcount,
+                     int32_t* copies, int n_layers, int h_kv, int d,
+                     const dustin_kv* kv, void* stream) {
+  const char* what = "dustin_kv_resize";
+  if (n_list < 0 || n_layers < 0)
+    return fail(DUSTIN_ERR_SHAPE, "%s: n_list=%d n_layers=%d", what, n_list, n_layers);
+  if (n_list > kResizeMaxList)
+    return fail(DUSTIN_ERR_UNSUPPORTED, "%s: n_list=%d > %d", what, n_list, kResizeMaxList);
+  if (n_list == 0) return DUSTIN_OK;
+  int rc = check_pages(n_seqs, pages_per_seq, page_size, num_pages, page_table, seq_len,
+                       refcount, what);
+  if (rc) return rc;
+  if (!seqs || !copies)
+    return fail(DUSTIN_ERR_INVALID_ARG, "%s: seqs and copies are required", what);
+  if ((reinterpret_cast<uintptr_t>(seqs) | reinterpret_cast<uintptr_t>(new_len) |
+       reinterpret_cast<uintptr_t>(copies)) & 3u)
+    return fail(DUSTIN_ERR_ALIGNMENT, "%s: an array is not 4-byte aligned", what);
+  if (n_layers > 0) {
+    if (h_kv < 1) return fail(DUSTIN_ERR_SHAPE, "%s: h_kv=%d", what, h_kv);
+    if (d != 64 && d != 128)
+      return fail(DUSTIN_ERR_UNSUPPORTED, "%s: d=%d (64 or 128)", what, d);
+    if ((long long)h_kv * page_size > 0x7fffffffLL - 65536)
+      return fail(DUSTIN_ERR_SHAPE, "%s: problem too large", what);
+    if (!kv) return fail(DUSTIN_ERR_INVALID_ARG, "%s: kv is NULL", what);
+    for (int l = 0; l < n_layers; ++l) {
+      if ((rc = check_kv(&kv[l], 1, 0, d, true, what))) return rc;
+      if (!kv[l].page_table || kv[l].page_size != page_size || kv[l].num_pages != num_pages)
+        return fail(DUSTIN_ERR_INVALID_ARG,
+                    "%s: layer %d: not a paged cache of %d pages of %d positions", what, l,
+                    num_pages, page_size);
+    }
+  }
+  ResizeArgs a{seqs, new_len, page_table, seq_len, refcount, copies, n_seqs, pages_per_seq,
+               page_size, num_pages, n_list};
+  cudaError_t e = launch_resize(a, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  CopyArgs c;
+  c.copies = copies;
+  c.hkv = h_kv;
+  // A call that frees only (new_len NULL) copies nothing.
+  for (int l0 = 0; new_len && l0 < n_layers; l0 += kCompactMaxLayers) {
+    c.layers = std::min(kCompactMaxLayers, n_layers - l0);
+    for (int l = 0; l < c.layers; ++l) c.kv[l] = to_view(kv[l0 + l]);
+    if ((e = launch_copy_pages(c, n_list, d, (cudaStream_t)stream)) != cudaSuccess)
+      return cuda_fail(e, what);
+  }
+  return DUSTIN_OK;
 }
 
 }  // extern "C"

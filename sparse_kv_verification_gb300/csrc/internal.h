@@ -80,6 +80,60 @@ int occupancy_attn_dense(int d, int mt);
 cudaError_t take_attn_sparse_flags(unsigned* flags);
 cudaError_t take_attn_dense_flags(unsigned* flags);
 
+// ---- verification of drafted tokens
+struct TokenArgs {
+  const void* p;                 // target rows, fp32 or bf16
+  const void* q;                 // draft rows of the same type (may be null)
+  long long stride_tb, stride_tw, stride_db, stride_dw;
+  const int* draft;              // [b][w - 1]
+  const int* n_draft;            // [b] or null
+  const float* u_accept;         // [b][w - 1]
+  const float* u_sample;         // [b]
+  int* tokens;                   // [b][w]
+  int* n_accepted;               // [b]
+  int b, w, vocab;
+};
+cudaError_t launch_tokens(const TokenArgs& a, bool bf16, int sms, cudaStream_t st);
+cudaError_t take_tokens_flags(unsigned* flags);
+
+// ---- cache compaction and shared pages
+constexpr int kCompactMaxLayers = 128;   // per launch (kernel parameter space)
+struct CompactArgs {
+  const int* idx;      // [b][k]
+  const int* k_len;    // [b] or null
+  int layers, b, hkv, n, k, in_place, splits;
+  struct { KvView src, dst; } layer[kCompactMaxLayers];
+};
+struct ForkArgs {
+  const int* parent;   // [n_forks]
+  const int* child;
+  int* page_table;     // [n_seqs][pages_per_seq]
+  int* seq_len;        // [n_seqs]
+  int* refcount;       // [num_pages]
+  int n_seqs, pages_per_seq, page_size, num_pages, n_forks;
+};
+constexpr int kResizeMaxList = 1024;
+constexpr int kResizeMaxPages = 1 << 22;
+struct ResizeArgs {
+  const int* seqs;     // [n_list]
+  const int* new_len;  // [n_list] or null (zeros)
+  int* page_table;
+  int* seq_len;
+  int* refcount;
+  int* copies;         // [n_list][2]
+  int n_seqs, pages_per_seq, page_size, num_pages, n_list;
+};
+struct CopyArgs {
+  const int* copies;
+  int layers, hkv;
+  KvView kv[kCompactMaxLayers];
+};
+cudaError_t launch_compact(const CompactArgs& a, int d, int sms, cudaStream_t st);
+cudaError_t launch_fork(const ForkArgs& a, cudaStream_t st);
+cudaError_t launch_resize(const ResizeArgs& a, cudaStream_t st);
+cudaError_t launch_copy_pages(const CopyArgs& a, int n_list, int d, cudaStream_t st);
+cudaError_t take_pages_flags(unsigned* flags);
+
 // ---- bookkeeping (api.cu)
 void note_launches(int count);
 int record_error(int status, const char* message);  // sets dustin_last_error()

@@ -18,6 +18,8 @@ from . import build as _build
 DUSTIN_OK = 0
 DUSTIN_NORM_NONE = 0
 DUSTIN_NORM_L1 = 1
+DUSTIN_DTYPE_F32 = 0
+DUSTIN_DTYPE_BF16 = 1
 DUSTIN_ATTN_KV_READY = 1
 
 EXPORTS = (
@@ -33,6 +35,8 @@ EXPORTS = (
     "dustin_sparse_verify_attn_layers",
     "dustin_quest_stats_size", "dustin_quest_page_stats",
     "dustin_quest_page_scores",
+    "dustin_verify_tokens", "dustin_kv_compact", "dustin_kv_fork",
+    "dustin_kv_resize",
 )
 
 
@@ -81,6 +85,7 @@ def load(build_if_missing: bool = False, path: Optional[str] = None
     lib = ctypes.CDLL(path)
     P, I, F, D, S, U = (ctypes.c_void_p, ctypes.c_int, ctypes.c_float,
                         ctypes.c_double, ctypes.c_size_t, ctypes.c_uint)
+    L = ctypes.c_int64
     sig = {
         "dustin_status_string": (ctypes.c_char_p, [I]),
         "dustin_last_error": (ctypes.c_char_p, []),
@@ -108,6 +113,11 @@ def load(build_if_missing: bool = False, path: Optional[str] = None
         "dustin_quest_stats_size": (S, [I, I, I, I, I]),
         "dustin_quest_page_stats": (I, [I, I, I, I, I, P, P, P]),
         "dustin_quest_page_scores": (I, [I, I, I, I, I, I, P, P, P, P]),
+        "dustin_verify_tokens": (I, [I, I, I, I, P, L, L, P, L, L, P, P, P, P, P,
+                                     P, P]),
+        "dustin_kv_compact": (I, [I, I, I, I, I, I, P, P, P, P, P]),
+        "dustin_kv_fork": (I, [I, I, I, I, I, P, P, P, P, P, P]),
+        "dustin_kv_resize": (I, [I, I, I, I, I, P, P, P, P, P, P, I, I, I, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -540,3 +550,138 @@ def prepare_full_verify_attn(q, kv, h_kv, n, scale, o, lse, ws, stream=None,
         _check(fn(*args))
     call.keep = kvc
     return call
+
+
+# ------------------------------------------- verification of drafted tokens
+
+def _one_device(*ts):
+    """Device tensors (None allowed) of one device."""
+    _need_cuda(*ts)
+    if len({t.device for t in ts if t is not None}) > 1:
+        raise ValueError("tensors must live on one device")
+
+
+def _int32(what, t, *shape):
+    if t.dtype != torch.int32 or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise ValueError(f"{what} must be contiguous int32 {list(shape)}")
+
+
+def dustin_verify_tokens(p_target: torch.Tensor, p_draft: Optional[torch.Tensor],
+                         draft: Optional[torch.Tensor],
+                         u_accept: Optional[torch.Tensor], u_sample: torch.Tensor,
+                         tokens: torch.Tensor, n_accepted: torch.Tensor,
+                         n_draft: Optional[torch.Tensor] = None,
+                         stream=None) -> None:
+    """p_target fp32 or bf16 [b][w][vocab]; p_draft of the same type
+    [b][w-1][vocab], or None (drafts taken as certain); draft int32 and
+    u_accept fp32 [b][w-1] (None if w is 1); u_sample fp32 [b].  tokens int32
+    [b][w] receives the accepted drafts, the drawn token and -1 behind it,
+    n_accepted int32 [b] the number of accepted drafts."""
+    _one_device(p_target, p_draft, draft, u_accept, u_sample, tokens, n_accepted,
+               n_draft)
+    if p_target.dim() != 3 or p_target.stride(2) != 1 and p_target.shape[2] > 1:
+        raise ValueError("p_target must be [b][w][vocab] with contiguous rows")
+    b, w, vocab = p_target.shape
+    if p_target.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("probabilities are fp32 or bf16")
+    if p_draft is not None and (
+            p_draft.dtype != p_target.dtype or tuple(p_draft.shape) != (b, w - 1, vocab)
+            or p_draft.stride(2) != 1 and vocab > 1):
+        raise ValueError("p_draft must be [b][w-1][vocab] of p_target's type with "
+                         "contiguous rows")
+    if w > 1:
+        if draft is None or u_accept is None:
+            raise ValueError("draft and u_accept are required")
+        _int32("draft", draft, b, w - 1)
+        if u_accept.dtype != torch.float32 or not u_accept.is_contiguous() or \
+                tuple(u_accept.shape) != (b, w - 1):
+            raise ValueError("u_accept must be contiguous fp32 [b][w-1]")
+    if u_sample.dtype != torch.float32 or not u_sample.is_contiguous() or \
+            tuple(u_sample.shape) != (b,):
+        raise ValueError("u_sample must be contiguous fp32 [b]")
+    _int32("tokens", tokens, b, w)
+    _int32("n_accepted", n_accepted, b)
+    if n_draft is not None:
+        _int32("n_draft", n_draft, b)
+    with torch.cuda.device(p_target.device):
+        _check(load().dustin_verify_tokens(
+            b, w, vocab,
+            DUSTIN_DTYPE_F32 if p_target.dtype == torch.float32 else DUSTIN_DTYPE_BF16,
+            p_target.data_ptr(), p_target.stride(0), p_target.stride(1), _ptr(p_draft),
+            0 if p_draft is None else p_draft.stride(0),
+            0 if p_draft is None else p_draft.stride(1), _ptr(draft), _ptr(n_draft),
+            _ptr(u_accept), u_sample.data_ptr(), tokens.data_ptr(),
+            n_accepted.data_ptr(), _stream(stream, p_target.device)))
+
+
+# ------------------------------------------------- compaction, shared pages
+
+def dustin_kv_compact(src: Sequence[DustinKV], dst: Sequence[DustinKV], h_kv: int,
+                      d: int, n: int, idx: torch.Tensor,
+                      k_len: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Row i of each sequence and layer of dst becomes row idx[b][i] of src
+    (idx int32 [b][k], i < k_len[b]); in place where dst is src."""
+    _one_device(idx, k_len)
+    if len(src) != len(dst):
+        raise ValueError("one src and one dst cache per layer")
+    if idx.dtype != torch.int32 or not idx.is_contiguous() or idx.dim() != 2:
+        raise ValueError("idx must be contiguous int32 [b][k]")
+    b, k = idx.shape
+    if k_len is not None:
+        _int32("k_len", k_len, b)
+    sa, da = (DustinKV * len(src))(*src), (DustinKV * len(dst))(*dst)
+    with torch.cuda.device(idx.device):
+        _check(load().dustin_kv_compact(
+            len(src), b, h_kv, d, n, k, ctypes.addressof(sa), ctypes.addressof(da),
+            idx.data_ptr(), _ptr(k_len), _stream(stream, idx.device)))
+
+
+def _page_state(page_table, seq_len, refcount):
+    _one_device(page_table, seq_len, refcount)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be int32 [n_seqs][pages_per_seq]")
+    _int32("page_table", page_table, *page_table.shape)
+    _int32("seq_len", seq_len, page_table.shape[0])
+    _int32("refcount", refcount, refcount.numel())
+    return (page_table.shape[0], page_table.shape[1], refcount.numel())
+
+
+def dustin_kv_fork(page_table: torch.Tensor, seq_len: torch.Tensor,
+                   refcount: torch.Tensor, page_size: int, parent: torch.Tensor,
+                   child: torch.Tensor, stream=None) -> None:
+    """Sequence child[f] (empty) shares all pages of sequence parent[f]."""
+    n_seqs, ppseq, pages = _page_state(page_table, seq_len, refcount)
+    _one_device(page_table, parent, child)
+    _int32("parent", parent, parent.numel())
+    _int32("child", child, parent.numel())
+    with torch.cuda.device(page_table.device):
+        _check(load().dustin_kv_fork(
+            n_seqs, ppseq, page_size, pages, parent.numel(), parent.data_ptr(),
+            child.data_ptr(), page_table.data_ptr(), seq_len.data_ptr(),
+            refcount.data_ptr(), _stream(stream, page_table.device)))
+
+
+def dustin_kv_resize(page_table: torch.Tensor, seq_len: torch.Tensor,
+                     refcount: torch.Tensor, page_size: int, seqs: torch.Tensor,
+                     new_len: Optional[torch.Tensor], copies: torch.Tensor,
+                     kvs: Sequence[DustinKV] = (), h_kv: int = 0, d: int = 0,
+                     stream=None) -> None:
+    """Sequence seqs[i] gets the length new_len[i] (None: all 0): pages behind
+    the new end are released, pages for a longer one taken, a shared partly
+    full last page copied first (in the caches kvs; copies int32 [n][2]
+    receives {old page, new page} or {-1, -1})."""
+    n_seqs, ppseq, pages = _page_state(page_table, seq_len, refcount)
+    _one_device(page_table, seqs, new_len, copies)
+    n = seqs.numel()
+    _int32("seqs", seqs, n)
+    if new_len is not None:
+        _int32("new_len", new_len, n)
+    _int32("copies", copies, n, 2)
+    arr = (DustinKV * len(kvs))(*kvs) if kvs else None
+    with torch.cuda.device(page_table.device):
+        _check(load().dustin_kv_resize(
+            n_seqs, ppseq, page_size, pages, n, seqs.data_ptr(), _ptr(new_len),
+            page_table.data_ptr(), seq_len.data_ptr(), refcount.data_ptr(),
+            copies.data_ptr(), len(kvs), h_kv, d,
+            ctypes.addressof(arr) if kvs else None,
+            _stream(stream, page_table.device)))
