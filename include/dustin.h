@@ -348,6 +348,48 @@ int dustin_full_verify_attn_window(int b, int h_q, int h_kv, int d, int w, int n
                                    unsigned flags, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Verification attention of a batch whose sequences share prefixes (samples
+ * of one prompt, requests under one system prompt).  Not an API of the
+ * paper.  The b sequences form `groups` groups of b / groups consecutive
+ * ones; group g's sequences share the P_g positions of row g of `prefix`,
+ * and sequence i goes on with the L_i positions of row i of `own` and, with
+ * win, the w window positions (causal, as in the *_window calls):
+ *   o[i][h][t] = softmax over [prefix g 0..P_g), own 0..L_i), window 0..t]
+ *                of scale * q . K, times V;   lse = log sum exp (natural)
+ * for g = i / (b / groups).  The prefix is read once per kv head and row
+ * tile of 256 query rows, not once per sequence.  A row that sees no
+ * position gives o = 0, lse = -inf.
+ *
+ *   q           bf16 [b][h_q][w][d], device (contiguous); o like q; lse fp32
+ *               [b][h_q][w]
+ *   prefix      one row (contiguous cache or page-table row) per group;
+ *               ignored (may be NULL) if n_prefix is 0
+ *   prefix_len  int32 [groups], device, or NULL (n_prefix each); own_len
+ *               int32 [b] or NULL (n_own each); clamped to [0, n_prefix],
+ *               [0, n_own]
+ *   own         one row per sequence; ignored if n_own is 0.  Where a fork
+ *               shares whole pages, a sequence's own positions are the rest
+ *               of its page-table row: page_table + shared pages, with the
+ *               full row's pages_per_seq
+ *   win         [b][h_kv][w][d], contiguous, or NULL
+ * Positions behind the lengths are never used, whatever they hold; window
+ * rows, however, are weighted with exact zeros above the diagonal, so V of
+ * the window is finite.  Pages outside the pool are left out
+ * (DUSTIN_DEVFLAG_PAGE_RANGE).  DUSTIN_ATTN_KV_READY is accepted, without
+ * effect.  Sums are taken in a fixed order: equal calls give equal bits.
+ * Limits: as dustin_sparse_verify_attn; kv strides below 2^39 elements.
+ * Workspace: dustin_prefix_verify_attn_workspace_size (with or without win).
+ */
+size_t dustin_prefix_verify_attn_workspace_size(int b, int groups, int h_q, int h_kv,
+                                                int d, int w, int n_prefix, int n_own);
+int dustin_prefix_verify_attn(int b, int groups, int h_q, int h_kv, int d, int w,
+                              int n_prefix, int n_own, const void* q,
+                              const dustin_kv* prefix, const int32_t* prefix_len,
+                              const dustin_kv* own, const int32_t* own_len,
+                              const dustin_kv* win, float scale, void* o, float* lse,
+                              void* ws, size_t ws_bytes, unsigned flags, void* stream);
+
+/* ------------------------------------------------------------------------
  * Verification of drafted tokens (speculative sampling), the step that
  * follows the target's pass over its w verification rows.  Not an API of the
  * paper.

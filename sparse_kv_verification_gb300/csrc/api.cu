@@ -515,6 +515,7 @@ int dustin_device_status(uint32_t* flags) {
       (e = take_attn_dense_flags(&f)) != cudaSuccess ||
       (e = take_attn_ml_flags(&f)) != cudaSuccess ||
       (e = take_quest_flags(&f)) != cudaSuccess ||
+      (e = take_prefix_flags(&f)) != cudaSuccess ||
       (e = take_tokens_flags(&f)) != cudaSuccess ||
       (e = take_pages_flags(&f)) != cudaSuccess ||
       (e = take_score_flags(&f)) != cudaSuccess)
@@ -808,6 +809,93 @@ int dustin_full_verify_attn_window(int b, int h_q, int h_kv, int d, int w, int n
   if (!win) return fail(DUSTIN_ERR_INVALID_ARG, "dustin_full_verify_attn_window: win is NULL");
   return run_attn(true, b, h_q, h_kv, d, w, n, n, q, kv, nullptr, win, scale, o, lse,
                   ws, ws_bytes, flags, stream);
+}
+
+static int check_prefix_shape(int b, int groups, int h_q, int h_kv, int d, int w, int n_prefix,
+                              int n_own, const char* what) {
+  if (groups < 1 || b % groups)
+    return fail(DUSTIN_ERR_SHAPE, "%s: b=%d is not a multiple of groups=%d", what, b, groups);
+  if (n_prefix < 0)
+    return fail(DUSTIN_ERR_SHAPE, "%s: n_prefix=%d", what, n_prefix);
+  int rc = check_attn_shape(b, h_q, h_kv, d, w, n_own, what);
+  if (rc) return rc;
+  // The line of (row tile, K/V tile) pairs is counted in 32 bits.
+  const double tiles = n_prefix / 128 + 1.0, own = n_own / 128 + w / 128 + 2.0;
+  const double rows = (double)(h_q / h_kv) * w;
+  if (h_kv * (groups * tiles * (rows * (b / groups) / 128 + 1) + b * own * (rows / 128 + 1)) >
+          (double)(1 << 30) ||
+      rows * b * h_kv > (double)(1 << 30))
+    return fail(DUSTIN_ERR_SHAPE, "%s: problem too large", what);
+  return DUSTIN_OK;
+}
+
+static PrefixArgs prefix_args(int b, int groups, int h_q, int h_kv, int d, int w, int n_prefix,
+                              int n_own) {
+  PrefixArgs p{};
+  p.b = b;
+  p.groups = groups;
+  p.hq = h_q;
+  p.hkv = h_kv;
+  p.d = d;
+  p.w = w;
+  p.n_prefix = n_prefix;
+  p.n_own = n_own;
+  return p;
+}
+
+size_t dustin_prefix_verify_attn_workspace_size(int b, int groups, int h_q, int h_kv, int d, int w,
+                                                int n_prefix, int n_own) {
+  if (b <= 0 || check_prefix_shape(b, groups, h_q, h_kv, d, w, n_prefix, n_own,
+                                   "dustin_prefix_verify_attn_workspace_size"))
+    return 0;
+  return prefix_workspace(prefix_args(b, groups, h_q, h_kv, d, w, n_prefix, n_own), sm_count());
+}
+
+int dustin_prefix_verify_attn(int b, int groups, int h_q, int h_kv, int d, int w, int n_prefix,
+                              int n_own, const void* q, const dustin_kv* prefix,
+                              const int32_t* prefix_len, const dustin_kv* own,
+                              const int32_t* own_len, const dustin_kv* win, float scale, void* o,
+                              float* lse, void* ws, size_t ws_bytes, unsigned flags,
+                              void* stream) {
+  const char* what = "dustin_prefix_verify_attn";
+  int rc = check_prefix_shape(b, groups, h_q, h_kv, d, w, n_prefix, n_own, what);
+  if (rc) return rc;
+  if (b == 0) return DUSTIN_OK;
+  if (!q || !o || !lse)
+    return fail(DUSTIN_ERR_INVALID_ARG, "%s: q, o and lse are required", what);
+  if (!aligned16(q) || !aligned16(o) ||
+      ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(prefix_len) |
+        reinterpret_cast<uintptr_t>(own_len)) & 3u))
+    return fail(DUSTIN_ERR_ALIGNMENT, "%s: q/o need 16-byte, lse and lengths 4-byte alignment",
+                what);
+  if (!std::isfinite(scale) || !(scale > 0.f))
+    return fail(DUSTIN_ERR_INVALID_ARG, "%s: scale must be finite and > 0", what);
+  if (flags & ~DUSTIN_ATTN_KV_READY)
+    return fail(DUSTIN_ERR_INVALID_ARG, "%s: unknown flags 0x%x", what, flags);
+  if (n_prefix > 0 && (rc = check_kv(prefix, groups, n_prefix, d, true, what))) return rc;
+  if (n_own > 0 && (rc = check_kv(own, b, n_own, d, true, what))) return rc;
+  if (win && (rc = check_win(win, d, what))) return rc;
+  PrefixArgs p = prefix_args(b, groups, h_q, h_kv, d, w, n_prefix, n_own);
+  const size_t need = prefix_workspace(p, sm_count());
+  if (!ws || ws_bytes < need || !aligned16(ws))
+    return fail(DUSTIN_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu (16-byte aligned)", what,
+                ws_bytes, need);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  if (n_prefix > 0) p.prefix = to_view(*prefix);
+  if (n_own > 0) p.own = to_view(*own);
+  if (win) p.win = to_view(*win);
+  p.has_win = win ? 1 : 0;
+  p.prefix_len = prefix_len;
+  p.own_len = own_len;
+  p.scale_log2 = scale * kLog2e;
+  cudaError_t e = launch_attn_prefix(p, sm_count(), ws, (cudaStream_t)stream);
+  if (e == cudaErrorNotSupported)
+    return fail(DUSTIN_ERR_UNSUPPORTED, "%s: a cache's strides or extent exceed a tensor map's",
+                what);
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  return DUSTIN_OK;
 }
 
 int dustin_verify_tokens(int b, int w, int vocab, int dtype, const void* p_target,

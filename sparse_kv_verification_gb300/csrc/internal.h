@@ -80,6 +80,21 @@ int occupancy_attn_dense(int d, int mt);
 cudaError_t take_attn_sparse_flags(unsigned* flags);
 cudaError_t take_attn_dense_flags(unsigned* flags);
 
+// ---- attention of a batch that shares prefixes
+struct PrefixArgs {
+  const __nv_bfloat16* q;   // [b][h_q][w][d]
+  __nv_bfloat16* o;
+  float* lse;
+  KvView prefix, own, win;
+  const int* prefix_len;    // [groups] or null
+  const int* own_len;       // [b] or null
+  int b, groups, hq, hkv, d, w, n_prefix, n_own, has_win;
+  float scale_log2;
+};
+size_t prefix_workspace(const PrefixArgs& p, int sms);
+cudaError_t launch_attn_prefix(const PrefixArgs& p, int sms, void* ws, cudaStream_t st);
+cudaError_t take_prefix_flags(unsigned* flags);
+
 // ---- verification of drafted tokens
 struct TokenArgs {
   const void* p;                 // target rows, fp32 or bf16

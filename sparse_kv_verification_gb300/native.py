@@ -35,6 +35,7 @@ EXPORTS = (
     "dustin_sparse_verify_attn_layers",
     "dustin_quest_stats_size", "dustin_quest_page_stats",
     "dustin_quest_page_scores",
+    "dustin_prefix_verify_attn_workspace_size", "dustin_prefix_verify_attn",
     "dustin_verify_tokens", "dustin_kv_compact", "dustin_kv_fork",
     "dustin_kv_resize",
 )
@@ -113,6 +114,9 @@ def load(build_if_missing: bool = False, path: Optional[str] = None
         "dustin_quest_stats_size": (S, [I, I, I, I, I]),
         "dustin_quest_page_stats": (I, [I, I, I, I, I, P, P, P]),
         "dustin_quest_page_scores": (I, [I, I, I, I, I, I, P, P, P, P]),
+        "dustin_prefix_verify_attn_workspace_size": (S, [I, I, I, I, I, I, I, I]),
+        "dustin_prefix_verify_attn": (I, [I, I, I, I, I, I, I, I, P, P, P, P, P, P, F,
+                                          P, P, P, S, U, P]),
         "dustin_verify_tokens": (I, [I, I, I, I, P, L, L, P, L, L, P, P, P, P, P,
                                      P, P]),
         "dustin_kv_compact": (I, [I, I, I, I, I, I, P, P, P, P, P]),
@@ -552,7 +556,7 @@ def prepare_full_verify_attn(q, kv, h_kv, n, scale, o, lse, ws, stream=None,
     return call
 
 
-# ------------------------------------------- verification of drafted tokens
+# ------------------------------------------------ attention, shared prefixes
 
 def _one_device(*ts):
     """Device tensors (None allowed) of one device."""
@@ -565,6 +569,42 @@ def _int32(what, t, *shape):
     if t.dtype != torch.int32 or not t.is_contiguous() or tuple(t.shape) != shape:
         raise ValueError(f"{what} must be contiguous int32 {list(shape)}")
 
+
+def dustin_prefix_verify_attn_workspace_size(b, groups, h_q, h_kv, d, w, n_prefix,
+                                             n_own) -> int:
+    return int(load().dustin_prefix_verify_attn_workspace_size(
+        b, groups, h_q, h_kv, d, w, n_prefix, n_own))
+
+
+def dustin_prefix_verify_attn(q: torch.Tensor, prefix: Optional[DustinKV],
+                              own: Optional[DustinKV], h_kv: int, groups: int,
+                              n_prefix: int, n_own: int, scale: float,
+                              o: torch.Tensor, lse: torch.Tensor,
+                              ws: Optional[torch.Tensor], win: Optional[DustinKV] = None,
+                              prefix_len: Optional[torch.Tensor] = None,
+                              own_len: Optional[torch.Tensor] = None, stream=None,
+                              flags: int = 0) -> None:
+    """Attention of sequences that share their group's prefix (row g of
+    `prefix`), each with own positions behind it (row i of `own`) and, with
+    win, the window's causal block.  prefix_len int32 [groups] and own_len
+    int32 [b] give lengths below n_prefix and n_own."""
+    _attn_checks(q, o, lse)
+    _one_device(q, o, lse, ws, prefix_len, own_len)
+    b, h_q, w, d = q.shape
+    if prefix_len is not None:
+        _int32("prefix_len", prefix_len, groups)
+    if own_len is not None:
+        _int32("own_len", own_len, b)
+    ref = lambda kv: None if kv is None else ctypes.byref(kv)
+    with torch.cuda.device(q.device):
+        _check(load().dustin_prefix_verify_attn(
+            b, groups, h_q, h_kv, d, w, n_prefix, n_own, q.data_ptr(), ref(prefix),
+            _ptr(prefix_len), ref(own), _ptr(own_len), ref(win), float(scale),
+            o.data_ptr(), lse.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),
+            int(flags), _stream(stream, q.device)))
+
+
+# ------------------------------------------- verification of drafted tokens
 
 def dustin_verify_tokens(p_target: torch.Tensor, p_draft: Optional[torch.Tensor],
                          draft: Optional[torch.Tensor],

@@ -87,3 +87,31 @@ def test_fork_and_resize_refusals(lib):
     assert resize(layers=1, kv=desc(True, num_pages=32)) == 1     # another pool
     assert resize(layers=1, kv=desc(True, num_pages=64, v=None)) == 1
     assert resize(m=0, table=None) == 0
+
+
+def test_prefix_attention_refusals(lib):
+    def call(b=4, groups=2, hq=8, hkv=2, d=128, w=4, n_p=256, n_o=64, q=FAKE, prefix=desc(),
+             own=desc(), plen=None, olen=None, win=None, scale=0.1, o=FAKE, lse=FAKE, ws=FAKE,
+             ws_bytes=1 << 40, flags=0):
+        ref = lambda kv: None if kv is None else ctypes.byref(kv)
+        return lib.dustin_prefix_verify_attn(b, groups, hq, hkv, d, w, n_p, n_o, q, ref(prefix), plen,
+                                             ref(own), olen, ref(win), scale, o, lse, ws, ws_bytes,
+                                             flags, None)
+    assert call(groups=3) == 2 and call(groups=0) == 2 and call(b=-2) == 2
+    assert call(n_p=-1) == 2 and call(n_o=-1) == 2 and call(w=0) == 2 and call(hq=7) == 2
+    assert call(d=96) == 3
+    assert call(n_p=1 << 30, hq=512, b=400) == 2                # 32-bit work line
+    assert call(q=None) == 1 and call(o=None) == 1 and call(lse=None) == 1
+    assert call(q=FAKE + 8) == 5 and call(plen=FAKE + 2) == 5 and call(olen=FAKE + 1) == 5
+    assert call(scale=0.0) == 1 and call(scale=float("inf")) == 1 and call(flags=2) == 1
+    assert call(prefix=None) == 1 and call(own=None) == 1
+    assert call(prefix=desc(v=None)) == 1 and call(own=desc(stride_n=100)) == 2
+    assert call(prefix=desc(True, pages_per_seq=15)) == 2
+    assert call(own=desc(True, page_size=24)) == 3
+    assert call(win=desc(True)) == 3 and call(win=desc(k=None)) == 1
+    assert call(ws=None) == 4 and call(ws_bytes=1000) == 4 and call(ws=FAKE + 8) == 4
+    assert "workspace" in lib.dustin_last_error().decode()
+    assert call(b=0, q=None) == 0
+    size = lib.dustin_prefix_verify_attn_workspace_size
+    assert size(4, 2, 8, 2, 128, 4, 256, 64) > 0
+    assert size(4, 3, 8, 2, 128, 4, 256, 64) == 0 and size(0, 1, 8, 2, 128, 4, 256, 64) == 0
