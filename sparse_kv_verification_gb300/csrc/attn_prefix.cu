@@ -19,12 +19,13 @@
 // the workspace, one slot per (CTA, item), and attn_prefix_combine_kernel
 // adds each row's partials in a fixed order.
 //
-// Roles of the 12 warps: 0-3 and 4-7 softmax (one thread per row of stream
-// A / B), 8 issues tcgen05.mma, 9 TMA (10 and 11 complete their warpgroup).  S = Q K^T and O += P V accumulate in
-// tensor memory (S_A, S_B, O_A, O_B: 512 columns); P replaces S in place as
-// bf16 and is read from there as the A operand, so only Q, K and V live in
-// shared memory.  While one stream's softmax runs, the tensor cores work on
-// the other's products.
+// Roles of the 20 warps: 0-7 and 8-15 softmax of stream A / B (two threads
+// per row, 64 columns each), 16 issues tcgen05.mma, 17 TMA loads of K and V,
+// 18 copies Q rows, 19 walks the CTA's range and publishes its segments.
+// S = Q K^T and O += P V accumulate in tensor memory (S_A, S_B, O_A, O_B:
+// 512 columns); P replaces S in place as bf16 and is read from there as the A
+// operand, so only Q, K and V live in shared memory.  While one stream's
+// softmax runs, the tensor cores work on the other's products.
 #include <algorithm>
 #include <cuda.h>
 
@@ -40,21 +41,22 @@ namespace {
 __device__ unsigned int g_prefix_dev_flags;
 
 constexpr int kTile = 128;        // positions of a K/V tile, rows of a row tile
-constexpr int kThreads = 384;
-// Registers: a softmax thread holds a row of S (128 values); the producer and
-// MMA warps' group gives up what they need beyond the launch's 168.
+constexpr int kSoftmaxWarps = 8;  // per stream
+constexpr int kThreads = (2 * kSoftmaxWarps + 4) * 32;
+// Registers: a softmax thread holds half a row of S (64 values); the other
+// warpgroup gives up what they need beyond the launch's 96.
 struct Split {
-  static constexpr int NT = kThreads, NPW = 4, NCW = 8;
-  static constexpr int PRODUCER_REGS = 72, CONSUMER_REGS = 216;
+  static constexpr int NT = kThreads, NPW = 4, NCW = 2 * kSoftmaxWarps;
+  static constexpr int PRODUCER_REGS = 64, CONSUMER_REGS = 104;
 };
 constexpr int kMaskRing = 8;
+constexpr int kSegRing = 4;
 
 template <int D>
 struct Cfg {
   static constexpr int TILE_BYTES = kTile * D * 2;
   static constexpr int SLOTS = D == 128 ? 5 : 10;
   static constexpr int HALF = kTile * 128;            // bytes of a 64-column half
-  static constexpr int SMEM = 1024 + (2 + SLOTS) * TILE_BYTES;
 };
 
 // A cache as the kernel sees it; the tensor maps come beside it.
@@ -85,15 +87,40 @@ struct Maps {
   CUtensorMap k[3], v[3];
 };
 
-struct Shared {
+// One CTA's share of one item.
+struct Seg {
+  int kind;            // 0 prefix, 1 own, -1: no more
+  int gi, h, rt;       // group or sequence, kv head, first row tile
+  int t0, n;           // tiles of the item
+  int len, hist;       // cached positions, tiles that hold them
+  int slot;            // partial slot
+  int pair;
+  // Steps of stream s: a pair's streams share every tile, a single's alternate.
+  __device__ __forceinline__ int steps(int s) const { return pair ? n : (n + 1 - s) >> 1; }
+  // Tile of a step, counted from t0.
+  __device__ __forceinline__ int tile(int s, int step) const { return pair ? step : 2 * step + s; }
+  // Ring order of the tiles' K and V: the order in which the MMA warp is
+  // done with them.
+  __device__ __forceinline__ int k_at(int t) const { return pair ? 2 * t : t ? 2 * t - 1 : 0; }
+  __device__ __forceinline__ int v_at(int t) const {
+    return pair ? 2 * t + 1 : t + 1 < n ? 2 * t + 2 : 2 * t + 1;
+  }
+};
+
+struct Control {
+  float exchange[2][2][kTile];     // between the two threads of a row
   unsigned long long full[10], empty[10];
-  unsigned long long q_full[2], s_full[2], p_ready[2], o_final[2], mask_full[kMaskRing], drain;
+  unsigned long long q_full[2], q_empty[2], s_full[2], p_ready[2], o_final[2];
+  unsigned long long seg_full[kSegRing], seg_empty[kSegRing], mask_full[kMaskRing], drain;
   unsigned bad[kMaskRing][4];      // positions on pages outside the pool
-  int scan[16];
-  int start_kind, start_gi, start_pos, total;
+  Seg seg[kSegRing];
   int abort;
   uint32_t tmem;
 };
+
+template <int D>
+constexpr int kSmem = (2 + Cfg<D>::SLOTS) * Cfg<D>::TILE_BYTES + (int)sizeof(Control);
+static_assert(kSmem<128> <= 232448, "shared memory of one CTA");
 
 // The clobbers keep a role's set-up code inside the role.
 __device__ __forceinline__ void role_begin() { asm volatile("" ::: "memory"); }
@@ -137,47 +164,34 @@ __device__ __forceinline__ int tiles_of(const PrefixKArgs& a, int kind, int len)
 __device__ __forceinline__ int sharers(int total, int grid) {
   return max(1, min(grid, total >> 1));
 }
-// First position of CTA c's range, n CTAs sharing the line.
-__device__ __forceinline__ int range_start(int c, int total, int n) {
-  return c >= n ? total : (int)(((long long)c * total + n - 1) / n);
-}
-__device__ __forceinline__ int cta_of(int pos, int total, int n) {
-  return (int)((long long)pos * n / total);
-}
-
-// One CTA's share of one item.
-struct Seg {
-  int kind, gi, h, set, item;
-  int t0, t1;          // tiles of the item
-  int len, hist;       // cached positions, tiles that hold them
-  bool pair;
-  // Steps of stream s: a pair's streams share every tile, a single's alternate.
-  __device__ __forceinline__ int steps(int s) const {
-    const int n = t1 - t0;
-    return pair ? n : (n + 1 - s) >> 1;
+// The line cut into n ranges: range c starts at ceil(c * total / n), which is
+// c * (total / n) + ceil(c * (total % n) / n), all in 32 bits.
+struct Cut {
+  int n, total, q, r;
+  __device__ __forceinline__ Cut(int line, int grid) {
+    total = line;
+    n = sharers(line, grid);
+    q = total / n;
+    r = total - q * n;
   }
-  __device__ __forceinline__ int tile(int s, int step) const {
-    return t0 + (pair ? step : 2 * step + s);
+  __device__ __forceinline__ int start(int c) const {
+    return c >= n ? total : c * q + (c * r + n - 1) / n;
   }
-  // Ring order of the tiles' K and V (t counted from t0): the order in which
-  // the MMA warp is done with them.
-  __device__ __forceinline__ int k_at(int t) const { return pair ? 2 * t : t ? 2 * t - 1 : 0; }
-  __device__ __forceinline__ int v_at(int t) const {
-    return pair ? 2 * t + 1 : t + 1 < t1 - t0 ? 2 * t + 2 : 2 * t + 1;
+  // The range that holds pos: a float estimate, at most one off, put right.
+  __device__ __forceinline__ int of(int pos) const {
+    int c = min((int)((float)pos * (float)n / (float)total), n - 1);
+    while (start(c) > pos) --c;
+    while (start(c + 1) <= pos) ++c;
+    return c;
   }
 };
 
-// Walks the segments of [b0, b1); every role walks on its own.
+// Walks the segments of [b0, b1).
 struct Walk {
   const PrefixKArgs& a;
   int b0, b1, kind, gi, h, set, pos, len, tiles;
-  __device__ Walk(const PrefixKArgs& args, const Shared& sh) : a(args) {
-    const int n = sharers(sh.total, a.grid);
-    b0 = range_start(blockIdx.x, sh.total, n);
-    b1 = range_start(blockIdx.x + 1, sh.total, n);
-    kind = sh.start_kind;
-    gi = sh.start_gi;
-    pos = sh.start_pos;
+  __device__ explicit Walk(const PrefixKArgs& args) : a(args) {
+    plan();
     h = set = 0;
     if (b0 >= b1) {
       pos = b1;   // nothing here
@@ -190,6 +204,55 @@ struct Walk {
   __device__ __forceinline__ void load() {
     len = length_of(a, kind, gi);
     tiles = tiles_of(a, kind, len);
+  }
+  // The range [b0, b1) and the group or sequence it starts in; CTA 0 leaves
+  // the line's length and all starts on it for the combine kernel.  A warp
+  // scans the lengths, 32 at a time, twice (for the length, for the start).
+  __device__ void plan() {
+    const int lane = threadIdx.x & 31;
+    int total = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      int sum = 0;
+      if ((k ? a.own_len : a.prefix_len) == nullptr) {
+        sum = a.count[k] * tiles_of(a, k, a.n[k]);
+      } else {
+        for (int i = lane; i < a.count[k]; i += 32) sum += tiles_of(a, k, length_of(a, k, i));
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      }
+      total += sum * a.hkv * a.row_tiles[k];
+    }
+    const Cut cut(total, a.grid);
+    b0 = cut.start(blockIdx.x);
+    b1 = cut.start(blockIdx.x + 1);
+    kind = gi = pos = 0;
+    int base = 0;
+    if (blockIdx.x == 0 && lane == 0) a.plan[0] = total;
+    for (int k = 0; k < 2; ++k) {
+      const int unit = a.hkv * a.row_tiles[k];
+      for (int i0 = 0; i0 < a.count[k]; i0 += 32) {
+        const int i = i0 + lane;
+        const int mine = i < a.count[k] ? tiles_of(a, k, length_of(a, k, i)) * unit : 0;
+        int inc = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, inc, d);
+          if (lane >= d) inc += y;
+        }
+        const int at = base + inc - mine;
+        if (blockIdx.x == 0 && i < a.count[k]) a.plan[1 + k * a.count[0] + i] = at;
+        const unsigned here = __ballot_sync(0xffffffffu, at <= b0 && b0 < at + mine);
+        if (here) {
+          const int src = __ffs((int)here) - 1;
+          kind = k;
+          gi = i0 + src;
+          pos = __shfl_sync(0xffffffffu, at, src);
+          if (blockIdx.x != 0) return;
+        }
+        base += __shfl_sync(0xffffffffu, inc, 31);
+      }
+    }
   }
   __device__ bool next(Seg& s) {
     while (pos < b1) {
@@ -210,10 +273,10 @@ struct Walk {
       s.kind = kind;
       s.gi = gi;
       s.h = h;
-      s.set = set;
-      s.item = (gi * a.hkv + h) * ((rt + 1) >> 1) + set;
+      s.rt = 2 * set;
+      s.slot = blockIdx.x + (gi * a.hkv + h) * ((rt + 1) >> 1) + set;
       s.t0 = lo;
-      s.t1 = hi;
+      s.n = hi - lo;
       s.len = len;
       s.hist = (len + kTile - 1) / kTile;
       s.pair = pair;
@@ -228,69 +291,87 @@ struct Walk {
   }
 };
 
-// The line's length, where this CTA's range starts, and (CTA 0) the starts of
-// all groups and sequences for the combine kernel.
-__device__ void make_plan(const PrefixKArgs& a, Shared& sh) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int base = 0, first[2];
-  int mine_lo[2], mine_hi[2];
-  for (int kind = 0; kind < 2; ++kind) {
-    const int unit = a.hkv * a.row_tiles[kind];
-    const int m = (a.count[kind] + kThreads - 1) / kThreads;
-    const int lo = min(tid * m, a.count[kind]), hi = min(lo + m, a.count[kind]);
-    int sum = 0;
-    for (int i = lo; i < hi; ++i) sum += tiles_of(a, kind, length_of(a, kind, i)) * unit;
-    int inc = sum;
+// ---- softmax arithmetic: two columns at a time
+
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float lo_of(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float hi_of(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max32(const uint32_t (&x)[32], float top) {
+  float a = top, b = __uint_as_float(x[0]);
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += y;
-    }
-    __syncthreads();
-    if (lane == 31) sh.scan[warp] = inc;
-    __syncthreads();
-    int below = 0, all = 0;
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < warp) below += sh.scan[i];
-      all += sh.scan[i];
-    }
-    first[kind] = base + below + inc - sum;
-    mine_lo[kind] = lo;
-    mine_hi[kind] = hi;
-    base += all;
+  for (int i = 1; i < 29; i += 4) {
+    a = max3(a, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+    b = max3(b, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
   }
-  const int total = base;
-  if (tid == 0) {
-    sh.total = total;
-    if (blockIdx.x == 0) a.plan[0] = total;
+  a = max3(a, __uint_as_float(x[29]), __uint_as_float(x[30]));
+  return max3(a, b, __uint_as_float(x[31]));
+}
+// p = 2^(x * scale - m) as 16 bf16 pairs, the fp32 values added to sum, the
+// largest x to top.
+__device__ __forceinline__ void exp32(const uint32_t (&x)[32], uint64_t scale, uint64_t minus_m,
+                                      uint64_t (&sum)[2], float& top, uint32_t* p) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    top = max3(top, __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+    const uint64_t y = fma2(pack2(x[2 * i], x[2 * i + 1]), scale, minus_m);
+    const float e0 = ex2(lo_of(y)), e1 = ex2(hi_of(y));
+    sum[i & 1] = add2(sum[i & 1], pack2(__float_as_uint(e0), __float_as_uint(e1)));
+    // P in bf16, as the tensor cores take it (relative rounding 2^-8 per
+    // weight); the row sum keeps the fp32 values.
+    p[i] = pack_bf16(e0, e1);
   }
-  const int b0 = range_start(blockIdx.x, total, sharers(total, a.grid));
-  for (int kind = 0; kind < 2; ++kind) {
-    const int unit = a.hkv * a.row_tiles[kind];
-    int at = first[kind];
-    for (int i = mine_lo[kind]; i < mine_hi[kind]; ++i) {
-      const int next = at + tiles_of(a, kind, length_of(a, kind, i)) * unit;
-      if (at <= b0 && b0 < next) {
-        sh.start_kind = kind;
-        sh.start_gi = i;
-        sh.start_pos = at;
-      }
-      if (blockIdx.x == 0) a.plan[1 + kind * a.count[0] + i] = at;
-      at = next;
-    }
-  }
-  __syncthreads();
+}
+// Columns [lim, 32) of x do not count.
+__device__ __forceinline__ void mask32(uint32_t (&x)[32], int lim) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (i >= lim) x[i] = 0xff800000u;   // -inf
+}
+__device__ __forceinline__ void mask_bits(uint32_t (&x)[32], unsigned bad) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (bad >> i & 1) x[i] = 0xff800000u;
+}
+
+// Barrier of the two warps that share 32 rows; whether any thread said yes.
+__device__ __forceinline__ bool pair_any(int id, bool yes) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
+      " bar.red.or.pred q, %2, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)yes), "r"(id)
+      : "memory");
+  return r != 0;
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_prefix_kernel(const __grid_constant__ PrefixKArgs a, const __grid_constant__ Maps maps) {
   using C = Cfg<D>;
-  extern __shared__ unsigned char raw[];
-  __shared__ Shared sh;
-  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  extern __shared__ __align__(1024) unsigned char raw[];
+  Control& sh = *reinterpret_cast<Control*>(raw + (2 + C::SLOTS) * C::TILE_BYTES);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t q_buf = base, ring = base + 2 * C::TILE_BYTES;
+  const uint32_t q_buf = smem_u32(raw), ring = q_buf + 2 * C::TILE_BYTES;
 
   if (tid == 0) {
     for (int i = 0; i < C::SLOTS; ++i) {
@@ -298,38 +379,123 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sh.empty[i]), 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_u32(&sh.q_full[s]), 4);
+      mbar_init(smem_u32(&sh.q_full[s]), 1);
+      mbar_init(smem_u32(&sh.q_empty[s]), 1);
       mbar_init(smem_u32(&sh.s_full[s]), 1);
-      mbar_init(smem_u32(&sh.p_ready[s]), 4);
+      mbar_init(smem_u32(&sh.p_ready[s]), kSoftmaxWarps);
       mbar_init(smem_u32(&sh.o_final[s]), 1);
     }
     for (int i = 0; i < kMaskRing; ++i) mbar_init(smem_u32(&sh.mask_full[i]), 1);
+    for (int i = 0; i < kSegRing; ++i) {
+      mbar_init(smem_u32(&sh.seg_full[i]), 1);
+      mbar_init(smem_u32(&sh.seg_empty[i]), 2 * kSoftmaxWarps + 3);
+    }
     mbar_init(smem_u32(&sh.drain), 1);
     mbar_fence_init();
     sh.abort = 0;
   }
-  if (warp == 8) tmem_alloc<512>(smem_u32(&sh.tmem));
+  if (warp == 16) tmem_alloc<512>(smem_u32(&sh.tmem));
+  // Rows a row tile lacks keep finite values: zeros, later another tile's.
+  for (int i = tid; i < 2 * C::TILE_BYTES / 16; i += kThreads)
+    *reinterpret_cast<uint4*>(raw + i * 16) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   griddep_wait();
   griddep_launch_dependents();
-  make_plan(a, sh);          // ends with a CTA barrier
-  tc_fence_after();
   const uint32_t tmem = sh.tmem;
 
-  if (warp >= 8) give_registers();   // one instruction for the whole warpgroup
-  if (warp == 9) {
-    // ------------------------------------------------------------- producer
+  // Segment `at` of the ring, once published; null: given up.
+  auto segment = [&](int at) -> const Seg* {
+    if (!pwait_warp(&sh.seg_full[at % kSegRing], (at / kSegRing) & 1, &sh.abort)) return nullptr;
+    return &sh.seg[at % kSegRing];
+  };
+  auto done_with = [&](int at) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh.seg_empty[at % kSegRing]));
+  };
+
+  if (warp >= 16) give_registers();   // one instruction for the whole warpgroup
+  if (warp == 19) {
+    // --------------------------------------------------------------- walker
     role_begin();
-    Walk walk(a, sh);
+    Walk walk(a);
     Seg s;
+    for (int at = 0;; ++at) {
+      const bool more = walk.next(s);
+      if (!pwait_warp(&sh.seg_empty[at % kSegRing], (at / kSegRing & 1) ^ 1, &sh.abort)) break;
+      if (!more) s.kind = -1;
+      if (lane == 0) {
+        sh.seg[at % kSegRing] = s;
+        mbar_arrive(smem_u32(&sh.seg_full[at % kSegRing]));
+      }
+      if (!more) break;
+    }
+  } else if (warp == 18) {
+    // ------------------------------------------------------------------- Q
+    // Row tiles in the tensor cores' swizzled layout; a pair fills both
+    // buffers, singles take turns, so that the next one's rows are there
+    // before this one ends.
+    role_begin();
+    int fills[2] = {0, 0}, turn = 0;
+    for (int at = 0;; ++at) {
+      const Seg* sp = segment(at);
+      if (!sp || sp->kind < 0) break;
+      const Seg s = *sp;
+      done_with(at);
+      bool ok = true;
+      for (int i = 0; ok && i <= s.pair; ++i) {
+        const int buf = s.pair ? i : turn;
+        const int first = (s.rt + i) * kTile;
+        const int rows = min(kTile, a.rows[s.kind] - first);
+        ok = pwait_warp(&sh.q_empty[buf], (fills[buf] & 1) ^ 1, &sh.abort);
+        if (!ok) break;
+        ++fills[buf];
+        constexpr int CPR = D / 8, STEP = 32 / CPR;     // 16-byte pieces, rows per pass
+        const int c = lane % CPR;
+        int r = lane / CPR;
+        int seq = s.gi, in_seq = first + r;
+        if (s.kind == 0) {
+          seq = s.gi * a.per + in_seq / a.gw;
+          in_seq %= a.gw;
+        }
+        const uint32_t dst = q_buf + buf * C::TILE_BYTES + (c / 8) * C::HALF;
+        const __nv_bfloat16* src = a.q + ((long long)seq * a.hq_w + s.h * a.gw + in_seq) * D + c * 8;
+        for (; r < rows; r += STEP) {
+          cp_async_16_full(dst + r * 128 + ((c % 8 ^ (r & 7)) << 4), src);
+          in_seq += STEP;
+          src += STEP * D;
+          while (s.kind == 0 && in_seq >= a.gw) {       // on to the next sequence's rows
+            in_seq -= a.gw;
+            src += (long long)(a.hq_w - a.gw) * D;
+          }
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.q_full[buf]));
+      }
+      if (!ok) break;
+      if (!s.pair) turn ^= 1;
+    }
+  } else if (warp == 17) {
+    // --------------------------------------------------------- K and V loads
+    role_begin();
     int slot = 0, tile_count = 0;
     uint32_t phase = 0;
     int filled = 0;          // slots filled at least once
     bool ok = true;
-    while (ok && walk.next(s)) {
-      const int n = s.t1 - s.t0;
+    for (int at = 0; ok; ++at) {
+      const Seg* sp = segment(at);
+      ok = sp != nullptr;
+      if (!ok || sp->kind < 0) break;
+      const Seg s = *sp;
+      done_with(at);
       int kt = 0, vt = 0;    // next K, V tile
-      for (int x = 0; ok && x < 2 * n; ++x) {
-        const bool is_k = kt < n && s.k_at(kt) == x;
+      for (int x = 0; x < 2 * s.n; ++x) {
+        const bool is_k = kt < s.n && s.k_at(kt) == x;
         const int t = s.t0 + (is_k ? kt++ : vt++);
         ok = pwait_warp(&sh.empty[slot], phase ^ 1, &sh.abort);
         if (!ok) break;
@@ -371,12 +537,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const unsigned runs = __ballot_sync(0xffffffffu, bad != 0);
             if (lane < 4) {
               unsigned bits = 0;
-              for (int i = 0; i < 32; ++i)
-                if (runs >> ((lane * 32 + i) / c.box_rows) & 1) bits |= 1u << i;
-              sh.bad[tile_count % kMaskRing][lane] = runs ? bits : 0;
+              if (runs)
+                for (int i = 0; i < 32; ++i)
+                  if (runs >> ((lane * 32 + i) / c.box_rows) & 1) bits |= 1u << i;
+              sh.bad[tile_count % kMaskRing][lane] = bits;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.mask_full[tile_count % kMaskRing]));
+            ++tile_count;
           }
           __syncwarp();
           if (lane < boxes * (D / 64)) {
@@ -385,7 +553,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         (row0 + r) % c.page_size, s.h * c.zh, page, bar);
           }
         }
-        if (is_k && c.page_table) ++tile_count;
         filled = min(filled + 1, C::SLOTS);
         if (++slot == C::SLOTS) {
           slot = 0;
@@ -401,195 +568,245 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(smem_u32(&sh.full[slot]), phase, kWaitLimitCycles);
       }
     }
-  } else if (warp == 8) {
+  } else if (warp == 16) {
     // ------------------------------------------------------------------ MMA
+    // The whole warp walks, one lane issues.  Slots are used in ring order: a
+    // running position serves K and V alike.
     role_begin();
-    if (lane == 0) {
-      Walk walk(a, sh);
-      Seg s;
-      constexpr uint32_t kQk = mma_idesc(128, 128, false), kPv = mma_idesc(128, D, true);
-      int ring0 = 0;                        // ring position of the segment's first slot
-      uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-      bool ok = true;
-      auto full = [&](int at) {
-        return pwait(&sh.full[at % C::SLOTS], (at / C::SLOTS) & 1, &sh.abort);
-      };
-      auto qk = [&](int st, int at) {
-        const uint64_t qd = smem_desc(q_buf + st * C::TILE_BYTES, 16, 1024);
-        const uint64_t kd = smem_desc(ring + at % C::SLOTS * C::TILE_BYTES, 16, 1024);
+    constexpr uint32_t kQk = mma_idesc(128, 128, false), kPv = mma_idesc(128, D, true);
+    constexpr uint32_t kStep = C::TILE_BYTES >> 4;       // slots apart, in descriptor units
+    const uint32_t on = elect_one();
+    const uint64_t qd0 = smem_desc(q_buf, 16, 1024), kd0 = smem_desc(ring, 16, 1024);
+    const uint64_t vd0 = smem_desc(ring, C::HALF, 1024);
+    int slot = 0, turn = 0;
+    uint32_t phase = 0, q_phase0 = 0, q_phase1 = 0, p_phase0 = 0, p_phase1 = 0;
+    bool ok = true;
+    auto next_slot = [&]() {
+      if (++slot == C::SLOTS) {
+        slot = 0;
+        phase ^= 1;
+      }
+    };
+    auto full = [&]() { return pwait_warp(&sh.full[slot], phase, &sh.abort); };
+    auto qk = [&](int st, int buf) {
+      const uint64_t qd = qd0 + buf * kStep, kd = kd0 + slot * kStep;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (uint32_t)((k / 4) * C::HALF + (k % 4) * 32) >> 4;
-          mma_ss(tmem + st * 128, qd + off, kd + off, kQk, k > 0);
-        }
-        mma_commit(smem_u32(&sh.s_full[st]));
-      };
-      auto pv = [&](int st, int at, bool acc) {
-        const uint64_t vd = smem_desc(ring + at % C::SLOTS * C::TILE_BYTES, C::HALF, 1024);
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t off = (uint32_t)((k / 4) * C::HALF + (k % 4) * 32) >> 4;
+        mma_ss(on, tmem + st * 128, qd + off, kd + off, kQk, k > 0);
+      }
+      mma_commit(on, smem_u32(&sh.s_full[st]));
+    };
+    auto pv = [&](int st, bool acc) {
+      const uint64_t vd = vd0 + slot * kStep;
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          mma_ts(tmem + 256 + st * 128, tmem + st * 128 + k * 8, vd + (uint32_t)(k * 2048 >> 4),
-                 kPv, acc || k > 0);
-      };
-      auto release = [&](int at) { mma_commit(smem_u32(&sh.empty[at % C::SLOTS])); };
-      while (ok && walk.next(s)) {
-        const int last = s.pair ? 1 : 0;   // the stream after which a pair's slot is free
-        for (int st = 0; ok && st < 2; ++st) {
-          if (s.steps(st) == 0) continue;
-          const int at = ring0 + s.k_at(s.tile(st, 0) - s.t0);
-          ok = pwait(&sh.q_full[st], q_phase[st], &sh.abort) && full(at);
-          if (!ok) break;
-          q_phase[st] ^= 1;
-          tc_fence_after();
-          qk(st, at);
-          if (!s.pair || st == last) release(at);
-        }
-        for (int step = 0; ok && step < s.steps(0); ++step) {
-          for (int st = 0; ok && st < 2; ++st) {
-            if (step >= s.steps(st)) continue;
-            const int vat = ring0 + s.v_at(s.tile(st, step) - s.t0);
-            ok = pwait(&sh.p_ready[st], p_phase[st], &sh.abort) && full(vat);
-            if (!ok) break;
-            p_phase[st] ^= 1;
-            tc_fence_after();
-            pv(st, vat, step > 0);
-            if (!s.pair || st == last) release(vat);
-            if (step + 1 < s.steps(st)) {
-              const int kat = ring0 + s.k_at(s.tile(st, step + 1) - s.t0);
-              ok = full(kat);
-              if (!ok) break;
-              qk(st, kat);
-              if (!s.pair || st == last) release(kat);
-            } else {
-              mma_commit(smem_u32(&sh.o_final[st]));
-            }
+      for (int k = 0; k < kTile / 16; ++k)
+        mma_ts(on, tmem + 256 + st * 128, tmem + st * 128 + k * 8, vd + (uint32_t)(k * 2048 >> 4),
+               kPv, acc || k > 0);
+    };
+    auto release = [&]() { mma_commit(on, smem_u32(&sh.empty[slot])); };
+    auto p_ready = [&](int st) {
+      uint32_t& ph = st ? p_phase1 : p_phase0;
+      const bool r = pwait_warp(&sh.p_ready[st], ph, &sh.abort);
+      ph ^= 1;
+      tc_fence_after();
+      return r;
+    };
+    auto q_ready = [&](int buf) {
+      uint32_t& ph = buf ? q_phase1 : q_phase0;
+      const bool r = pwait_warp(&sh.q_full[buf], ph, &sh.abort);
+      ph ^= 1;
+      tc_fence_after();
+      return r;
+    };
+    for (int at = 0; ok; ++at) {
+      const Seg* sp = segment(at);
+      ok = sp != nullptr;
+      if (!ok) break;
+      const int kind = sp->kind, n = sp->n, paired = sp->pair;
+      if (kind < 0) break;
+      done_with(at);
+      if (paired) {
+        // K0 for both, then per tile: V, next K, each used by A, then by B.
+        if (!(ok = q_ready(0) && full())) break;
+        qk(0, 0);
+        if (!(ok = q_ready(1))) break;
+        qk(1, 1);
+        release();
+        next_slot();
+        for (int i = 0; i < n; ++i) {
+          const bool more = i + 1 < n;
+          const int vslot = slot;
+          if (!(ok = p_ready(0) && full())) break;
+          pv(0, i > 0);
+          next_slot();
+          if (more) {
+            if (!(ok = full())) break;
+            qk(0, 0);
+          } else {
+            mma_commit(on, smem_u32(&sh.o_final[0]));
+            mma_commit(on, smem_u32(&sh.q_empty[0]));
+          }
+          if (!(ok = p_ready(1))) break;
+          const int kslot = slot;
+          slot = vslot;
+          pv(1, i > 0);
+          release();
+          slot = kslot;
+          if (more) {
+            qk(1, 1);
+            release();
+            next_slot();
+          } else {
+            mma_commit(on, smem_u32(&sh.o_final[1]));
+            mma_commit(on, smem_u32(&sh.q_empty[1]));
           }
         }
-        ring0 += 2 * (s.t1 - s.t0);
-      }
-      if (!ok) {   // given up: the products in flight end before tensor memory is freed
-        mma_commit(smem_u32(&sh.drain));
-        mbar_wait(smem_u32(&sh.drain), 0, kWaitLimitCycles);
+      } else {
+        // Streams take the tiles in turn: K0, K1, then V0, K2, V1, K3, ...
+        const int buf = turn;
+        turn ^= 1;
+        if (!(ok = q_ready(buf) && full())) break;
+        qk(0, buf);
+        release();
+        next_slot();
+        if (n > 1) {
+          if (!(ok = full())) break;
+          qk(1, buf);
+          release();
+          next_slot();
+        }
+        if (n <= 2) mma_commit(on, smem_u32(&sh.q_empty[buf]));
+        for (int i = 0; i < n; ++i) {
+          const int st = i & 1;
+          if (!(ok = p_ready(st) && full())) break;
+          pv(st, i > 1);
+          release();
+          next_slot();
+          if (i + 2 < n) {
+            if (!(ok = full())) break;
+            qk(st, buf);
+            release();
+            next_slot();
+            if (i + 3 == n) mma_commit(on, smem_u32(&sh.q_empty[buf]));
+          } else {
+            mma_commit(on, smem_u32(&sh.o_final[st]));
+          }
+        }
       }
     }
+    if (!ok) {   // given up: the products in flight end before tensor memory is freed
+      mma_commit(on, smem_u32(&sh.drain));
+      mbar_wait(smem_u32(&sh.drain), 0, kWaitLimitCycles);
+    }
     __syncwarp();
-  } else if (warp < 8) {
+  } else {
     // -------------------------------------------------------------- softmax
     take_registers();
-    const int st = warp >> 2, row = tid & 127;
+    const int st = warp >> 3, half = warp >> 2 & 1, row = (warp & 3) * 32 + lane;
+    const int pair_id = 1 + st * 4 + (warp & 3);
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // TMEM lane of the warp's first row
-    const uint32_t tS = tmem + lanes + st * 128, tO = tmem + lanes + 256 + st * 128;
-    Walk walk(a, sh);
-    Seg s;
-    int ring0 = 0, tile_count = 0;
+    const uint32_t tS = tmem + lanes + st * 128, tO = tmem + lanes + 256 + st * 128 + half * (D / 2);
+    float* mine = &sh.exchange[st][half][row];
+    const float* other = &sh.exchange[st][half ^ 1][row];
+    const uint64_t scale2 = pack2(__float_as_uint(a.scale_log2), __float_as_uint(a.scale_log2));
+    int ring0 = 0, tiles0 = 0;                 // ring position, paged tiles before the segment
     uint32_t s_phase = 0, o_phase = 0;
     bool ok = true;
-    while (ok && walk.next(s)) {
+    for (int at = 0; ok; ++at) {
+      const Seg* sp = segment(at);
+      if (!sp || sp->kind < 0) break;
+      const Seg s = *sp;
+      done_with(at);
       const int steps = s.steps(st);
-      const int rt = s.pair ? 2 * s.set + st : 2 * (a.row_tiles[s.kind] >> 1);
+      const int rt = s.rt + (s.pair ? st : 0);
       const int rows = min(kTile, a.rows[s.kind] - rt * kTile);
-      const long long slot = (long long)(blockIdx.x + s.item) * 2 + st;
-      float2* ml = a.ws_ml[s.kind] + slot * a.slot_rows[s.kind];
-      const int paged_tiles0 = tile_count;
-      if (a.cache[s.kind].page_table)
-        tile_count += max(0, min(s.t1, s.hist) - s.t0);
-      if (steps == 0) {
-        if (row < rows) ml[row] = make_float2(-INFINITY, 0.f);
-        ring0 += 2 * (s.t1 - s.t0);
-        continue;
-      }
-      // Q rows, swizzled as the tensor cores read them; absent rows are zero.
-      {
-        constexpr int CPR = D / 8;
-        const uint32_t dst = q_buf + st * C::TILE_BYTES;
-#pragma unroll 4
-        for (int i = row; i < kTile * CPR; i += 128) {
-          const int r = i / CPR, c = i % CPR;
-          const int rr = rt * kTile + r;
-          const int seq = s.kind ? s.gi : s.gi * a.per + rr / a.gw;
-          const int in_seq = s.kind ? rr : rr % a.gw;
-          const bool have = r < rows;
-          const __nv_bfloat16* src =
-              a.q + (have ? ((long long)seq * a.hq_w + s.h * a.gw + in_seq) * D + c * 8 : 0);
-          cp_async_16(dst + (c / 8) * C::HALF + r * 128 + ((c % 8 ^ (r & 7)) << 4), src,
-                      have ? 16 : 0);
-        }
-        cp_async_commit();
-        cp_async_wait<0>();
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.q_full[st]));
-      }
+      const int sr = a.slot_rows[s.kind];
+      const long long slot = (long long)s.slot * 2 + st;
+      float2* ml = a.ws_ml[s.kind] + slot * sr;
+      const bool paged = a.cache[s.kind].page_table != nullptr;
+      if (steps == 0 && half == 0 && row < rows) ml[row] = make_float2(-INFINITY, 0.f);
       const bool live = (warp & 3) * 32 < rows;           // the warp has rows
-      int t_row = 0;                                      // window row of this row
-      if (s.kind) t_row = (rt * kTile + row) % a.w;
-      float m = -INFINITY, l = 0.f;
+      const int t_row = s.kind ? (rt * kTile + row) % a.w : 0;   // window row of this row
+      float m = -INFINITY;
+      uint64_t sum[2] = {0, 0};
       for (int step = 0; step < steps; ++step) {
-        const int t = s.tile(st, step);
+        const int tl = s.tile(st, step), t = s.t0 + tl;
+        const bool window = s.kind && t >= s.hist;
+        // Columns [0, lim) of this thread's 64 count.
+        const int lim = (window ? min(a.w, t_row + 1) - (t - s.hist) * kTile : s.len - t * kTile) -
+                        half * 64;
         ok = pwait_warp(&sh.s_full[st], s_phase, &sh.abort);
         if (!ok) break;
         s_phase ^= 1;
         tc_fence_after();
-        // Columns [0, lim) count.
-        int lim;
-        const bool window = s.kind && t >= s.hist;
-        if (window)
-          lim = min(a.w, t_row + 1) - (t - s.hist) * kTile;
-        else
-          lim = s.len - t * kTile;
-        const bool paged = !window && a.cache[s.kind].page_table;
-        const int mslot = (paged_tiles0 + t - s.t0) % kMaskRing;
-        if (paged) {
-          ok = pwait_warp(&sh.mask_full[mslot],
-                          ((paged_tiles0 + t - s.t0) / kMaskRing) & 1, &sh.abort);
+        if (paged && !window) {
+          ok = pwait_warp(&sh.mask_full[(tiles0 + tl) % kMaskRing],
+                          ((tiles0 + tl) / kMaskRing) & 1, &sh.abort);
           if (!ok) break;
         }
         if (live) {
-          uint32_t x[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, x[c]);
-          tc_wait_ld();
-          if (__any_sync(0xffffffffu, lim < kTile)) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (c * 32 + i >= lim) x[c][i] = 0xff800000u;   // -inf
-          }
-          if (paged) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const unsigned bad = sh.bad[mslot][c];
-              if (bad) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (bad >> i & 1) x[c][i] = 0xff800000u;
+          uint32_t x0[32], x1[32], p[32];
+          auto load = [&]() {
+            tmem_ld32(tS + half * 64, x0);
+            tmem_ld32(tS + half * 64 + 32, x1);
+            tc_wait_ld();
+            if (__any_sync(0xffffffffu, lim < 64)) {
+              mask32(x0, lim);
+              mask32(x1, lim - 32);
+            }
+            if (paged && !window) {
+              const int k = (tiles0 + tl) % kMaskRing;
+              const unsigned b0 = sh.bad[k][2 * half], b1 = sh.bad[k][2 * half + 1];
+              if (b0 | b1) {
+                mask_bits(x0, b0);
+                mask_bits(x1, b1);
               }
             }
+          };
+          auto exps = [&](uint64_t (&to)[2]) {
+            const float ms = m == -INFINITY ? 0.f : -m;
+            const uint64_t mm = pack2(__float_as_uint(ms), __float_as_uint(ms));
+            float top0 = -INFINITY, top1 = -INFINITY;
+            exp32(x0, scale2, mm, to, top0, p);
+            exp32(x1, scale2, mm, to, top1, p + 16);
+            return fmaxf(top0, top1) * a.scale_log2;
+          };
+          load();
+          // The reference maximum m moves only when a tile exceeds it by
+          // more than a factor 2^8, so P is formed with the old one while
+          // the tile's maximum is still being taken; where it does move (the
+          // first tile, then rarely), S, not overwritten yet, is read again.
+          bool again = true;
+          float top;
+          if (step == 0) {
+            top = max32(x1, max32(x0, -INFINITY)) * a.scale_log2;
+          } else {
+            uint64_t to[2] = {sum[0], sum[1]};
+            top = exps(to);
+            // Also the point after which P may overwrite S: both threads of
+            // a row have read it.
+            again = pair_any(pair_id, m == -INFINITY ? top > m : top > m + kLazyRescale);
+            if (!again) {
+              sum[0] = to[0];
+              sum[1] = to[1];
+            }
           }
-          float mx[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            mx[c] = __uint_as_float(x[c][0]);
-#pragma unroll
-            for (int i = 1; i < 32; ++i) mx[c] = fmaxf(mx[c], __uint_as_float(x[c][i]));
-          }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-          // The reference maximum moves only when a tile exceeds it by more
-          // than a factor 2^8 (or sets it): P stays below 2^8, and O is
-          // rescaled a few times per item.
-          const bool up = top > m + kLazyRescale || (m == -INFINITY && top > m);
-          if (__any_sync(0xffffffffu, up)) {
-            const float m_new = up ? top : m;
-            const float f = up ? ex2(m - m_new) : 1.f;
-            m = m_new;
-            l *= f;
+          if (again) {
+            *mine = top;
+            named_bar_sync(pair_id, 64);
+            top = fmaxf(top, *other);
+            const bool up = m == -INFINITY ? top > m : top > m + kLazyRescale;
+            const float f = up ? ex2(m - top) : 1.f;
+            if (up) m = top;
+            const uint64_t f2 = pack2(__float_as_uint(f), __float_as_uint(f));
+            sum[0] = fma2(sum[0], f2, 0);
+            sum[1] = fma2(sum[1], f2, 0);
             if (step > 0) {
               // The product that wrote O was issued before the one that
               // signalled S: it is complete.
 #pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
+              for (int c = 0; c < D / 64; ++c) {
                 uint32_t o[32];
                 tmem_ld32(tO + c * 32, o);
                 tc_wait_ld();
@@ -598,39 +815,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st32(tO + c * 32, o);
               }
             }
+            load();
+            named_bar_sync(pair_id, 64);   // both have read S again
+            exps(sum);
           }
-          const float ms = m == -INFINITY ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t p[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float e0 = ex2(fmaf(__uint_as_float(x[c][2 * i]), a.scale_log2, -ms));
-              const float e1 = ex2(fmaf(__uint_as_float(x[c][2 * i + 1]), a.scale_log2, -ms));
-              sum[i & 3] += e0 + e1;
-              // P in bf16, as the tensor cores take it (relative rounding
-              // 2^-8 per weight); the row sum keeps the fp32 values.
-              p[i] = pack_bf16(e0, e1);
-            }
-            tmem_st16(tS + c * 16, p);
-          }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st32(tS + half * 32, p);
           tc_wait_st();
         }
         // V rows behind the end hold whatever the cache holds there, NaN
         // included: 0 * NaN must not reach O.
         const int valid = s.len - t * kTile;
         if (!window && valid < kTile && (!s.pair || st == 0)) {
-          const int vat = ring0 + s.v_at(t - s.t0);
+          const int vat = ring0 + s.v_at(tl);
           ok = pwait_warp(&sh.full[vat % C::SLOTS], (vat / C::SLOTS) & 1, &sh.abort);
           if (!ok) break;
           const uint32_t v = ring + vat % C::SLOTS * C::TILE_BYTES;
-          for (int i = valid * 8 + row; i < kTile * 8; i += 128)
+          for (int i = valid * 8 + half * 128 + row; i < kTile * 8; i += 256)
 #pragma unroll
-            for (int half = 0; half < D / 64; ++half)
-              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(
-                               v + half * C::HALF + i * 16),
+            for (int c = 0; c < D / 64; ++c)
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(v + c * C::HALF +
+                                                                              i * 16),
                            "r"(0)
                            : "memory");
           fence_proxy_async_smem();
@@ -640,35 +844,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(&sh.p_ready[st]));
       }
       if (!ok) break;
+      ring0 += 2 * s.n;
+      if (paged) tiles0 += max(0, min(s.t0 + s.n, s.hist) - s.t0);
+      if (steps == 0) continue;
       ok = pwait_warp(&sh.o_final[st], o_phase, &sh.abort);
       if (!ok) break;
       o_phase ^= 1;
       tc_fence_after();
       if (live) {
-        float* out = a.ws_o[s.kind] + (slot * a.slot_rows[s.kind] + row) * D;
+        // Pieces of four columns, rows side by side: full lines per store.
+        float* out = a.ws_o[s.kind] + slot * sr * D + (long long)(half * (D / 8)) * sr * 4 + row * 4;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < D / 64; ++c) {
           uint32_t o[32];
           tmem_ld32(tO + c * 32, o);
           tc_wait_ld();
           if (row < rows) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4*>(out + c * 32 + i) =
+              *reinterpret_cast<uint4*>(out + (c * 8 + i / 4) * (sr * 4)) =
                   make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
         }
-        if (row < rows) ml[row] = make_float2(m, l);
+        const uint64_t all = add2(sum[0], sum[1]);
+        const float l = lo_of(all) + hi_of(all);
+        if (half) *mine = l;
+        named_bar_sync(pair_id, 64);
+        if (!half && row < rows) ml[row] = make_float2(m, l + *other);
+        named_bar_sync(pair_id, 64);   // read before the next segment writes
       }
-      ring0 += 2 * (s.t1 - s.t0);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc<512>(tmem);
+  if (warp == 16) tmem_dealloc<512>(tmem);
 }
 
-// ---- combine: one warp per output row
+// ---- combine: one thread per four columns of an output row
 
 struct CombineArgs {
   PrefixKArgs k;
@@ -677,107 +889,79 @@ struct CombineArgs {
   long long rows;      // b * h_q * w
 };
 
-constexpr int kCombineWarps = 8;
+constexpr int kCombineThreads = 256;
 
 template <int D>
-__global__ void __launch_bounds__(kCombineWarps * 32)
+__global__ void __launch_bounds__(kCombineThreads)
     attn_prefix_combine_kernel(const __grid_constant__ CombineArgs c) {
-  constexpr int CPL = D / 32;
+  constexpr int ROWS = kCombineThreads / (D / 4);
   const PrefixKArgs& a = c.k;
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
+  const int piece = threadIdx.x / ROWS;
+  const long long row = (long long)blockIdx.x * ROWS + threadIdx.x % ROWS;
   griddep_wait();
   griddep_launch_dependents();
   if (row >= c.rows) return;
   const int seq = (int)(row / a.hq_w), in_seq = (int)(row % a.hq_w);
   const int h = in_seq / a.gw, r = in_seq % a.gw;
-  const int total = a.plan[0], n_cta = sharers(total, a.grid);
-  // Partials of the row: parts[0] of its prefix item, then parts[1] of its own.
-  int parts[2], first_cta[2], item[2], in_tile[2], twice[2], stream[2];
+  const Cut cut(a.plan[0], a.grid);
+  // Partials of the row in its prefix item and in its own: CTAs first ..
+  // first + ctas - 1, one stream of a pair's slot or both of a single's.
+  int ctas[2], twice[2];
+  long long at[2];
 #pragma unroll
   for (int kind = 0; kind < 2; ++kind) {
     const int gi = kind ? seq : seq / a.per;
     const int rr = kind ? r : seq % a.per * a.gw + r;
     const int rt = rr / kTile, pairs = a.row_tiles[kind] >> 1, set = rt >> 1;
     const bool pair = set < pairs;
-    const int tiles = a.count[kind] ? tiles_of(a, kind, length_of(a, kind, gi)) : 0;
-    parts[kind] = 0;
-    in_tile[kind] = rr % kTile;
-    stream[kind] = pair ? rt & 1 : 0;
+    const int tiles = tiles_of(a, kind, length_of(a, kind, gi));
+    ctas[kind] = 0;
     twice[kind] = pair ? 0 : 1;
-    item[kind] = (gi * a.hkv + h) * ((a.row_tiles[kind] + 1) >> 1) + set;
-    first_cta[kind] = 0;
     if (tiles > 0) {
       const int start = a.plan[1 + kind * a.count[0] + gi] +
                         (h * a.row_tiles[kind] + set * 2) * tiles;
-      first_cta[kind] = cta_of(start, total, n_cta);
-      const int last = cta_of(start + (tiles - 1) * (pair ? 2 : 1), total, n_cta);
-      parts[kind] = (last - first_cta[kind] + 1) << twice[kind];
+      const int first = cut.of(start);
+      ctas[kind] = cut.of(start + (tiles - 1) * (pair ? 2 : 1)) - first + 1;
+      const int item = (gi * a.hkv + h) * ((a.row_tiles[kind] + 1) >> 1) + set;
+      at[kind] = (long long)(first + item) * 2 + (pair ? rt & 1 : 0);
     }
   }
-  const int n = parts[0] + parts[1];
-  // Row index (in rows of its workspace) of partial i.
-  auto where = [&](int i, int& kind) {
-    kind = i >= parts[0];
-    const int x = kind ? i - parts[0] : i;
-    const int cta = first_cta[kind] + (x >> twice[kind]);
-    const int st = twice[kind] ? x & 1 : stream[kind];
-    return ((long long)(cta + item[kind]) * 2 + st) * a.slot_rows[kind] + in_tile[kind];
-  };
   float top = -INFINITY;
-  for (int i = lane; i < n; i += 32) {
-    int kind;
-    const long long at = where(i, kind);
-    top = fmaxf(top, a.ws_ml[kind][at].x);
-  }
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  const float m = top == -INFINITY ? 0.f : top;
-  float acc[CPL] = {};
-  float l = 0.f;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    float weight = 0.f, lsum = 0.f;
-    long long at = 0;
-    int kind = 0;
-    if (i0 + lane < n) {
-      at = where(i0 + lane, kind);
-      const float2 ml = a.ws_ml[kind][at];
-      weight = ex2(ml.x - m);
-      lsum = ml.y * weight;
-    }
-    l += lsum;
-    const int count = min(32, n - i0);
+  for (int kind = 0; kind < 2; ++kind) {
+    const int sr = a.slot_rows[kind], in_tile = (kind ? r : seq % a.per * a.gw + r) % kTile;
+    const int n = ctas[kind] << twice[kind], stride = 2 - twice[kind];
 #pragma unroll 4
-    for (int i = 0; i < count; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, weight, i);
-      const long long ai = __shfl_sync(0xffffffffu, at, i);
-      const int ki = __shfl_sync(0xffffffffu, kind, i);
-      if (wi == 0.f) continue;   // nothing seen there (O may be unwritten)
-      const float* src = a.ws_o[ki] + ai * D + lane * CPL;
-      float v[CPL];
-      if constexpr (CPL == 4) {
-        const float4 f = *reinterpret_cast<const float4*>(src);
-        v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-      } else {
-        const float2 f = *reinterpret_cast<const float2*>(src);
-        v[0] = f.x, v[1] = f.y;
-      }
+    for (int i = 0; i < n; ++i)
+      top = fmaxf(top, a.ws_ml[kind][(at[kind] + i * stride) * sr + in_tile].x);
+  }
+  const float m = top == -INFINITY ? 0.f : top;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
 #pragma unroll
-      for (int x = 0; x < CPL; ++x) acc[x] = fmaf(wi, v[x], acc[x]);
+  for (int kind = 0; kind < 2; ++kind) {
+    const int sr = a.slot_rows[kind], in_tile = (kind ? r : seq % a.per * a.gw + r) % kTile;
+    const int n = ctas[kind] << twice[kind], stride = 2 - twice[kind];
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const long long base = (at[kind] + i * stride) * sr;
+      const float2 ml = a.ws_ml[kind][base + in_tile];
+      const float4 v = *reinterpret_cast<const float4*>(a.ws_o[kind] + base * D +
+                                                        ((long long)piece * sr + in_tile) * 4);
+      const float wt = ex2(ml.x - m);
+      if (wt > 0.f) {   // otherwise nothing was seen there (O may be unwritten)
+        l = fmaf(wt, ml.y, l);
+        acc.x = fmaf(wt, v.x, acc.x);
+        acc.y = fmaf(wt, v.y, acc.y);
+        acc.z = fmaf(wt, v.z, acc.z);
+        acc.w = fmaf(wt, v.w, acc.w);
+      }
     }
   }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
   const float inv = top == -INFINITY ? 0.f : 1.f / l;
-  uint32_t out[CPL / 2];
-#pragma unroll
-  for (int x = 0; x < CPL / 2; ++x) out[x] = pack_bf16(acc[2 * x] * inv, acc[2 * x + 1] * inv);
-  __nv_bfloat16* dst = c.o + row * D + lane * CPL;
-  if constexpr (CPL == 4)
-    *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
-  else
-    *reinterpret_cast<uint32_t*>(dst) = out[0];
-  if (lane == 0) c.lse[row] = top == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
+  *reinterpret_cast<uint2*>(c.o + row * D + piece * 4) =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (piece == 0) c.lse[row] = top == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // ---- host side
@@ -868,21 +1052,21 @@ cudaError_t run_prefix(const PrefixKArgs& k, const Maps& maps, const PrefixArgs&
                        cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   auto kern = attn_prefix_kernel<D>;
-  cudaError_t e = ensure_smem_attr(kern, Cfg<D>::SMEM, done);
+  cudaError_t e = ensure_smem_attr(kern, kSmem<D>, done);
   if (e != cudaSuccess) return e;
   static std::atomic<int> split_ok{0};
   if ((e = check_register_split<Split>(kern, split_ok)) != cudaSuccess) return e;
-  e = launch_pdl(kern, dim3((unsigned)k.grid), dim3(kThreads), Cfg<D>::SMEM, st, k, maps);
+  e = launch_pdl(kern, dim3((unsigned)k.grid), dim3(kThreads), kSmem<D>, st, k, maps);
   if (e != cudaSuccess) return e;
   note_launches(1);
+  constexpr int kRows = kCombineThreads / (D / 4);
   CombineArgs c{};
   c.k = k;
   c.o = p.o;
   c.lse = p.lse;
   c.rows = (long long)p.b * p.hq * p.w;
   e = launch_pdl(attn_prefix_combine_kernel<D>,
-                 dim3((unsigned)((c.rows + kCombineWarps - 1) / kCombineWarps)),
-                 dim3(kCombineWarps * 32), 0, st, c);
+                 dim3((unsigned)((c.rows + kRows - 1) / kRows)), dim3(kCombineThreads), 0, st, c);
   if (e == cudaSuccess) note_launches(1);
   return e;
 }
