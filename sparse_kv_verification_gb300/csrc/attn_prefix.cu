@@ -13,19 +13,29 @@
 // tiles to pair run them side by side over each K/V tile; the odd one runs
 // alone, its even and odd K/V tiles side by side.
 //
-// One persistent CTA per SM; the items' tiles, weighted by row tiles, form
-// one line that is cut into equal ranges (lengths are on the device, so every
-// CTA computes its cut itself).  Partial results (O unnormalised, m, l) go to
-// the workspace, one slot per (CTA, item), and attn_prefix_combine_kernel
-// adds each row's partials in a fixed order.
+// One persistent CTA per SM; lengths are on the device, so every CTA works
+// out its share itself (Walk::make_plan).  The items' tiles form one line, cut
+// into equal ranges.  On it an item lies in chunks of M tiles: within a chunk
+// one segment after another, two half chunks for each pair, the whole for
+// the single, all M units (row tile x K/V tile) long, about one CTA's share.
+// So the CTAs that read the same K/V tiles for different rows do it at the
+// same time: a prefix of 32768 positions is as large as L2, and with the row
+// tiles one after another it came from HBM once per pair of them (512 rows:
+// 64 instead of 44 us for the loads alone).  A segment is no longer than a
+// range, so at most two CTAs share it: its partial results (O unnormalised,
+// m, l) have two places in the workspace, known without the cut, and
+// attn_prefix_combine_kernel adds each row's partials in a fixed order.
 //
-// Roles of the 20 warps: 0-7 and 8-15 softmax of stream A / B (two threads
-// per row, 64 columns each), 16 issues tcgen05.mma, 17 TMA loads of K and V,
-// 18 copies Q rows, 19 walks the CTA's range and publishes its segments.
-// S = Q K^T and O += P V accumulate in tensor memory (S_A, S_B, O_A, O_B:
-// 512 columns); P replaces S in place as bf16 and is read from there as the A
-// operand, so only Q, K and V live in shared memory.  While one stream's
-// softmax runs, the tensor cores work on the other's products.
+// Roles of the 12 warps: 0-3 and 4-7 softmax (one thread per row of stream
+// A / B), 8 issues tcgen05.mma, 9 TMA loads of K and V, 10 copies Q rows, 11
+// walks the CTA's range and publishes its segments.  S = Q K^T and O += P V
+// accumulate in tensor memory (512 columns: two S buffers of 64 positions and
+// an O per stream); P replaces S in place as bf16 and is read from there as
+// the A operand, so only Q, K and V live in shared memory.  With two S
+// buffers a stream's next scores are there before its P is consumed: a
+// softmax warp never waits for its own product, nor the tensor cores for one
+// softmax (with one buffer of 128 positions per stream, steps of 4400
+// cycles; see the figures at the kernel).
 #include <algorithm>
 #include <cuda.h>
 
@@ -41,13 +51,15 @@ namespace {
 __device__ unsigned int g_prefix_dev_flags;
 
 constexpr int kTile = 128;        // positions of a K/V tile, rows of a row tile
-constexpr int kSoftmaxWarps = 8;  // per stream
-constexpr int kThreads = (2 * kSoftmaxWarps + 4) * 32;
-// Registers: a softmax thread holds half a row of S (64 values); the other
-// warpgroup gives up what they need beyond the launch's 96.
+constexpr int kHalf = 64;         // positions of an S buffer
+constexpr int kSoftmaxWarps = 4;  // per stream
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kQWarp = 10, kWalkWarp = 11;
+constexpr int kThreads = 12 * 32;
+// Registers: a softmax thread holds 64 scores and their weights; the other
+// warpgroup gives up what they need beyond the launch's 168.
 struct Split {
   static constexpr int NT = kThreads, NPW = 4, NCW = 2 * kSoftmaxWarps;
-  static constexpr int PRODUCER_REGS = 64, CONSUMER_REGS = 104;
+  static constexpr int PRODUCER_REGS = 104, CONSUMER_REGS = 200;
 };
 constexpr int kMaskRing = 8;
 constexpr int kSegRing = 4;
@@ -73,7 +85,7 @@ struct PrefixKArgs {
   const int* own_len;
   float* ws_o[2];      // partial O: prefix slots, own slots
   float2* ws_ml[2];
-  int* plan;           // [0] total, then starts of the groups, of the sequences
+  int* plan;           // see kPlanInts
   PrefixCache cache[3];
   int n[2];            // prefix, own positions at most
   int count[2];        // groups, sequences
@@ -86,6 +98,7 @@ struct PrefixKArgs {
 struct Maps {
   CUtensorMap k[3], v[3];
 };
+constexpr int kPlanInts = 4;   // plan: range, then from here on first segments
 
 // One CTA's share of one item.
 struct Seg {
@@ -93,7 +106,8 @@ struct Seg {
   int gi, h, rt;       // group or sequence, kv head, first row tile
   int t0, n;           // tiles of the item
   int len, hist;       // cached positions, tiles that hold them
-  int slot;            // partial slot
+  int slot;            // partial slot: the segment's first or second
+  int whole;           // the segment is not shared: its second slot stays empty
   int pair;
   // Steps of stream s: a pair's streams share every tile, a single's alternate.
   __device__ __forceinline__ int steps(int s) const { return pair ? n : (n + 1 - s) >> 1; }
@@ -108,9 +122,9 @@ struct Seg {
 };
 
 struct Control {
-  float exchange[2][2][kTile];     // between the two threads of a row
+  float2 exchange[2][kTile];       // m, l of a single's streams
   unsigned long long full[10], empty[10];
-  unsigned long long q_full[2], q_empty[2], s_full[2], p_ready[2], o_final[2];
+  unsigned long long q_full[2], q_empty[2], s_full[2][2], p_ready[2][2], o_final[2];
   unsigned long long seg_full[kSegRing], seg_empty[kSegRing], mask_full[kMaskRing], drain;
   unsigned bad[kMaskRing][4];      // positions on pages outside the pool
   Seg seg[kSegRing];
@@ -158,135 +172,224 @@ __device__ __forceinline__ int length_of(const PrefixKArgs& a, int kind, int gi)
 __device__ __forceinline__ int tiles_of(const PrefixKArgs& a, int kind, int len) {
   return (len + kTile - 1) / kTile + (kind ? a.win_tiles : 0);
 }
-// CTAs that share a line of length total: at least two units each, so that
-// every CTA between an item's first and last one has a tile of it (a pair's
-// tiles lie two units apart).
-__device__ __forceinline__ int sharers(int total, int grid) {
-  return max(1, min(grid, total >> 1));
-}
-// The line cut into n ranges: range c starts at ceil(c * total / n), which is
-// c * (total / n) + ceil(c * (total % n) / n), all in 32 bits.
+// The line is counted in quarters of a unit (one row tile on one tile of a
+// prefix).  An own tile costs more than that, its K and V coming for one row
+// tile alone, and a segment's start and end cost about two units.
+__host__ __device__ constexpr int unit_cost(int kind) { return kind ? 5 : 4; }
+constexpr int kSegmentCost = 8;
+constexpr int kMinRange = 24;         // at least four tiles of a prefix and a segment's cost
+
+// The line cut into n ranges of at least kMinRange: range c starts at
+// ceil(c * total / n), which is c * (total / n) + ceil(c * (total % n) / n),
+// all in 32 bits.
 struct Cut {
   int n, total, q, r;
   __device__ __forceinline__ Cut(int line, int grid) {
     total = line;
-    n = sharers(line, grid);
+    n = max(1, min(grid, total / kMinRange));
     q = total / n;
     r = total - q * n;
   }
   __device__ __forceinline__ int start(int c) const {
     return c >= n ? total : c * q + (c * r + n - 1) / n;
   }
-  // The range that holds pos: a float estimate, at most one off, put right.
-  __device__ __forceinline__ int of(int pos) const {
-    int c = min((int)((float)pos * (float)n / (float)total), n - 1);
-    while (start(c) > pos) --c;
-    while (start(c + 1) <= pos) ++c;
-    return c;
+};
+
+// A segment's tiles on the line: n of them, w apart, then its fixed cost.
+struct Span {
+  int pos, n, w;
+  __device__ __forceinline__ int length() const { return n ? n * w + kSegmentCost : 0; }
+  // The first tile at or behind a cut at b.  A cut that would leave a piece
+  // shorter than `snap` moves to the segment's end.
+  __device__ __forceinline__ int tile(int b, int snap) const {
+    const int x = b - pos, len = length();
+    if (x <= 0) return 0;
+    if (x >= len) return n;
+    if (x < snap && x <= len - x) return 0;
+    if (len - x < snap) return n;
+    return min(n, (x + w - 1) / w);
   }
 };
 
-// Walks the segments of [b0, b1).
+// The chunks of one (group or sequence, kv head): each holds row_tiles
+// segments, 0 .. pairs-1 on its first half, pairs .. 2 pairs-1 on its second,
+// the single on all of it.
+struct Chunks {
+  int tiles, chunk, rt, pairs, unit;
+  __device__ __forceinline__ Chunks(const PrefixKArgs& a, int kind, int tiles_, int range) {
+    tiles = tiles_;
+    // The most tiles, an even number, whose segment fits a range.
+    chunk = max(2, (range - kSegmentCost) / unit_cost(kind) & ~1);
+    rt = a.row_tiles[kind];
+    pairs = rt >> 1;
+    unit = unit_cost(kind);
+  }
+  __device__ __forceinline__ int count() const { return (tiles + chunk - 1) / chunk; }
+  // Length on the line of a chunk of m tiles, of everything.
+  __device__ __forceinline__ int length_of(int m) const {
+    const int first = min(m, chunk >> 1);
+    return m * rt * unit + kSegmentCost * (rt - (m > first ? 0 : pairs));
+  }
+  __device__ __forceinline__ int length() const {
+    if (tiles == 0) return 0;
+    const int n = count();
+    return (n - 1) * length_of(chunk) + length_of(tiles - (n - 1) * chunk);
+  }
+  // Segment y of chunk c; pos: the chunk's place on the line.
+  __device__ __forceinline__ Span segment(int c, int y, int pos, int* t0) const {
+    const int m = min(chunk, tiles - c * chunk), first = min(m, chunk >> 1), second = m - first;
+    const int l0 = first * 2 * unit + kSegmentCost, l1 = second ? second * 2 * unit + kSegmentCost : 0;
+    *t0 = c * chunk;
+    if (y < pairs) return {pos + y * l0, first, 2 * unit};
+    if (y < 2 * pairs) {
+      *t0 += first;
+      return {pos + pairs * l0 + (y - pairs) * l1, second, 2 * unit};
+    }
+    return {pos + pairs * (l0 + l1), m, unit};
+  }
+};
+
+// Walks the segments of this CTA's range.
 struct Walk {
   const PrefixKArgs& a;
-  int b0, b1, kind, gi, h, set, pos, len, tiles;
+  int range, snap, b0, b1;   // range: a lower bound of the ranges' length
+  int kind, gi, h, c, y;
+  int pos, ord, len, tiles, chunks;   // pos: of chunk c; ord: of its first segment
   __device__ explicit Walk(const PrefixKArgs& args) : a(args) {
-    plan();
-    h = set = 0;
+    make_plan();
+    h = c = y = 0;
     if (b0 >= b1) {
       pos = b1;   // nothing here
-    } else {
-      load();
-      h = (b0 - pos) / (tiles * a.row_tiles[kind]);
-      pos += h * tiles * a.row_tiles[kind];
+      return;
     }
+    load();
+    const Chunks ch(a, kind, tiles, range);
+    h = (b0 - pos) / ch.length();
+    pos += h * ch.length();
+    if (chunks > 1) c = min((b0 - pos) / ch.length_of(ch.chunk), chunks - 1);
+    if (c) pos += c * ch.length_of(ch.chunk);
+    ord += (h * chunks + c) * ch.rt;
   }
   __device__ __forceinline__ void load() {
     len = length_of(a, kind, gi);
     tiles = tiles_of(a, kind, len);
+    chunks = Chunks(a, kind, tiles, range).count();
   }
-  // The range [b0, b1) and the group or sequence it starts in; CTA 0 leaves
-  // the line's length and all starts on it for the combine kernel.  A warp
-  // scans the lengths, 32 at a time, twice (for the length, for the start).
-  __device__ void plan() {
-    const int lane = threadIdx.x & 31;
+  // Sum over the warp's lanes.
+  __device__ static int warp_sum(int x) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+  }
+  // One warp.  CTA 0 leaves the range and the first segments of all groups
+  // and sequences for the combine kernel.
+  __device__ void make_plan() {
+    const int lane = threadIdx.x & 31, cta = blockIdx.x;
+    // An equal share of the tiles alone; the line, segment costs included, is
+    // longer.
+    int work = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      int sum = 0;
+      for (int i = lane; i < a.count[k]; i += 32) sum += tiles_of(a, k, length_of(a, k, i));
+      work += warp_sum(sum) * a.hkv * a.row_tiles[k] * unit_cost(k);
+    }
+    range = max(kMinRange, work / a.grid);
     int total = 0;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       int sum = 0;
-      if ((k ? a.own_len : a.prefix_len) == nullptr) {
-        sum = a.count[k] * tiles_of(a, k, a.n[k]);
-      } else {
-        for (int i = lane; i < a.count[k]; i += 32) sum += tiles_of(a, k, length_of(a, k, i));
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      }
-      total += sum * a.hkv * a.row_tiles[k];
+      for (int i = lane; i < a.count[k]; i += 32)
+        sum += Chunks(a, k, tiles_of(a, k, length_of(a, k, i)), range).length();
+      total += warp_sum(sum) * a.hkv;
     }
     const Cut cut(total, a.grid);
-    b0 = cut.start(blockIdx.x);
-    b1 = cut.start(blockIdx.x + 1);
-    kind = gi = pos = 0;
-    int base = 0;
-    if (blockIdx.x == 0 && lane == 0) a.plan[0] = total;
+    snap = cut.q >> 4;
+    b0 = cut.start(cta);
+    b1 = cut.start(cta + 1);
+    if (cta == 0 && lane == 0) {
+      a.plan[0] = range;
+    }
+    kind = gi = pos = ord = 0;
+    int base = 0, segments = 0;
     for (int k = 0; k < 2; ++k) {
-      const int unit = a.hkv * a.row_tiles[k];
       for (int i0 = 0; i0 < a.count[k]; i0 += 32) {
         const int i = i0 + lane;
-        const int mine = i < a.count[k] ? tiles_of(a, k, length_of(a, k, i)) * unit : 0;
-        int inc = mine;
+        int mine = 0, segs = 0;
+        if (i < a.count[k]) {
+          const Chunks ch(a, k, tiles_of(a, k, length_of(a, k, i)), range);
+          mine = ch.length() * a.hkv;
+          segs = ch.count() * ch.rt * a.hkv;
+        }
+        int inc = mine, sinc = segs;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, inc, d);
-          if (lane >= d) inc += y;
+          const int x = __shfl_up_sync(0xffffffffu, inc, d);
+          const int z = __shfl_up_sync(0xffffffffu, sinc, d);
+          if (lane >= d) {
+            inc += x;
+            sinc += z;
+          }
         }
-        const int at = base + inc - mine;
-        if (blockIdx.x == 0 && i < a.count[k]) a.plan[1 + k * a.count[0] + i] = at;
+        const int at = base + inc - mine, so = segments + sinc - segs;
+        if (cta == 0 && i < a.count[k]) a.plan[kPlanInts + k * a.count[0] + i] = so;
         const unsigned here = __ballot_sync(0xffffffffu, at <= b0 && b0 < at + mine);
         if (here) {
           const int src = __ffs((int)here) - 1;
           kind = k;
           gi = i0 + src;
           pos = __shfl_sync(0xffffffffu, at, src);
-          if (blockIdx.x != 0) return;
+          ord = __shfl_sync(0xffffffffu, so, src);
+          if (cta != 0) return;
         }
         base += __shfl_sync(0xffffffffu, inc, 31);
+        segments += __shfl_sync(0xffffffffu, sinc, 31);
       }
+      segments = 0;   // slots are counted per family
     }
   }
   __device__ bool next(Seg& s) {
     while (pos < b1) {
-      const int rt = a.row_tiles[kind], pairs = rt >> 1;
+      const Chunks ch(a, kind, tiles, range);
       if (tiles == 0 || h == a.hkv) {
         h = 0;
         if (++gi == a.count[kind]) {
           gi = 0;
+          ord = 0;
           ++kind;      // pos < b1 <= total: there is work left in kind 1
         }
         load();
         continue;
       }
-      const bool pair = set < pairs;
-      const int wt = pair ? 2 : 1;
-      const int lo = b0 > pos ? (b0 - pos + wt - 1) / wt : 0;
-      const int hi = min(tiles, (b1 - pos + wt - 1) / wt);
+      int t0;
+      const Span sp = ch.segment(c, y, pos, &t0);
+      const int lo = sp.tile(b0, snap), hi = sp.tile(b1, snap);
       s.kind = kind;
       s.gi = gi;
       s.h = h;
-      s.rt = 2 * set;
-      s.slot = blockIdx.x + (gi * a.hkv + h) * ((rt + 1) >> 1) + set;
-      s.t0 = lo;
+      s.pair = y < 2 * ch.pairs;
+      s.rt = s.pair ? 2 * (y < ch.pairs ? y : y - ch.pairs) : ch.rt - 1;
+      s.slot = (ord + y) * 2 + (lo > 0);
+      s.whole = hi - lo == sp.n;
+      s.t0 = t0 + lo;
       s.n = hi - lo;
       s.len = len;
       s.hist = (len + kTile - 1) / kTile;
-      s.pair = pair;
-      pos += tiles * wt;
-      if (++set == (rt + 1) >> 1) {
-        set = 0;
-        ++h;
+      const bool found = lo < hi;
+      const bool past = sp.pos >= b1;
+      if (++y == ch.rt) {
+        y = 0;
+        ord += ch.rt;
+        pos += ch.length_of(min(ch.chunk, tiles - c * ch.chunk));
+        if (++c == chunks) {
+          c = 0;
+          ++h;
+        }
       }
-      if (lo < hi) return true;
+      if (found) return true;
+      if (past) break;
     }
+    pos = b1;
     return false;
   }
 };
@@ -315,16 +418,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float max32(const uint32_t (&x)[32], float top) {
-  float a = top, b = __uint_as_float(x[0]);
-#pragma unroll
-  for (int i = 1; i < 29; i += 4) {
-    a = max3(a, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-    b = max3(b, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
-  }
-  a = max3(a, __uint_as_float(x[29]), __uint_as_float(x[30]));
-  return max3(a, b, __uint_as_float(x[31]));
-}
 // p = 2^(x * scale - m) as 16 bf16 pairs, the fp32 values added to sum, the
 // largest x to top.
 __device__ __forceinline__ void exp32(const uint32_t (&x)[32], uint64_t scale, uint64_t minus_m,
@@ -352,16 +445,11 @@ __device__ __forceinline__ void mask_bits(uint32_t (&x)[32], unsigned bad) {
     if (bad >> i & 1) x[i] = 0xff800000u;
 }
 
-// Barrier of the two warps that share 32 rows; whether any thread said yes.
-__device__ __forceinline__ bool pair_any(int id, bool yes) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
-      " bar.red.or.pred q, %2, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"((uint32_t)yes), "r"(id)
-      : "memory");
-  return r != 0;
+// 32 columns to `out`, four to a piece, pieces `apart` floats apart.
+__device__ __forceinline__ void store_pieces(float* out, int apart, const uint32_t* o) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 4)
+    *reinterpret_cast<uint4*>(out + (i / 4) * apart) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
 }
 
 template <int D>
@@ -381,8 +469,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&sh.q_full[s]), 1);
       mbar_init(smem_u32(&sh.q_empty[s]), 1);
-      mbar_init(smem_u32(&sh.s_full[s]), 1);
-      mbar_init(smem_u32(&sh.p_ready[s]), kSoftmaxWarps);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(smem_u32(&sh.s_full[s][i]), 1);
+        mbar_init(smem_u32(&sh.p_ready[s][i]), kSoftmaxWarps);
+      }
       mbar_init(smem_u32(&sh.o_final[s]), 1);
     }
     for (int i = 0; i < kMaskRing; ++i) mbar_init(smem_u32(&sh.mask_full[i]), 1);
@@ -394,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_fence_init();
     sh.abort = 0;
   }
-  if (warp == 16) tmem_alloc<512>(smem_u32(&sh.tmem));
+  if (warp == kMmaWarp) tmem_alloc<512>(smem_u32(&sh.tmem));
   // Rows a row tile lacks keep finite values: zeros, later another tile's.
   for (int i = tid; i < 2 * C::TILE_BYTES / 16; i += kThreads)
     *reinterpret_cast<uint4*>(raw + i * 16) = make_uint4(0, 0, 0, 0);
@@ -416,8 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(smem_u32(&sh.seg_empty[at % kSegRing]));
   };
 
-  if (warp >= 16) give_registers();   // one instruction for the whole warpgroup
-  if (warp == 19) {
+  if (warp >= kMmaWarp) give_registers();   // one instruction for the whole warpgroup
+  if (warp == kWalkWarp) {
     // --------------------------------------------------------------- walker
     role_begin();
     Walk walk(a);
@@ -432,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!more) break;
     }
-  } else if (warp == 18) {
+  } else if (warp == kQWarp) {
     // ------------------------------------------------------------------- Q
     // Row tiles in the tensor cores' swizzled layout; a pair fills both
     // buffers, singles take turns, so that the next one's rows are there
@@ -480,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       if (!s.pair) turn ^= 1;
     }
-  } else if (warp == 17) {
+  } else if (warp == kLoadWarp) {
     // --------------------------------------------------------- K and V loads
     role_begin();
     int slot = 0, tile_count = 0;
@@ -568,18 +658,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(smem_u32(&sh.full[slot]), phase, kWaitLimitCycles);
       }
     }
-  } else if (warp == 16) {
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ MMA
     // The whole warp walks, one lane issues.  Slots are used in ring order: a
     // running position serves K and V alike.
     role_begin();
-    constexpr uint32_t kQk = mma_idesc(128, 128, false), kPv = mma_idesc(128, D, true);
+    constexpr uint32_t kQk = mma_idesc(128, kHalf, false), kPv = mma_idesc(128, D, true);
     constexpr uint32_t kStep = C::TILE_BYTES >> 4;       // slots apart, in descriptor units
     const uint32_t on = elect_one();
     const uint64_t qd0 = smem_desc(q_buf, 16, 1024), kd0 = smem_desc(ring, 16, 1024);
     const uint64_t vd0 = smem_desc(ring, C::HALF, 1024);
     int slot = 0, turn = 0;
-    uint32_t phase = 0, q_phase0 = 0, q_phase1 = 0, p_phase0 = 0, p_phase1 = 0;
+    uint32_t phase = 0, q_phase0 = 0, q_phase1 = 0, p_phase = 0;   // p_phase: a bit per stream
     bool ok = true;
     auto next_slot = [&]() {
       if (++slot == C::SLOTS) {
@@ -588,27 +678,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     auto full = [&]() { return pwait_warp(&sh.full[slot], phase, &sh.abort); };
-    auto qk = [&](int st, int buf) {
-      const uint64_t qd = qd0 + buf * kStep, kd = kd0 + slot * kStep;
+    // Scores of 64 positions (rows x * 64 .. of a K tile) into buffer x.
+    auto qk = [&](int st, int x, int buf, int kslot) {
+      const uint64_t qd = qd0 + buf * kStep, kd = kd0 + kslot * kStep + x * (kHalf * 128 >> 4);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint32_t off = (uint32_t)((k / 4) * C::HALF + (k % 4) * 32) >> 4;
-        mma_ss(on, tmem + st * 128, qd + off, kd + off, kQk, k > 0);
+        mma_ss(on, tmem + st * 128 + x * kHalf, qd + off, kd + off, kQk, k > 0);
       }
-      mma_commit(on, smem_u32(&sh.s_full[st]));
+      mma_commit(on, smem_u32(&sh.s_full[st][x]));
     };
-    auto pv = [&](int st, bool acc) {
-      const uint64_t vd = vd0 + slot * kStep;
+    auto pv = [&](int st, int x, int vslot, bool acc) {
+      const uint64_t vd = vd0 + vslot * kStep + x * (kHalf * 128 >> 4);
 #pragma unroll
-      for (int k = 0; k < kTile / 16; ++k)
-        mma_ts(on, tmem + 256 + st * 128, tmem + st * 128 + k * 8, vd + (uint32_t)(k * 2048 >> 4),
-               kPv, acc || k > 0);
+      for (int k = 0; k < kHalf / 16; ++k)
+        mma_ts(on, tmem + 256 + st * 128, tmem + st * 128 + x * kHalf + k * 8,
+               vd + (uint32_t)(k * 2048 >> 4), kPv, acc || k > 0);
     };
-    auto release = [&]() { mma_commit(on, smem_u32(&sh.empty[slot])); };
-    auto p_ready = [&](int st) {
-      uint32_t& ph = st ? p_phase1 : p_phase0;
-      const bool r = pwait_warp(&sh.p_ready[st], ph, &sh.abort);
-      ph ^= 1;
+    auto release = [&](int at) { mma_commit(on, smem_u32(&sh.empty[at])); };
+    // Buffer x of a stream is used once per tile: one phase for both.
+    auto p_ready = [&](int st, int x) {
+      const bool r = pwait_warp(&sh.p_ready[st][x], p_phase >> st & 1, &sh.abort);
       tc_fence_after();
       return r;
     };
@@ -619,6 +709,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       return r;
     };
+    // A tile's second half done: no more scores follow in this stream.  After
+    // the first half of the last tile buffer 0 is signalled all the same: by
+    // it a softmax thread knows that the product before is complete.
+    auto tail = [&](int st, int x) {
+      mma_commit(on, x ? smem_u32(&sh.o_final[st]) : smem_u32(&sh.s_full[st][0]));
+    };
     for (int at = 0; ok; ++at) {
       const Seg* sp = segment(at);
       ok = sp != nullptr;
@@ -627,71 +723,89 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kind < 0) break;
       done_with(at);
       if (paired) {
-        // K0 for both, then per tile: V, next K, each used by A, then by B.
+        // K0 for both, then per tile: V, next K, half by half, A then B.
         if (!(ok = q_ready(0) && full())) break;
-        qk(0, 0);
+        qk(0, 0, 0, slot);
+        qk(0, 1, 0, slot);
         if (!(ok = q_ready(1))) break;
-        qk(1, 1);
-        release();
+        qk(1, 0, 1, slot);
+        qk(1, 1, 1, slot);
+        release(slot);
         next_slot();
-        for (int i = 0; i < n; ++i) {
+        for (int i = 0; ok && i < n; ++i) {
           const bool more = i + 1 < n;
           const int vslot = slot;
-          if (!(ok = p_ready(0) && full())) break;
-          pv(0, i > 0);
-          next_slot();
-          if (more) {
-            if (!(ok = full())) break;
-            qk(0, 0);
-          } else {
-            mma_commit(on, smem_u32(&sh.o_final[0]));
-            mma_commit(on, smem_u32(&sh.q_empty[0]));
+          int kslot = 0;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+              if (!(ok = ok && p_ready(st, x))) break;
+              if (x == 0 && st == 0) {
+                if (!(ok = full())) break;
+                next_slot();
+              }
+              pv(st, x, vslot, i > 0 || x > 0);
+              if (x == 1 && st == 1) release(vslot);
+              if (more) {
+                if (x == 0 && st == 0) {
+                  if (!(ok = full())) break;
+                  kslot = slot;
+                  next_slot();
+                }
+                qk(st, x, st, kslot);
+                if (x == 1 && st == 1) release(kslot);
+              } else {
+                tail(st, x);
+                if (x == 1) mma_commit(on, smem_u32(&sh.q_empty[st]));
+              }
+            }
           }
-          if (!(ok = p_ready(1))) break;
-          const int kslot = slot;
-          slot = vslot;
-          pv(1, i > 0);
-          release();
-          slot = kslot;
-          if (more) {
-            qk(1, 1);
-            release();
-            next_slot();
-          } else {
-            mma_commit(on, smem_u32(&sh.o_final[1]));
-            mma_commit(on, smem_u32(&sh.q_empty[1]));
-          }
+          p_phase ^= 3;
         }
       } else {
         // Streams take the tiles in turn: K0, K1, then V0, K2, V1, K3, ...
         const int buf = turn;
         turn ^= 1;
-        if (!(ok = q_ready(buf) && full())) break;
-        qk(0, buf);
-        release();
-        next_slot();
-        if (n > 1) {
+        if (!(ok = q_ready(buf))) break;
+        for (int st = 0; st < min(n, 2); ++st) {
           if (!(ok = full())) break;
-          qk(1, buf);
-          release();
+          qk(st, 0, buf, slot);
+          qk(st, 1, buf, slot);
+          release(slot);
           next_slot();
         }
         if (n <= 2) mma_commit(on, smem_u32(&sh.q_empty[buf]));
-        for (int i = 0; i < n; ++i) {
+        for (int i = 0; ok && i < n; ++i) {
           const int st = i & 1;
-          if (!(ok = p_ready(st) && full())) break;
-          pv(st, i > 1);
-          release();
-          next_slot();
-          if (i + 2 < n) {
-            if (!(ok = full())) break;
-            qk(st, buf);
-            release();
-            next_slot();
-            if (i + 3 == n) mma_commit(on, smem_u32(&sh.q_empty[buf]));
-          } else {
-            mma_commit(on, smem_u32(&sh.o_final[st]));
+          const bool more = i + 2 < n;
+          const int vslot = slot;
+          int kslot = 0;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!(ok = p_ready(st, x))) break;
+            if (x == 0) {
+              if (!(ok = full())) break;
+              next_slot();
+            }
+            pv(st, x, vslot, i > 1 || x > 0);
+            if (x) release(vslot);
+            if (more) {
+              if (x == 0) {
+                if (!(ok = full())) break;
+                kslot = slot;
+                next_slot();
+              }
+              qk(st, x, buf, kslot);
+              if (x) {
+                release(kslot);
+                if (i + 3 == n) mma_commit(on, smem_u32(&sh.q_empty[buf]));
+              }
+            } else {
+              tail(st, x);
+            }
           }
+          p_phase ^= 1u << st;
         }
       }
     }
@@ -703,15 +817,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // -------------------------------------------------------------- softmax
     take_registers();
-    const int st = warp >> 3, half = warp >> 2 & 1, row = (warp & 3) * 32 + lane;
-    const int pair_id = 1 + st * 4 + (warp & 3);
+    const int st = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // TMEM lane of the warp's first row
-    const uint32_t tS = tmem + lanes + st * 128, tO = tmem + lanes + 256 + st * 128 + half * (D / 2);
-    float* mine = &sh.exchange[st][half][row];
-    const float* other = &sh.exchange[st][half ^ 1][row];
+    const uint32_t tS = tmem + lanes + st * 128, tO = tmem + lanes + 256;
     const uint64_t scale2 = pack2(__float_as_uint(a.scale_log2), __float_as_uint(a.scale_log2));
     int ring0 = 0, tiles0 = 0;                 // ring position, paged tiles before the segment
-    uint32_t s_phase = 0, o_phase = 0;
+    uint32_t s_phase = 0, o_phase = 0;         // s_phase: a bit per buffer
     bool ok = true;
     for (int at = 0; ok; ++at) {
       const Seg* sp = segment(at);
@@ -721,163 +832,182 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int steps = s.steps(st);
       const int rt = s.rt + (s.pair ? st : 0);
       const int rows = min(kTile, a.rows[s.kind] - rt * kTile);
-      const int sr = a.slot_rows[s.kind];
-      const long long slot = (long long)s.slot * 2 + st;
-      float2* ml = a.ws_ml[s.kind] + slot * sr;
       const bool paged = a.cache[s.kind].page_table != nullptr;
-      if (steps == 0 && half == 0 && row < rows) ml[row] = make_float2(-INFINITY, 0.f);
       const bool live = (warp & 3) * 32 < rows;           // the warp has rows
       const int t_row = s.kind ? (rt * kTile + row) % a.w : 0;   // window row of this row
       float m = -INFINITY;
       uint64_t sum[2] = {0, 0};
-      for (int step = 0; step < steps; ++step) {
+      for (int step = 0; ok && step < steps; ++step) {
         const int tl = s.tile(st, step), t = s.t0 + tl;
         const bool window = s.kind && t >= s.hist;
-        // Columns [0, lim) of this thread's 64 count.
-        const int lim = (window ? min(a.w, t_row + 1) - (t - s.hist) * kTile : s.len - t * kTile) -
-                        half * 64;
-        ok = pwait_warp(&sh.s_full[st], s_phase, &sh.abort);
-        if (!ok) break;
-        s_phase ^= 1;
-        tc_fence_after();
-        if (paged && !window) {
+        const int valid = s.len - t * kTile;
+        // Columns [0, lim) of the tile count.
+        const int lim = window ? min(a.w, t_row + 1) - (t - s.hist) * kTile : valid;
+        const bool masked = __any_sync(0xffffffffu, lim < kTile);
+        const bool bad = paged && !window;
+        if (bad) {
           ok = pwait_warp(&sh.mask_full[(tiles0 + tl) % kMaskRing],
                           ((tiles0 + tl) / kMaskRing) & 1, &sh.abort);
           if (!ok) break;
         }
-        if (live) {
-          uint32_t x0[32], x1[32], p[32];
-          auto load = [&]() {
-            tmem_ld32(tS + half * 64, x0);
-            tmem_ld32(tS + half * 64 + 32, x1);
-            tc_wait_ld();
-            if (__any_sync(0xffffffffu, lim < 64)) {
-              mask32(x0, lim);
-              mask32(x1, lim - 32);
-            }
-            if (paged && !window) {
-              const int k = (tiles0 + tl) % kMaskRing;
-              const unsigned b0 = sh.bad[k][2 * half], b1 = sh.bad[k][2 * half + 1];
-              if (b0 | b1) {
-                mask_bits(x0, b0);
-                mask_bits(x1, b1);
-              }
-            }
-          };
-          auto exps = [&](uint64_t (&to)[2]) {
-            const float ms = m == -INFINITY ? 0.f : -m;
-            const uint64_t mm = pack2(__float_as_uint(ms), __float_as_uint(ms));
-            float top0 = -INFINITY, top1 = -INFINITY;
-            exp32(x0, scale2, mm, to, top0, p);
-            exp32(x1, scale2, mm, to, top1, p + 16);
-            return fmaxf(top0, top1) * a.scale_log2;
-          };
-          load();
-          // The reference maximum m moves only when a tile exceeds it by
-          // more than a factor 2^8, so P is formed with the old one while
-          // the tile's maximum is still being taken; where it does move (the
-          // first tile, then rarely), S, not overwritten yet, is read again.
-          bool again = true;
-          float top;
-          if (step == 0) {
-            top = max32(x1, max32(x0, -INFINITY)) * a.scale_log2;
-          } else {
-            uint64_t to[2] = {sum[0], sum[1]};
-            top = exps(to);
-            // Also the point after which P may overwrite S: both threads of
-            // a row have read it.
-            again = pair_any(pair_id, m == -INFINITY ? top > m : top > m + kLazyRescale);
-            if (!again) {
-              sum[0] = to[0];
-              sum[1] = to[1];
-            }
-          }
-          if (again) {
-            *mine = top;
-            named_bar_sync(pair_id, 64);
-            top = fmaxf(top, *other);
-            const bool up = m == -INFINITY ? top > m : top > m + kLazyRescale;
-            const float f = up ? ex2(m - top) : 1.f;
-            if (up) m = top;
-            const uint64_t f2 = pack2(__float_as_uint(f), __float_as_uint(f));
-            sum[0] = fma2(sum[0], f2, 0);
-            sum[1] = fma2(sum[1], f2, 0);
-            if (step > 0) {
-              // The product that wrote O was issued before the one that
-              // signalled S: it is complete.
-#pragma unroll
-              for (int c = 0; c < D / 64; ++c) {
-                uint32_t o[32];
-                tmem_ld32(tO + c * 32, o);
-                tc_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st32(tO + c * 32, o);
-              }
-            }
-            load();
-            named_bar_sync(pair_id, 64);   // both have read S again
-            exps(sum);
-          }
-          tmem_st32(tS + half * 32, p);
-          tc_wait_st();
-        }
-        // V rows behind the end hold whatever the cache holds there, NaN
-        // included: 0 * NaN must not reach O.
-        const int valid = s.len - t * kTile;
-        if (!window && valid < kTile && (!s.pair || st == 0)) {
-          const int vat = ring0 + s.v_at(tl);
-          ok = pwait_warp(&sh.full[vat % C::SLOTS], (vat / C::SLOTS) & 1, &sh.abort);
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          ok = pwait_warp(&sh.s_full[st][x], s_phase >> x & 1, &sh.abort);
           if (!ok) break;
-          const uint32_t v = ring + vat % C::SLOTS * C::TILE_BYTES;
-          for (int i = valid * 8 + half * 128 + row; i < kTile * 8; i += 256)
+          s_phase ^= 1u << x;
+          tc_fence_after();
+          if (live) {
+            // The reference maximum m moves only when scores exceed it by
+            // more than a factor 2^8, so P is formed with the old one while
+            // the maximum is still being taken; where it does move (the
+            // first scores, then rarely), S, not overwritten yet, is read
+            // again.
+            const uint32_t tX = tS + x * kHalf;
+            uint32_t p[32];
+            for (;;) {
+              uint32_t x0[32], x1[32];
+              tmem_ld32(tX, x0);
+              tmem_ld32(tX + 32, x1);
+              tc_wait_ld();
+              if (masked) {
+                mask32(x0, lim - x * kHalf);
+                mask32(x1, lim - x * kHalf - 32);
+              }
+              if (bad) {
+                const int k = (tiles0 + tl) % kMaskRing;
+                const unsigned b0 = sh.bad[k][2 * x], b1 = sh.bad[k][2 * x + 1];
+                if (b0 | b1) {
+                  mask_bits(x0, b0);
+                  mask_bits(x1, b1);
+                }
+              }
+              const float ms = m == -INFINITY ? 0.f : -m;
+              const uint64_t mm = pack2(__float_as_uint(ms), __float_as_uint(ms));
+              uint64_t to[2] = {sum[0], sum[1]};
+              float top0 = -INFINITY, top1 = -INFINITY;
+              exp32(x0, scale2, mm, to, top0, p);
+              exp32(x1, scale2, mm, to, top1, p + 16);
+              const float top = fmaxf(top0, top1) * a.scale_log2;
+              const bool up = m == -INFINITY ? top > m : top > m + kLazyRescale;
+              if (!__any_sync(0xffffffffu, up)) {
+                sum[0] = to[0];
+                sum[1] = to[1];
+                break;
+              }
+              const float f = up ? ex2(m - top) : 1.f;
+              if (up) m = top;
+              const uint64_t f2 = pack2(__float_as_uint(f), __float_as_uint(f));
+              sum[0] = fma2(sum[0], f2, 0);
+              sum[1] = fma2(sum[1], f2, 0);
+              if (step > 0 || x > 0) {
+                // O is scaled once the product before is complete: it was
+                // issued before the scores after these, or what is signalled
+                // in their place.
+                ok = pwait_warp(&sh.s_full[st][x ^ 1], s_phase >> (x ^ 1) & 1, &sh.abort);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                  const uint32_t to_o = tO + st * 128 + c * 32;
+                  uint32_t o[32];
+                  tmem_ld32(to_o, o);
+                  tc_wait_ld();
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(v + c * C::HALF +
-                                                                              i * 16),
-                           "r"(0)
-                           : "memory");
-          fence_proxy_async_smem();
+                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                  tmem_st32(to_o, o);
+                }
+              }
+            }
+            if (!ok) break;
+            tmem_st32(tX, p);
+            tc_wait_st();
+          }
+          // V rows behind the end hold whatever the cache holds there, NaN
+          // included: 0 * NaN must not reach O.
+          if (x == 0 && !window && valid < kTile && (!s.pair || st == 0)) {
+            const int vat = ring0 + s.v_at(tl);
+            ok = pwait_warp(&sh.full[vat % C::SLOTS], (vat / C::SLOTS) & 1, &sh.abort);
+            if (!ok) break;
+            const uint32_t v = ring + vat % C::SLOTS * C::TILE_BYTES;
+            for (int i = valid * 8 + row; i < kTile * 8; i += 128)
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(v + c * C::HALF +
+                                                                                i * 16),
+                             "r"(0)
+                             : "memory");
+            fence_proxy_async_smem();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.p_ready[st][x]));
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.p_ready[st]));
       }
       if (!ok) break;
       ring0 += 2 * s.n;
       if (paged) tiles0 += max(0, min(s.t0 + s.n, s.hist) - s.t0);
       if (steps == 0) continue;
+      s_phase ^= 1;                            // buffer 0 is signalled once more after the last scores
       ok = pwait_warp(&sh.o_final[st], o_phase, &sh.abort);
       if (!ok) break;
       o_phase ^= 1;
       tc_fence_after();
-      if (live) {
-        // Pieces of four columns, rows side by side: full lines per store.
-        float* out = a.ws_o[s.kind] + slot * sr * D + (long long)(half * (D / 8)) * sr * 4 + row * 4;
+      // Partials: a pair's streams write their rows each; a single's are
+      // merged, each writing half of the columns.  Pieces of four columns,
+      // rows side by side: full lines per store.
+      const int sr = a.slot_rows[s.kind];
+      const long long slot = (long long)s.slot * 2 + (s.pair ? st : 0);
+      float* out = a.ws_o[s.kind] + slot * sr * D + row * 4;
+      const uint64_t both = add2(sum[0], sum[1]);
+      float l = lo_of(both) + hi_of(both);
+      if (s.pair || s.n == 1) {
+        if (live) {
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tO + c * 32, o);
-          tc_wait_ld();
-          if (row < rows) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4*>(out + (c * 8 + i / 4) * (sr * 4)) =
-                  make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + st * 128 + c * 32, o);
+            tc_wait_ld();
+            if (row < rows) store_pieces(out + c * 8 * (sr * 4), sr * 4, o);
           }
         }
-        const uint64_t all = add2(sum[0], sum[1]);
-        const float l = lo_of(all) + hi_of(all);
-        if (half) *mine = l;
-        named_bar_sync(pair_id, 64);
-        if (!half && row < rows) ml[row] = make_float2(m, l + *other);
-        named_bar_sync(pair_id, 64);   // read before the next segment writes
+      } else {
+        sh.exchange[st][row] = make_float2(m, l);
+        named_bar_sync(1, 2 * kTile);          // both streams' O, m and l are there
+        const float2 y = sh.exchange[st ^ 1][row];
+        const float big = fmaxf(m, y.x), ref = big == -INFINITY ? 0.f : big;
+        const float f0 = ex2(m - ref), f1 = ex2(y.x - ref);
+        m = big;
+        l = l * f0 + y.y * f1;
+        tc_fence_after();
+        if (live) {
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            const int col = st * (D / 2) + c * 32;
+            uint32_t o[32], z[32];
+            tmem_ld32(tO + st * 128 + col, o);
+            tmem_ld32(tO + (st ^ 1) * 128 + col, z);
+            tc_wait_ld();
+            if (row < rows) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                o[i] = __float_as_uint(fmaf(__uint_as_float(o[i]), f0, __uint_as_float(z[i]) * f1));
+              store_pieces(out + (col / 4) * (sr * 4), sr * 4, o);
+            }
+          }
+        }
+        tc_fence_before();
+        named_bar_sync(1, 2 * kTile);          // read before the next segment writes
+      }
+      if (row < rows && (s.pair || st == 0)) {
+        float2* ml = a.ws_ml[s.kind] + slot * sr + row;
+        *ml = make_float2(m, l);
+        if (s.whole) ml[2 * sr] = make_float2(-INFINITY, 0.f);
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) tmem_dealloc<512>(tmem);
+  if (warp == kMmaWarp) tmem_dealloc<512>(tmem);
 }
 
 // ---- combine: one thread per four columns of an output row
@@ -886,82 +1016,144 @@ struct CombineArgs {
   PrefixKArgs k;
   __nv_bfloat16* o;
   float* lse;
-  long long rows;      // b * h_q * w
+  int rows;            // b * h_q * w
 };
 
 constexpr int kCombineThreads = 256;
 
+constexpr int kPartBatch = 64;
+
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads)
     attn_prefix_combine_kernel(const __grid_constant__ CombineArgs c) {
-  constexpr int ROWS = kCombineThreads / (D / 4);
+  constexpr int PIECES = D / 4, ROWS = kCombineThreads / PIECES;
+  // Partials of a batch, by row: first m, l and place of each, then, with
+  // nothing-seen ones dropped, weight and place (index of its first four
+  // columns in float4s, the family in bit 0).
+  __shared__ float2 ml_of[ROWS][kPartBatch + 1];
+  __shared__ unsigned at_of[ROWS][kPartBatch + 1];
+  __shared__ float weight_of[ROWS][kPartBatch];
+  __shared__ float m_of[ROWS], l_of[ROWS], rescale_of[ROWS];
+  __shared__ int kept_of[ROWS];
   const PrefixKArgs& a = c.k;
-  const int piece = threadIdx.x / ROWS;
-  const long long row = (long long)blockIdx.x * ROWS + threadIdx.x % ROWS;
+  const int piece = threadIdx.x / ROWS, mine = threadIdx.x % ROWS;
+  const int row = blockIdx.x * ROWS + mine;
   griddep_wait();
   griddep_launch_dependents();
-  if (row >= c.rows) return;
-  const int seq = (int)(row / a.hq_w), in_seq = (int)(row % a.hq_w);
-  const int h = in_seq / a.gw, r = in_seq % a.gw;
-  const Cut cut(a.plan[0], a.grid);
-  // Partials of the row in its prefix item and in its own: CTAs first ..
-  // first + ctas - 1, one stream of a pair's slot or both of a single's.
-  int ctas[2], twice[2];
-  long long at[2];
+  const bool have = row < c.rows;
+  const int seq = have ? row / a.hq_w : 0, in_seq = have ? row - seq * a.hq_w : 0;
+  const int h = in_seq / a.gw, r = in_seq - h * a.gw, g = seq / a.per;
+  const int range = a.plan[0];
+  // The row's places: two slots per segment.
+  int n[2], base[2], segs[2], in_tile[2], chunks[2], second[2];
+  bool pair[2];
 #pragma unroll
-  for (int kind = 0; kind < 2; ++kind) {
-    const int gi = kind ? seq : seq / a.per;
-    const int rr = kind ? r : seq % a.per * a.gw + r;
-    const int rt = rr / kTile, pairs = a.row_tiles[kind] >> 1, set = rt >> 1;
-    const bool pair = set < pairs;
-    const int tiles = tiles_of(a, kind, length_of(a, kind, gi));
-    ctas[kind] = 0;
-    twice[kind] = pair ? 0 : 1;
-    if (tiles > 0) {
-      const int start = a.plan[1 + kind * a.count[0] + gi] +
-                        (h * a.row_tiles[kind] + set * 2) * tiles;
-      const int first = cut.of(start);
-      ctas[kind] = cut.of(start + (tiles - 1) * (pair ? 2 : 1)) - first + 1;
-      const int item = (gi * a.hkv + h) * ((a.row_tiles[kind] + 1) >> 1) + set;
-      at[kind] = (long long)(first + item) * 2 + (pair ? rt & 1 : 0);
-    }
+  for (int k = 0; k < 2; ++k) {
+    const int gi = k ? seq : g, rr = k ? r : (seq - g * a.per) * a.gw + r, rt = rr / kTile;
+    const Chunks ch(a, k, tiles_of(a, k, length_of(a, k, gi)), range);
+    pair[k] = rt < 2 * ch.pairs;
+    chunks[k] = ch.count();
+    // A last chunk of half a chunk's tiles or less has no second half.
+    second[k] = ch.tiles - (chunks[k] - 1) * ch.chunk > ch.chunk >> 1;
+    segs[k] = ch.rt;
+    in_tile[k] = rr - rt * kTile;
+    base[k] = a.plan[kPlanInts + k * a.count[0] + gi] + h * chunks[k] * ch.rt +
+              (pair[k] ? rt >> 1 : 2 * ch.pairs);
+    base[k] = base[k] * 4 + (pair[k] ? rt & 1 : 0);
+    n[k] = have ? chunks[k] * (pair[k] ? 4 : 2) : 0;
   }
-  float top = -INFINITY;
-#pragma unroll
-  for (int kind = 0; kind < 2; ++kind) {
-    const int sr = a.slot_rows[kind], in_tile = (kind ? r : seq % a.per * a.gw + r) % kTile;
-    const int n = ctas[kind] << twice[kind], stride = 2 - twice[kind];
-#pragma unroll 4
-    for (int i = 0; i < n; ++i)
-      top = fmaxf(top, a.ws_ml[kind][(at[kind] + i * stride) * sr + in_tile].x);
+  // Place e of family k: chunk, (pair) half, slot.
+  auto stream_slot = [&](int k, int e) -> int {
+    if (!pair[k]) return base[k] + (e >> 1) * segs[k] * 4 + (e & 1) * 2;
+    const int cc = e >> 2, hi = e >> 1 & 1, lo = e & 1;
+    if (hi && cc == chunks[k] - 1 && !second[k]) return -1;
+    return base[k] + (cc * segs[k] + hi * (segs[k] >> 1)) * 4 + lo * 2;
+  };
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x < ROWS) {
+    m_of[threadIdx.x] = -INFINITY;
+    l_of[threadIdx.x] = 0.f;
   }
-  const float m = top == -INFINITY ? 0.f : top;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
+  const int count = n[0] + n[1];
+  for (int i0 = 0;; i0 += kPartBatch) {
+    for (int i = piece; i < kPartBatch; i += PIECES) {
+      const int e = i0 + i;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      unsigned at = 0;
+      if (e < count) {
+        const int k = e < n[1] ? 1 : 0;
+        const int slot = stream_slot(k, k ? e : e - n[1]);
+        if (slot >= 0) {
+          at = ((unsigned)slot * (a.slot_rows[k] * (D / 4)) + in_tile[k]) * 2 + k;
+          ml = a.ws_ml[k][(long long)slot * a.slot_rows[k] + in_tile[k]];
+        }
+      }
+      ml_of[mine][i] = ml;
+      at_of[mine][i] = at;
+    }
+    __syncthreads();
+    // One warp per row: running maximum, weights, the list without gaps.
+    for (int x = warp; x < ROWS; x += kCombineThreads / 32) {
+      const float2 p0 = ml_of[x][lane], p1 = ml_of[x][lane + 32];
+      const unsigned a0 = at_of[x][lane], a1 = at_of[x][lane + 32];
+      const float old = m_of[x];
+      float top = fmaxf(old, fmaxf(p0.x, p1.x));
 #pragma unroll
-  for (int kind = 0; kind < 2; ++kind) {
-    const int sr = a.slot_rows[kind], in_tile = (kind ? r : seq % a.per * a.gw + r) % kTile;
-    const int n = ctas[kind] << twice[kind], stride = 2 - twice[kind];
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const long long base = (at[kind] + i * stride) * sr;
-      const float2 ml = a.ws_ml[kind][base + in_tile];
-      const float4 v = *reinterpret_cast<const float4*>(a.ws_o[kind] + base * D +
-                                                        ((long long)piece * sr + in_tile) * 4);
-      const float wt = ex2(ml.x - m);
-      if (wt > 0.f) {   // otherwise nothing was seen there (O may be unwritten)
-        l = fmaf(wt, ml.y, l);
-        acc.x = fmaf(wt, v.x, acc.x);
-        acc.y = fmaf(wt, v.y, acc.y);
-        acc.z = fmaf(wt, v.z, acc.z);
-        acc.w = fmaf(wt, v.w, acc.w);
+      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const float ref = top == -INFINITY ? 0.f : top;
+      const bool s0 = p0.x != -INFINITY, s1 = p1.x != -INFINITY;   // else O may be unwritten
+      const float w0 = ex2(p0.x - ref), w1 = ex2(p1.x - ref);
+      float sum = (s0 ? w0 * p0.y : 0.f) + (s1 ? w1 * p1.y : 0.f);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      const unsigned b0 = __ballot_sync(0xffffffffu, s0), b1 = __ballot_sync(0xffffffffu, s1);
+      const unsigned below = (1u << lane) - 1;
+      if (s0) {
+        const int to = __popc(b0 & below);
+        weight_of[x][to] = w0;
+        at_of[x][to] = a0;
+      }
+      if (s1) {
+        const int to = __popc(b0) + __popc(b1 & below);
+        weight_of[x][to] = w1;
+        at_of[x][to] = a1;
+      }
+      if (lane == 0) {
+        const float f = old == -INFINITY ? 0.f : ex2(old - ref);
+        m_of[x] = top;
+        l_of[x] = l_of[x] * f + sum;
+        rescale_of[x] = f;
+        kept_of[x] = __popc(b0) + __popc(b1);
       }
     }
+    __syncthreads();
+    const float f = rescale_of[mine];
+    acc.x *= f;
+    acc.y *= f;
+    acc.z *= f;
+    acc.w *= f;
+    const int kept = kept_of[mine];
+    const float4* from[2] = {reinterpret_cast<const float4*>(a.ws_o[0]) + piece * a.slot_rows[0],
+                             reinterpret_cast<const float4*>(a.ws_o[1]) + piece * a.slot_rows[1]};
+#pragma unroll 8
+    for (int i = 0; i < kept; ++i) {
+      const unsigned at = at_of[mine][i];
+      const float4 v = (at & 1 ? from[1] : from[0])[at >> 1];
+      const float wt = weight_of[mine][i];
+      acc.x = fmaf(wt, v.x, acc.x);
+      acc.y = fmaf(wt, v.y, acc.y);
+      acc.z = fmaf(wt, v.z, acc.z);
+      acc.w = fmaf(wt, v.w, acc.w);
+    }
+    if (!__syncthreads_or(count > i0 + kPartBatch)) break;   // also: the batch is read
   }
-  const float inv = top == -INFINITY ? 0.f : 1.f / l;
-  *reinterpret_cast<uint2*>(c.o + row * D + piece * 4) =
+  const float m = m_of[mine], l = l_of[mine];
+  if (!have) return;
+  const float inv = m == -INFINITY ? 0.f : 1.f / l;
+  *reinterpret_cast<uint2*>(c.o + (long long)row * D + piece * 4) =
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (piece == 0) c.lse[row] = top == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
+  if (piece == 0) c.lse[row] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // ---- host side
@@ -1034,15 +1226,21 @@ PrefixKArgs shape_args(const PrefixArgs& p, int sms, Layout* lay) {
   a.grid = sms;
   size_t at = 0;
   for (int k = 0; k < 2; ++k) {
-    const size_t items = (size_t)a.count[k] * a.hkv * ((a.row_tiles[k] + 1) / 2);
-    const size_t rows = (items + a.grid) * 2 * a.slot_rows[k];
+    // Segments: one per chunk (two tiles at least) and row tile.  A chunk is
+    // as long as a range allows: 4 M + 8 (prefix), 5 M + 8 (own) quarters of
+    // at most `range`, M even, so the whole chunks' units, work / 4 or / 5 at
+    // most, make up to 2 or 3 segments per CTA (the most at range 31, 27).
+    const size_t items = (size_t)a.count[k] * a.hkv * a.row_tiles[k];
+    const size_t tiles = (a.n[k] + kTile - 1) / kTile + (k ? a.win_tiles : 0);
+    const size_t segs = std::min(items * ((tiles + 1) / 2), items + (2 + k) * (size_t)a.grid);
+    const size_t rows = segs * 4 * a.slot_rows[k];
     lay->o[k] = at;
     at += align256(rows * p.d * sizeof(float));
     lay->ml[k] = at;
     at += align256(rows * sizeof(float2));
   }
   lay->plan = at;
-  at += align256((size_t)(1 + p.groups + p.b) * sizeof(int));
+  at += align256((size_t)(kPlanInts + p.groups + p.b) * sizeof(int));
   lay->total = at;
   return a;
 }
@@ -1064,7 +1262,7 @@ cudaError_t run_prefix(const PrefixKArgs& k, const Maps& maps, const PrefixArgs&
   c.k = k;
   c.o = p.o;
   c.lse = p.lse;
-  c.rows = (long long)p.b * p.hq * p.w;
+  c.rows = p.b * p.hq * p.w;
   e = launch_pdl(attn_prefix_combine_kernel<D>,
                  dim3((unsigned)((c.rows + kRows - 1) / kRows)), dim3(kCombineThreads), 0, st, c);
   if (e == cudaSuccess) note_launches(1);
