@@ -823,8 +823,8 @@ static int check_prefix_shape(int b, int groups, int h_q, int h_kv, int d, int w
   const double tiles = n_prefix / 128 + 1.0, own = n_own / 128 + w / 128 + 2.0;
   const double rows = (double)(h_q / h_kv) * w;
   if (h_kv * (groups * tiles * (rows * (b / groups) / 128 + 1) + b * own * (rows / 128 + 1)) >
-          (double)(1 << 27) ||
-      rows * b * h_kv > (double)(1 << 30))
+          (double)(1 << 25) ||
+      rows * b * h_kv > (double)(1 << 30) || b > (1 << 20))
     return fail(DUSTIN_ERR_SHAPE, "%s: problem too large", what);
   return DUSTIN_OK;
 }

@@ -14,21 +14,23 @@
 // alone, its even and odd K/V tiles side by side.
 //
 // One persistent CTA per SM; lengths are on the device, so every CTA works
-// out its share itself (Walk::make_plan).  The items' tiles form one line, cut
-// into equal ranges.  On it an item lies in chunks of M tiles: within a chunk
-// one segment after another, two half chunks for each pair, the whole for
-// the single, all M units (row tile x K/V tile) long, about one CTA's share.
-// So the CTAs that read the same K/V tiles for different rows do it at the
-// same time: a prefix of 32768 positions is as large as L2, and with the row
-// tiles one after another it came from HBM once per pair of them (512 rows:
-// 64 instead of 44 us for the loads alone).  A segment is no longer than a
-// range, so at most two CTAs share it: its partial results (O unnormalised,
-// m, l) have two places in the workspace, known without the cut, and
+// out its share itself (Walk).  Prefixes are split: each row tile pair's
+// tiles into np equal segments, the single's into ns (half as many, as its
+// tiles cost half), one segment to a CTA, np and ns from the smallest M
+// (units, row tile x K/V tile, per CTA) that fits the CTAs.  All pairs walk
+// the same K/V tiles at the same time: a prefix of 32768 positions is as
+// large as L2, and with the row tiles one after another it came from HBM once
+// per pair of them (512 rows: 64 instead of 44 us for the loads alone).  The
+// own items lie on a line that the remaining CTAs share in equal ranges, cut
+// into segments no longer than a range, so that at most two CTAs share one.
+// Where a split leaves CTAs idle too long, the prefixes go on the line too.
+// Partial results (O unnormalised, m, l) go to the workspace, each segment
+// (on the line: each of two parts) has its place, and
 // attn_prefix_combine_kernel adds each row's partials in a fixed order.
 //
-// Roles of the 12 warps: 0-3 and 4-7 softmax (one thread per row of stream
-// A / B), 8 issues tcgen05.mma, 9 TMA loads of K and V, 10 copies Q rows, 11
-// walks the CTA's range and publishes its segments.  S = Q K^T and O += P V
+// Roles of the 16 warps: 0-3 and 4-7 softmax (one thread per row of stream
+// A / B), 8 issues tcgen05.mma, 9 TMA loads of K and V, 10 walks the CTA's
+// share and publishes its segments, 12-15 copy Q rows.  S = Q K^T and O += P V
 // accumulate in tensor memory (512 columns: two S buffers of 64 positions and
 // an O per stream); P replaces S in place as bf16 and is read from there as
 // the A operand, so only Q, K and V live in shared memory.  With two S
@@ -53,13 +55,13 @@ __device__ unsigned int g_prefix_dev_flags;
 constexpr int kTile = 128;        // positions of a K/V tile, rows of a row tile
 constexpr int kHalf = 64;         // positions of an S buffer
 constexpr int kSoftmaxWarps = 4;  // per stream
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kQWarp = 10, kWalkWarp = 11;
-constexpr int kThreads = 12 * 32;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kWalkWarp = 10, kQWarp = 12, kQWarps = 4;
+constexpr int kThreads = 16 * 32;
 // Registers: a softmax thread holds 64 scores and their weights; the other
-// warpgroup gives up what they need beyond the launch's 168.
+// two warpgroups give up what they need beyond the launch's 128.
 struct Split {
-  static constexpr int NT = kThreads, NPW = 4, NCW = 2 * kSoftmaxWarps;
-  static constexpr int PRODUCER_REGS = 104, CONSUMER_REGS = 200;
+  static constexpr int NT = kThreads, NPW = 8, NCW = 2 * kSoftmaxWarps;
+  static constexpr int PRODUCER_REGS = 88, CONSUMER_REGS = 168;
 };
 constexpr int kMaskRing = 8;
 constexpr int kSegRing = 4;
@@ -91,14 +93,15 @@ struct PrefixKArgs {
   int count[2];        // groups, sequences
   int row_tiles[2];    // of a prefix, own item family
   int rows[2];         // rows of one (group or sequence, kv head)
-  int slot_rows[2];    // rows per stream of a partial slot
+  int slot_rows[2];    // rows per stream of a partial's place
+  int streams[2];      // streams per place (2 where the family has pairs)
   int per, gw, hq_w, hkv, w, win_tiles, grid;
-  float scale_log2;
+  float inv_grid, scale_log2;
+  float inv_per, inv_gw, inv_hq_w;   // for quotient()
 };
 struct Maps {
   CUtensorMap k[3], v[3];
 };
-constexpr int kPlanInts = 4;   // plan: range, then from here on first segments
 
 // One CTA's share of one item.
 struct Seg {
@@ -106,8 +109,8 @@ struct Seg {
   int gi, h, rt;       // group or sequence, kv head, first row tile
   int t0, n;           // tiles of the item
   int len, hist;       // cached positions, tiles that hold them
-  int slot;            // partial slot: the segment's first or second
-  int whole;           // the segment is not shared: its second slot stays empty
+  int slot;            // place of its partials
+  int whole;           // on the line, not shared: the place behind it stays empty
   int pair;
   // Steps of stream s: a pair's streams share every tile, a single's alternate.
   __device__ __forceinline__ int steps(int s) const { return pair ? n : (n + 1 - s) >> 1; }
@@ -147,12 +150,25 @@ __device__ __forceinline__ void take_registers() {
 
 __device__ __forceinline__ void raise_flag(unsigned f) { atomicOr(&g_prefix_dev_flags, f); }
 
-// Waits with the library's limit; gives up at once when another role has.
+// try_wait that may keep the thread suspended for up to 100 us.
+__device__ __forceinline__ bool try_wait_long(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(100000u)
+      : "memory");
+  return ok != 0;
+}
+// Waits with the library's limit; gives up when another role has.  Suspended,
+// not polling: waiting warps otherwise take the issue slots of those at work.
 __device__ __forceinline__ bool pwait(unsigned long long* bar, uint32_t parity, int* abort) {
   const uint32_t b = smem_u32(bar);
   if (mbar_try_wait(b, parity)) return true;
   const long long t0 = clock64();
-  while (!mbar_try_wait(b, parity)) {
+  while (!try_wait_long(b, parity)) {
     if (*(volatile int*)abort || clock64() - t0 > kWaitLimitCycles) {
       *(volatile int*)abort = 1;
       raise_flag(DUSTIN_DEVFLAG_WAIT_TIMEOUT);
@@ -172,33 +188,49 @@ __device__ __forceinline__ int length_of(const PrefixKArgs& a, int kind, int gi)
 __device__ __forceinline__ int tiles_of(const PrefixKArgs& a, int kind, int len) {
   return (len + kTile - 1) / kTile + (kind ? a.win_tiles : 0);
 }
-// The line is counted in quarters of a unit (one row tile on one tile of a
+// Quotient of x >= 0 by d > 0 from inv, 1 / d in fp32: below 2^21 (which the
+// host's limits ensure) the estimate is at most one off.
+__device__ __forceinline__ int quotient(int x, int d, float inv) {
+  const int q = (int)((float)x * inv), r = x - q * d;
+  return q + (r >= d) - (r < 0);
+}
+__device__ __forceinline__ int quotient(int x, int d) {
+  return quotient(x, d, __frcp_rn((float)d));
+}
+__device__ __forceinline__ int quotient_up(int x, int d) { return quotient(x + d - 1, d); }
+__device__ __forceinline__ int quotient_up(int x, int d, float inv) {
+  return quotient(x + d - 1, d, inv);
+}
+
+// Work is counted in quarters of a unit (one row tile on one tile of a
 // prefix).  An own tile costs more than that, its K and V coming for one row
 // tile alone, and a segment's start and end cost about two units.
 __host__ __device__ constexpr int unit_cost(int kind) { return kind ? 5 : 4; }
 constexpr int kSegmentCost = 8;
-constexpr int kMinRange = 24;         // at least four tiles of a prefix and a segment's cost
+constexpr int kMinRange = 24;
 
 // The line cut into n ranges of at least kMinRange: range c starts at
 // ceil(c * total / n), which is c * (total / n) + ceil(c * (total % n) / n),
 // all in 32 bits.
 struct Cut {
   int n, total, q, r;
-  __device__ __forceinline__ Cut(int line, int grid) {
+  float inv;
+  __device__ __forceinline__ Cut(int line, int ctas) {
     total = line;
-    n = max(1, min(grid, total / kMinRange));
-    q = total / n;
+    n = max(1, min(ctas, total / kMinRange));
+    inv = __frcp_rn((float)n);
+    q = quotient(total, n, inv);
     r = total - q * n;
   }
   __device__ __forceinline__ int start(int c) const {
-    return c >= n ? total : c * q + (c * r + n - 1) / n;
+    return c >= n ? total : c * q + quotient(c * r + n - 1, n, inv);
   }
 };
 
 // A segment's tiles on the line: n of them, w apart, then its fixed cost.
 struct Span {
   int pos, n, w;
-  __device__ __forceinline__ int length() const { return n ? n * w + kSegmentCost : 0; }
+  __device__ __forceinline__ int length() const { return n * w + kSegmentCost; }
   // The first tile at or behind a cut at b.  A cut that would leave a piece
   // shorter than `snap` moves to the segment's end.
   __device__ __forceinline__ int tile(int b, int snap) const {
@@ -207,180 +239,259 @@ struct Span {
     if (x >= len) return n;
     if (x < snap && x <= len - x) return 0;
     if (len - x < snap) return n;
-    return min(n, (x + w - 1) / w);
+    return min(n, quotient_up(x, w));
   }
 };
 
-// The chunks of one (group or sequence, kv head): each holds row_tiles
-// segments, 0 .. pairs-1 on its first half, pairs .. 2 pairs-1 on its second,
-// the single on all of it.
-struct Chunks {
-  int tiles, chunk, rt, pairs, unit;
-  __device__ __forceinline__ Chunks(const PrefixKArgs& a, int kind, int tiles_, int range) {
-    tiles = tiles_;
-    // The most tiles, an even number, whose segment fits a range.
-    chunk = max(2, (range - kSegmentCost) / unit_cost(kind) & ~1);
+// Items of one family on the line: per (group or sequence, kv head) chunks of
+// `chunk` tiles, each with one segment per set (pairs, then the single).
+struct Family {
+  int rt, pairs, sets, unit, chunk;
+  float inv;
+  __device__ __forceinline__ void set(const PrefixKArgs& a, int kind, int range) {
     rt = a.row_tiles[kind];
     pairs = rt >> 1;
+    sets = (rt + 1) >> 1;
     unit = unit_cost(kind);
+    // The most tiles whose segment fits a range.
+    chunk = max(1, quotient(range - kSegmentCost, pairs ? 2 * unit : unit));
+    inv = __frcp_rn((float)chunk);
   }
-  __device__ __forceinline__ int count() const { return (tiles + chunk - 1) / chunk; }
-  // Length on the line of a chunk of m tiles, of everything.
-  __device__ __forceinline__ int length_of(int m) const {
-    const int first = min(m, chunk >> 1);
-    return m * rt * unit + kSegmentCost * (rt - (m > first ? 0 : pairs));
+  __device__ __forceinline__ int count(int tiles) const {
+    return quotient(tiles + chunk - 1, chunk, inv);
   }
-  __device__ __forceinline__ int length() const {
-    if (tiles == 0) return 0;
-    const int n = count();
-    return (n - 1) * length_of(chunk) + length_of(tiles - (n - 1) * chunk);
+  // Length on the line of a chunk of m tiles; of all tiles of one kv head.
+  __device__ __forceinline__ int chunk_length(int m) const { return m * rt * unit + sets * kSegmentCost; }
+  __device__ __forceinline__ int length(int tiles) const {
+    return tiles * rt * unit + count(tiles) * sets * kSegmentCost;
   }
-  // Segment y of chunk c; pos: the chunk's place on the line.
-  __device__ __forceinline__ Span segment(int c, int y, int pos, int* t0) const {
-    const int m = min(chunk, tiles - c * chunk), first = min(m, chunk >> 1), second = m - first;
-    const int l0 = first * 2 * unit + kSegmentCost, l1 = second ? second * 2 * unit + kSegmentCost : 0;
-    *t0 = c * chunk;
-    if (y < pairs) return {pos + y * l0, first, 2 * unit};
-    if (y < 2 * pairs) {
-      *t0 += first;
-      return {pos + pairs * l0 + (y - pairs) * l1, second, 2 * unit};
-    }
-    return {pos + pairs * (l0 + l1), m, unit};
+  // Set y of a chunk of m tiles at pos.
+  __device__ __forceinline__ Span segment(int m, int y, int pos) const {
+    return {pos + y * (m * 2 * unit + kSegmentCost), m, y < pairs ? 2 * unit : unit};
   }
 };
 
-// Walks the segments of this CTA's range.
+// Plan header: 1 where the prefixes are split; then for every group and
+// sequence {first place, segments}: np | ns << 16 where split, else chunks.
+constexpr int kPlanInts = 4;
+
+// Walks the segments of this CTA.
 struct Walk {
   const PrefixKArgs& a;
-  int range, snap, b0, b1;   // range: a lower bound of the ranges' length
+  Family fam;
+  int snap, b0, b1, range;
   int kind, gi, h, c, y;
-  int pos, ord, len, tiles, chunks;   // pos: of chunk c; ord: of its first segment
+  int pos, place, len, tiles, chunks;   // pos, place: of chunk c and its first segment
+  bool one;                             // a split CTA: its segment is in `only`
+  Seg only;
+
+  // Over one family: tiles (x) and, with a chunk set, chunks, else members
+  // that have any (y).  t: of the first 32 members, one per lane.
+  __device__ __forceinline__ int2 sums(int k, int t, const Family* f) const {
+    const int lane = threadIdx.x & 31;
+    int x = 0, y = 0;
+    for (int i = lane; i < a.count[k]; i += 32) {
+      if (i != lane) t = tiles_at(k, i);
+      x += t;
+      y += f ? f->count(t) : t > 0;
+    }
+#pragma unroll 1
+    for (int d = 16; d > 0; d >>= 1) {
+      x += __shfl_xor_sync(0xffffffffu, x, d);
+      y += __shfl_xor_sync(0xffffffffu, y, d);
+    }
+    return make_int2(x, y);
+  }
+  __device__ __forceinline__ int tiles_at(int k, int i) const {
+    return tiles_of(a, k, length_of(a, k, i));
+  }
+
+  // One warp.  CTA 0 leaves the plan for the combine kernel.
   __device__ explicit Walk(const PrefixKArgs& args) : a(args) {
-    make_plan();
-    h = c = y = 0;
-    if (b0 >= b1) {
-      pos = b1;   // nothing here
-      return;
-    }
-    load();
-    const Chunks ch(a, kind, tiles, range);
-    h = (b0 - pos) / ch.length();
-    pos += h * ch.length();
-    if (chunks > 1) c = min((b0 - pos) / ch.length_of(ch.chunk), chunks - 1);
-    if (c) pos += c * ch.length_of(ch.chunk);
-    ord += (h * chunks + c) * ch.rt;
-  }
-  __device__ __forceinline__ void load() {
-    len = length_of(a, kind, gi);
-    tiles = tiles_of(a, kind, len);
-    chunks = Chunks(a, kind, tiles, range).count();
-  }
-  // Sum over the warp's lanes.
-  __device__ static int warp_sum(int x) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    return x;
-  }
-  // One warp.  CTA 0 leaves the range and the first segments of all groups
-  // and sequences for the combine kernel.
-  __device__ void make_plan() {
     const int lane = threadIdx.x & 31, cta = blockIdx.x;
-    // An equal share of the tiles alone; the line, segment costs included, is
-    // longer.
-    int work = 0;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      int sum = 0;
-      for (int i = lane; i < a.count[k]; i += 32) sum += tiles_of(a, k, length_of(a, k, i));
-      work += warp_sum(sum) * a.hkv * a.row_tiles[k] * unit_cost(k);
+    // This lane's group and sequence (the first 32).
+    const int t0 = lane < a.count[0] ? tiles_at(0, lane) : 0;
+    const int t1 = lane < a.count[1] ? tiles_at(1, lane) : 0;
+    const int rt = a.row_tiles[0], pairs = rt >> 1, single = rt & 1;
+    const int2 s0 = sums(0, t0, nullptr), s1 = sums(1, t1, nullptr);
+    const int wp = s0.x * a.hkv * rt * unit_cost(0);
+    const int wo = a.hkv * (s1.x * a.row_tiles[1] * unit_cost(1) +
+                            s1.y * ((a.row_tiles[1] + 1) >> 1) * kSegmentCost);
+    const int share = quotient_up(wp + wo, a.grid, a.inv_grid);
+    int split = 0, np = 0, ns = 0, m = 0;
+    if (wp > 0 && a.count[0] * a.hkv * ((rt + 1) >> 1) <= a.grid) {
+      // Candidates for M (tiles of a single, in units), from the even share
+      // on; lane 0 first.
+      const int least = max(4, quotient_up(share, unit_cost(0)));
+      m = (least + quotient(least * lane, 24) + 1) & ~1;
+      const float inv_s = __frcp_rn((float)m), inv_p = __frcp_rn((float)(m >> 1));
+      int ctas = 0;
+      for (int g = 0; g < a.count[0]; ++g) {
+        const int t = g < 32 ? __shfl_sync(0xffffffffu, t0, g) : tiles_at(0, g);
+        ctas += pairs * quotient(t + (m >> 1) - 1, m >> 1, inv_p) +
+                single * quotient(t + m - 1, m, inv_s);
+      }
+      ctas *= a.hkv;
+      const int rest = quotient_up(wo, m * unit_cost(0));
+      const unsigned fits = __ballot_sync(0xffffffffu, ctas + rest <= a.grid);
+      if (fits) {
+        const int src = __ffs((int)fits) - 1;
+        m = __shfl_sync(0xffffffffu, m, src);
+        split = __shfl_sync(0xffffffffu, ctas, src);
+      }
     }
-    range = max(kMinRange, work / a.grid);
+    // Work on the line, and a lower bound of its ranges' length.
+    const int on_line = wo + (split ? 0 : wp), ctas = a.grid - split;
+    range = max(kMinRange, quotient(on_line, max(ctas, 1)));
     int total = 0;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      int sum = 0;
-      for (int i = lane; i < a.count[k]; i += 32)
-        sum += Chunks(a, k, tiles_of(a, k, length_of(a, k, i)), range).length();
-      total += warp_sum(sum) * a.hkv;
+#pragma unroll 1
+    for (int k = split ? 1 : 0; k < 2; ++k) {
+      fam.set(a, k, range);
+      const int2 x = sums(k, k ? t1 : t0, &fam);
+      total += a.hkv * (x.x * fam.rt * fam.unit + x.y * fam.sets * kSegmentCost);
     }
-    const Cut cut(total, a.grid);
+    const Cut cut(total, max(ctas, 1));
     snap = cut.q >> 4;
-    b0 = cut.start(cta);
-    b1 = cut.start(cta + 1);
-    if (cta == 0 && lane == 0) {
-      a.plan[0] = range;
-    }
-    kind = gi = pos = ord = 0;
-    int base = 0, segments = 0;
+    one = cta < split;
+    b0 = one ? 0 : cut.start(cta - split);
+    b1 = one ? 0 : cut.start(cta - split + 1);
+    if (cta == 0 && lane == 0) a.plan[0] = split ? 1 : 0;
+    int2* table = reinterpret_cast<int2*>(a.plan + kPlanInts);
+    kind = gi = pos = place = 0;
+    int base = 0;
+#pragma unroll 1
     for (int k = 0; k < 2; ++k) {
+      const bool direct = k == 0 && split;
+      int places = 0;
+      fam.set(a, k, range);
       for (int i0 = 0; i0 < a.count[k]; i0 += 32) {
         const int i = i0 + lane;
-        int mine = 0, segs = 0;
-        if (i < a.count[k]) {
-          const Chunks ch(a, k, tiles_of(a, k, length_of(a, k, i)), range);
-          mine = ch.length() * a.hkv;
-          segs = ch.count() * ch.rt * a.hkv;
+        const int t = i0 ? (i < a.count[k] ? tiles_at(k, i) : 0) : (k ? t1 : t0);
+        // Its length on the line (split: nothing), its places, its segments.
+        int length = 0, mine = 0, segs = 0;
+        if (direct) {
+          const int in_pairs = pairs ? quotient_up(t, m >> 1) : 0;
+          const int in_single = single ? quotient_up(t, m) : 0;
+          mine = (pairs * in_pairs + in_single) * a.hkv;
+          segs = in_pairs | in_single << 16;
+        } else {
+          segs = fam.count(t);
+          length = fam.length(t) * a.hkv;
+          mine = segs * fam.sets * a.hkv * 2;
         }
-        int inc = mine, sinc = segs;
-#pragma unroll
+        int at = length, pl = mine;
+#pragma unroll 1
         for (int d = 1; d < 32; d <<= 1) {
-          const int x = __shfl_up_sync(0xffffffffu, inc, d);
-          const int z = __shfl_up_sync(0xffffffffu, sinc, d);
+          const int v = __shfl_up_sync(0xffffffffu, at, d), w = __shfl_up_sync(0xffffffffu, pl, d);
           if (lane >= d) {
-            inc += x;
-            sinc += z;
+            at += v;
+            pl += w;
           }
         }
-        const int at = base + inc - mine, so = segments + sinc - segs;
-        if (cta == 0 && i < a.count[k]) a.plan[kPlanInts + k * a.count[0] + i] = so;
-        const unsigned here = __ballot_sync(0xffffffffu, at <= b0 && b0 < at + mine);
+        const int all = __shfl_sync(0xffffffffu, at, 31), all_places = __shfl_sync(0xffffffffu, pl, 31);
+        at += base - length;
+        pl += places - mine;
+        if (cta == 0 && i < a.count[k]) table[k * a.count[0] + i] = make_int2(pl, segs);
+        const bool hit = direct ? one && pl <= cta && cta < pl + mine
+                                : !one && at <= b0 && b0 < at + length;
+        const unsigned here = __ballot_sync(0xffffffffu, hit);
         if (here) {
           const int src = __ffs((int)here) - 1;
           kind = k;
           gi = i0 + src;
           pos = __shfl_sync(0xffffffffu, at, src);
-          ord = __shfl_sync(0xffffffffu, so, src);
-          if (cta != 0) return;
+          place = __shfl_sync(0xffffffffu, pl, src);
+          const int x = __shfl_sync(0xffffffffu, segs, src);
+          np = x & 0xffff;
+          ns = x >> 16;
+          if (cta != 0) {
+            k = 2;
+            break;
+          }
         }
-        base += __shfl_sync(0xffffffffu, inc, 31);
-        segments += __shfl_sync(0xffffffffu, sinc, 31);
+        base += all;
+        places += all_places;
       }
-      segments = 0;   // slots are counted per family
+    }
+    h = c = y = 0;
+    if (one) {
+      // Segments of a kv head: for each of the np parts all pairs, then the
+      // single's.
+      load();
+      const int per = pairs * np + ns;
+      const int x = cta - place;
+      h = quotient(x, per);
+      const int z = x - h * per;
+      only.kind = 0;
+      only.gi = gi;
+      only.h = h;
+      only.pair = z < pairs * np;
+      const int part = only.pair ? quotient(z, pairs) : z - pairs * np;
+      const int parts = only.pair ? np : ns;
+      only.rt = only.pair ? 2 * (z - part * pairs) : rt - 1;
+      only.t0 = quotient(part * tiles, parts);
+      only.n = quotient((part + 1) * tiles, parts) - only.t0;
+      only.len = len;
+      only.hist = tiles;
+      only.slot = cta;
+      only.whole = 0;
+      pos = b1;
+    } else if (b0 >= b1) {
+      pos = b1;   // nothing here
+    } else {
+      load();
+      const int per = fam.length(tiles);
+      h = quotient(b0 - pos, per);
+      pos += h * per;
+      const int full = fam.chunk_length(fam.chunk);
+      c = min(quotient(b0 - pos, full), chunks - 1);
+      pos += c * full;
+      place += (h * chunks + c) * fam.sets * 2;
     }
   }
+  __device__ __forceinline__ void load() {
+    fam.set(a, kind, range);
+    len = length_of(a, kind, gi);
+    tiles = tiles_of(a, kind, len);
+    chunks = fam.count(tiles);
+  }
   __device__ bool next(Seg& s) {
+    if (one) {
+      s = only;
+      one = false;
+      return s.n > 0;
+    }
     while (pos < b1) {
-      const Chunks ch(a, kind, tiles, range);
       if (tiles == 0 || h == a.hkv) {
         h = 0;
         if (++gi == a.count[kind]) {
           gi = 0;
-          ord = 0;
-          ++kind;      // pos < b1 <= total: there is work left in kind 1
+          place = 0;
+          ++kind;      // pos < b1 <= total: there is work left in family 1
         }
         load();
         continue;
       }
-      int t0;
-      const Span sp = ch.segment(c, y, pos, &t0);
+      const int m = min(fam.chunk, tiles - c * fam.chunk);
+      const Span sp = fam.segment(m, y, pos);
       const int lo = sp.tile(b0, snap), hi = sp.tile(b1, snap);
       s.kind = kind;
       s.gi = gi;
       s.h = h;
-      s.pair = y < 2 * ch.pairs;
-      s.rt = s.pair ? 2 * (y < ch.pairs ? y : y - ch.pairs) : ch.rt - 1;
-      s.slot = (ord + y) * 2 + (lo > 0);
+      s.pair = y < fam.pairs;
+      s.rt = 2 * y;
+      s.slot = place + 2 * y + (lo > 0);
       s.whole = hi - lo == sp.n;
-      s.t0 = t0 + lo;
+      s.t0 = c * fam.chunk + lo;
       s.n = hi - lo;
       s.len = len;
       s.hist = (len + kTile - 1) / kTile;
       const bool found = lo < hi;
       const bool past = sp.pos >= b1;
-      if (++y == ch.rt) {
+      if (++y == fam.sets) {
         y = 0;
-        ord += ch.rt;
-        pos += ch.length_of(min(ch.chunk, tiles - c * ch.chunk));
+        place += fam.sets * 2;
+        pos += fam.chunk_length(m);
         if (++c == chunks) {
           c = 0;
           ++h;
@@ -467,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sh.empty[i]), 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_u32(&sh.q_full[s]), 1);
+      mbar_init(smem_u32(&sh.q_full[s]), kQWarps);
       mbar_init(smem_u32(&sh.q_empty[s]), 1);
       for (int i = 0; i < 2; ++i) {
         mbar_init(smem_u32(&sh.s_full[s][i]), 1);
@@ -478,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kMaskRing; ++i) mbar_init(smem_u32(&sh.mask_full[i]), 1);
     for (int i = 0; i < kSegRing; ++i) {
       mbar_init(smem_u32(&sh.seg_full[i]), 1);
-      mbar_init(smem_u32(&sh.seg_empty[i]), 2 * kSoftmaxWarps + 3);
+      mbar_init(smem_u32(&sh.seg_empty[i]), 2 * kSoftmaxWarps + 2 + kQWarps);
     }
     mbar_init(smem_u32(&sh.drain), 1);
     mbar_fence_init();
@@ -506,12 +617,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(smem_u32(&sh.seg_empty[at % kSegRing]));
   };
 
-  if (warp >= kMmaWarp) give_registers();   // one instruction for the whole warpgroup
+  if (warp >= kMmaWarp) give_registers();   // one instruction for whole warpgroups
   if (warp == kWalkWarp) {
     // --------------------------------------------------------------- walker
     role_begin();
     Walk walk(a);
-    Seg s;
+    Seg s{};
     for (int at = 0;; ++at) {
       const bool more = walk.next(s);
       if (!pwait_warp(&sh.seg_empty[at % kSegRing], (at / kSegRing & 1) ^ 1, &sh.abort)) break;
@@ -522,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!more) break;
     }
-  } else if (warp == kQWarp) {
+  } else if (warp >= kQWarp) {
     // ------------------------------------------------------------------- Q
     // Row tiles in the tensor cores' swizzled layout; a pair fills both
     // buffers, singles take turns, so that the next one's rows are there
@@ -542,24 +653,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = pwait_warp(&sh.q_empty[buf], (fills[buf] & 1) ^ 1, &sh.abort);
         if (!ok) break;
         ++fills[buf];
-        constexpr int CPR = D / 8, STEP = 32 / CPR;     // 16-byte pieces, rows per pass
-        const int c = lane % CPR;
-        int r = lane / CPR;
-        int seq = s.gi, in_seq = first + r;
-        if (s.kind == 0) {
-          seq = s.gi * a.per + in_seq / a.gw;
-          in_seq %= a.gw;
-        }
-        const uint32_t dst = q_buf + buf * C::TILE_BYTES + (c / 8) * C::HALF;
-        const __nv_bfloat16* src = a.q + ((long long)seq * a.hq_w + s.h * a.gw + in_seq) * D + c * 8;
-        for (; r < rows; r += STEP) {
-          cp_async_16_full(dst + r * 128 + ((c % 8 ^ (r & 7)) << 4), src);
-          in_seq += STEP;
-          src += STEP * D;
-          while (s.kind == 0 && in_seq >= a.gw) {       // on to the next sequence's rows
-            in_seq -= a.gw;
-            src += (long long)(a.hq_w - a.gw) * D;
+        constexpr int CPR = D / 8, STEP = 32 * kQWarps / CPR;   // 16-byte pieces, rows per pass
+        const int piece = tid - kQWarp * 32, c = piece % CPR;
+        static_assert(STEP % 8 == 0, "a thread's rows share their place in the swizzle");
+        int r = piece / CPR;
+        uint32_t dst = q_buf + buf * C::TILE_BYTES + (c / 8) * C::HALF + r * 128 +
+                       ((c % 8 ^ (r & 7)) << 4);
+        const __nv_bfloat16* src = a.q + (long long)s.h * a.gw * D + c * 8;
+        for (; r < rows; r += STEP, dst += STEP * 128) {
+          int seq = s.gi, in_seq = first + r;
+          if (s.kind == 0) {
+            const int rr = in_seq;
+            int q = (int)((float)rr * a.inv_gw);        // at most one off
+            q -= q * a.gw > rr;
+            q += (q + 1) * a.gw <= rr;
+            seq = s.gi * a.per + q;
+            in_seq = rr - q * a.gw;
           }
+          cp_async_16_full(dst, src + ((long long)seq * a.hq_w + in_seq) * D);
         }
         cp_async_commit();
         cp_async_wait<0>();
@@ -814,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(smem_u32(&sh.drain), 0, kWaitLimitCycles);
     }
     __syncwarp();
-  } else {
+  } else if (warp < kMmaWarp) {
     // -------------------------------------------------------------- softmax
     take_registers();
     const int st = warp >> 2, row = tid & 127;
@@ -956,7 +1067,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // merged, each writing half of the columns.  Pieces of four columns,
       // rows side by side: full lines per store.
       const int sr = a.slot_rows[s.kind];
-      const long long slot = (long long)s.slot * 2 + (s.pair ? st : 0);
+      const int streams = a.streams[s.kind];
+      const long long slot = (long long)s.slot * streams + (s.pair ? st : 0);
       float* out = a.ws_o[s.kind] + slot * sr * D + row * 4;
       const uint64_t both = add2(sum[0], sum[1]);
       float l = lo_of(both) + hi_of(both);
@@ -1001,7 +1113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (row < rows && (s.pair || st == 0)) {
         float2* ml = a.ws_ml[s.kind] + slot * sr + row;
         *ml = make_float2(m, l);
-        if (s.whole) ml[2 * sr] = make_float2(-INFINITY, 0.f);
+        if (s.whole) ml[streams * sr] = make_float2(-INFINITY, 0.f);
       }
     }
   }
@@ -1038,37 +1150,39 @@ __global__ void __launch_bounds__(kCombineThreads)
   const PrefixKArgs& a = c.k;
   const int piece = threadIdx.x / ROWS, mine = threadIdx.x % ROWS;
   const int row = blockIdx.x * ROWS + mine;
+  const bool have = row < c.rows;
+  const int seq = have ? quotient(row, a.hq_w, a.inv_hq_w) : 0;
+  const int in_seq = have ? row - seq * a.hq_w : 0;
+  const int h = quotient(in_seq, a.gw, a.inv_gw), r = in_seq - h * a.gw;
+  const int g = quotient(seq, a.per, a.inv_per);
   griddep_wait();
   griddep_launch_dependents();
-  const bool have = row < c.rows;
-  const int seq = have ? row / a.hq_w : 0, in_seq = have ? row - seq * a.hq_w : 0;
-  const int h = in_seq / a.gw, r = in_seq - h * a.gw, g = seq / a.per;
-  const int range = a.plan[0];
-  // The row's places: two slots per segment.
-  int n[2], base[2], segs[2], in_tile[2], chunks[2], second[2];
-  bool pair[2];
+  const int2* table = reinterpret_cast<const int2*>(a.plan + kPlanInts);
+  const int2 of[2] = {table[g], table[a.count[0] + seq]};
+  const bool split = a.plan[0];
+  // The row's places in family k: base + (e >> two) * stride + (e & two).
+  int n[2], base[2], stride[2], two[2], stream[2], in_tile[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const int gi = k ? seq : g, rr = k ? r : (seq - g * a.per) * a.gw + r, rt = rr / kTile;
-    const Chunks ch(a, k, tiles_of(a, k, length_of(a, k, gi)), range);
-    pair[k] = rt < 2 * ch.pairs;
-    chunks[k] = ch.count();
-    // A last chunk of half a chunk's tiles or less has no second half.
-    second[k] = ch.tiles - (chunks[k] - 1) * ch.chunk > ch.chunk >> 1;
-    segs[k] = ch.rt;
+    const int rr = k ? r : (seq - g * a.per) * a.gw + r, rt = rr / kTile;
+    const int pairs = a.row_tiles[k] >> 1, sets = (a.row_tiles[k] + 1) >> 1;
+    const bool pair = rt < 2 * pairs;
     in_tile[k] = rr - rt * kTile;
-    base[k] = a.plan[kPlanInts + k * a.count[0] + gi] + h * chunks[k] * ch.rt +
-              (pair[k] ? rt >> 1 : 2 * ch.pairs);
-    base[k] = base[k] * 4 + (pair[k] ? rt & 1 : 0);
-    n[k] = have ? chunks[k] * (pair[k] ? 4 : 2) : 0;
+    stream[k] = pair ? rt & 1 : 0;
+    if (k == 0 && split) {
+      const int np = of[k].y & 0xffff, ns = of[k].y >> 16;
+      base[k] = of[k].x + h * (pairs * np + ns) + (pair ? rt >> 1 : pairs * np);
+      stride[k] = pair ? pairs : 1;
+      two[k] = 0;
+      n[k] = pair ? np : ns;
+    } else {
+      base[k] = of[k].x + (h * of[k].y * sets + (rt >> 1)) * 2;
+      stride[k] = sets * 2;
+      two[k] = 1;
+      n[k] = of[k].y * 2;
+    }
+    if (!have) n[k] = 0;
   }
-  // Place e of family k: chunk, (pair) half, slot.
-  auto stream_slot = [&](int k, int e) -> int {
-    if (!pair[k]) return base[k] + (e >> 1) * segs[k] * 4 + (e & 1) * 2;
-    const int cc = e >> 2, hi = e >> 1 & 1, lo = e & 1;
-    if (hi && cc == chunks[k] - 1 && !second[k]) return -1;
-    return base[k] + (cc * segs[k] + hi * (segs[k] >> 1)) * 4 + lo * 2;
-  };
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x < ROWS) {
     m_of[threadIdx.x] = -INFINITY;
@@ -1083,11 +1197,11 @@ __global__ void __launch_bounds__(kCombineThreads)
       unsigned at = 0;
       if (e < count) {
         const int k = e < n[1] ? 1 : 0;
-        const int slot = stream_slot(k, k ? e : e - n[1]);
-        if (slot >= 0) {
-          at = ((unsigned)slot * (a.slot_rows[k] * (D / 4)) + in_tile[k]) * 2 + k;
-          ml = a.ws_ml[k][(long long)slot * a.slot_rows[k] + in_tile[k]];
-        }
+        const int x = k ? e : e - n[1];
+        const int at_place = base[k] + (x >> two[k]) * stride[k] + (x & two[k]);
+        const int slot = at_place * a.streams[k] + stream[k];
+        at = ((unsigned)slot * (a.slot_rows[k] * (D / 4)) + in_tile[k]) * 2 + k;
+        ml = a.ws_ml[k][(long long)slot * a.slot_rows[k] + in_tile[k]];
       }
       ml_of[mine][i] = ml;
       at_of[mine][i] = at;
@@ -1224,23 +1338,28 @@ PrefixKArgs shape_args(const PrefixArgs& p, int sms, Layout* lay) {
   // The workspace does not depend on whether the window comes along.
   a.win_tiles = (p.w + kTile - 1) / kTile;
   a.grid = sms;
+  a.inv_grid = 1.f / sms;
+  a.inv_per = 1.f / a.per;
+  a.inv_gw = 1.f / a.gw;
+  a.inv_hq_w = 1.f / a.hq_w;
   size_t at = 0;
   for (int k = 0; k < 2; ++k) {
-    // Segments: one per chunk (two tiles at least) and row tile.  A chunk is
-    // as long as a range allows: 4 M + 8 (prefix), 5 M + 8 (own) quarters of
-    // at most `range`, M even, so the whole chunks' units, work / 4 or / 5 at
-    // most, make up to 2 or 3 segments per CTA (the most at range 31, 27).
-    const size_t items = (size_t)a.count[k] * a.hkv * a.row_tiles[k];
+    // Places on the line: two per segment, a segment per set and chunk.  A
+    // chunk has as many tiles as a range allows (at least one), so beside one
+    // per item there are at most about four segments per CTA (the most at
+    // ranges just above kMinRange; towards one with longer ones).
+    a.streams[k] = a.row_tiles[k] > 1 ? 2 : 1;
+    const size_t items = (size_t)a.count[k] * a.hkv * ((a.row_tiles[k] + 1) / 2);
     const size_t tiles = (a.n[k] + kTile - 1) / kTile + (k ? a.win_tiles : 0);
-    const size_t segs = std::min(items * ((tiles + 1) / 2), items + (2 + k) * (size_t)a.grid);
-    const size_t rows = segs * 4 * a.slot_rows[k];
+    const size_t segs = std::min(items * tiles, items + 4 * (size_t)a.grid);
+    const size_t rows = std::max<size_t>(2 * segs, a.grid) * a.streams[k] * a.slot_rows[k];
     lay->o[k] = at;
     at += align256(rows * p.d * sizeof(float));
     lay->ml[k] = at;
     at += align256(rows * sizeof(float2));
   }
   lay->plan = at;
-  at += align256((size_t)(kPlanInts + p.groups + p.b) * sizeof(int));
+  at += align256((size_t)(kPlanInts + 2 * (p.groups + p.b)) * sizeof(int));
   lay->total = at;
   return a;
 }
