@@ -30,7 +30,8 @@
 //
 // Roles of the 16 warps: 0-3 and 4-7 softmax (one thread per row of stream
 // A / B), 8 issues tcgen05.mma, 9 TMA loads of K and V, 10 walks the CTA's
-// share and publishes its segments, 12-15 copy Q rows.  S = Q K^T and O += P V
+// share and publishes its segments, 11 (of CTA 0) writes the plan for the
+// combine kernel, 12-15 copy Q rows.  S = Q K^T and O += P V
 // accumulate in tensor memory (512 columns: two S buffers of 64 positions and
 // an O per stream); P replaces S in place as bf16 and is read from there as
 // the A operand, so only Q, K and V live in shared memory.  With two S
@@ -55,7 +56,7 @@ __device__ unsigned int g_prefix_dev_flags;
 constexpr int kTile = 128;        // positions of a K/V tile, rows of a row tile
 constexpr int kHalf = 64;         // positions of an S buffer
 constexpr int kSoftmaxWarps = 4;  // per stream
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kWalkWarp = 10, kQWarp = 12, kQWarps = 4;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kWalkWarp = 10, kTableWarp = 11, kQWarp = 12, kQWarps = 4;
 constexpr int kThreads = 16 * 32;
 // Registers: a softmax thread holds 64 scores and their weights; the other
 // two warpgroups give up what they need beyond the launch's 128.
@@ -96,6 +97,11 @@ struct PrefixKArgs {
   int slot_rows[2];    // rows per stream of a partial's place
   int streams[2];      // streams per place (2 where the family has pairs)
   int per, gw, hq_w, hkv, w, win_tiles, grid;
+  // Prefixes of one length: CTAs that have one segment of them each, segments
+  // of a pair and of the single.  0: decided on the device, where the lengths
+  // are.
+  int split, np, ns;
+  int range;           // with split > 0 and own parts of one length: the line's
   float inv_grid, scale_log2;
   float inv_per, inv_gw, inv_hq_w;   // for quotient()
 };
@@ -280,6 +286,7 @@ struct Walk {
   const PrefixKArgs& a;
   Family fam;
   int snap, b0, b1, range;
+  int m;                                // device search: tiles of a single's segment
   int kind, gi, h, c, y;
   int pos, place, len, tiles, chunks;   // pos, place: of chunk c and its first segment
   bool one;                             // a split CTA: its segment is in `only`
@@ -306,43 +313,128 @@ struct Walk {
     return tiles_of(a, k, length_of(a, k, i));
   }
 
-  // One warp.  CTA 0 leaves the plan for the combine kernel.
-  __device__ explicit Walk(const PrefixKArgs& args) : a(args) {
-    const int lane = threadIdx.x & 31, cta = blockIdx.x;
-    // This lane's group and sequence (the first 32).
-    const int t0 = lane < a.count[0] ? tiles_at(0, lane) : 0;
-    const int t1 = lane < a.count[1] ? tiles_at(1, lane) : 0;
+  // M by search: CTAs the prefixes take, 0 where they go on the line.  One
+  // warp; t0: tiles of the first 32 groups.
+  __device__ __forceinline__ int search(int t0, int wp, int wo) {
+    const int lane = threadIdx.x & 31;
     const int rt = a.row_tiles[0], pairs = rt >> 1, single = rt & 1;
-    const int2 s0 = sums(0, t0, nullptr), s1 = sums(1, t1, nullptr);
-    const int wp = s0.x * a.hkv * rt * unit_cost(0);
-    const int wo = a.hkv * (s1.x * a.row_tiles[1] * unit_cost(1) +
-                            s1.y * ((a.row_tiles[1] + 1) >> 1) * kSegmentCost);
+    if (wp == 0 || a.count[0] * a.hkv * ((rt + 1) >> 1) > a.grid) return 0;
+    // Candidates from the even share on, lane 0 first.
     const int share = quotient_up(wp + wo, a.grid, a.inv_grid);
-    int split = 0, np = 0, ns = 0, m = 0;
-    if (wp > 0 && a.count[0] * a.hkv * ((rt + 1) >> 1) <= a.grid) {
-      // Candidates for M (tiles of a single, in units), from the even share
-      // on; lane 0 first.
-      const int least = max(4, quotient_up(share, unit_cost(0)));
-      m = (least + quotient(least * lane, 24) + 1) & ~1;
-      const float inv_s = __frcp_rn((float)m), inv_p = __frcp_rn((float)(m >> 1));
-      int ctas = 0;
-      for (int g = 0; g < a.count[0]; ++g) {
-        const int t = g < 32 ? __shfl_sync(0xffffffffu, t0, g) : tiles_at(0, g);
-        ctas += pairs * quotient(t + (m >> 1) - 1, m >> 1, inv_p) +
-                single * quotient(t + m - 1, m, inv_s);
+    const int least = max(4, quotient_up(share, unit_cost(0)));
+    int x = (least + quotient(least * lane, 24) + 1) & ~1;
+    const float inv_s = __frcp_rn((float)x), inv_p = __frcp_rn((float)(x >> 1));
+    int ctas = 0;
+    for (int g = 0; g < a.count[0]; ++g) {
+      const int t = g < 32 ? __shfl_sync(0xffffffffu, t0, g) : tiles_at(0, g);
+      ctas += pairs * quotient(t + (x >> 1) - 1, x >> 1, inv_p) + single * quotient(t + x - 1, x, inv_s);
+    }
+    ctas *= a.hkv;
+    const unsigned fits =
+        __ballot_sync(0xffffffffu, ctas + quotient_up(wo, x * unit_cost(0)) <= a.grid);
+    if (!fits) return 0;
+    const int src = __ffs((int)fits) - 1;
+    m = __shfl_sync(0xffffffffu, x, src);
+    return __shfl_sync(0xffffffffu, ctas, src);
+  }
+  // The one segment of a split CTA, the x-th of group gi.  Of a kv head: for
+  // each of the np parts all pairs, then the single's.
+  __device__ __forceinline__ void direct(int x, int np, int ns) {
+    const int rt = a.row_tiles[0], pairs = rt >> 1, per = pairs * np + ns;
+    len = length_of(a, 0, gi);
+    tiles = (len + kTile - 1) / kTile;
+    h = quotient(x, per);
+    const int z = x - h * per;
+    only.kind = 0;
+    only.gi = gi;
+    only.h = h;
+    only.pair = z < pairs * np;
+    const int part = only.pair ? quotient(z, pairs) : z - pairs * np;
+    const int parts = only.pair ? np : ns;
+    const float inv = __frcp_rn((float)parts);
+    only.rt = only.pair ? 2 * (z - part * pairs) : rt - 1;
+    only.t0 = quotient(part * tiles, parts, inv);
+    only.n = quotient((part + 1) * tiles, parts, inv) - only.t0;
+    only.len = len;
+    only.hist = tiles;
+    only.slot = blockIdx.x;
+    only.whole = 0;
+    one = true;
+    pos = b1 = 0;
+  }
+  // On the line: from the sequence (or group) at pos to the segment at b0.
+  __device__ __forceinline__ void seek() {
+    if (b0 >= b1) {
+      pos = b1;   // nothing here
+      return;
+    }
+    load();
+    const int per = fam.length(tiles);
+    h = quotient(b0 - pos, per);
+    pos += h * per;
+    const int full = fam.chunk_length(fam.chunk);
+    c = min(quotient(b0 - pos, full), chunks - 1);
+    pos += c * full;
+    place += (h * chunks + c) * fam.sets * 2;
+  }
+
+  // One warp.  With `write` (one warp of the grid) it leaves the plan for the
+  // combine kernel instead of looking for this CTA's share.
+  __device__ Walk(const PrefixKArgs& args, bool write) : a(args) {
+    const int lane = threadIdx.x & 31, cta = blockIdx.x;
+    int2* table = reinterpret_cast<int2*>(a.plan + kPlanInts);
+    kind = gi = pos = place = h = c = y = 0;
+    one = false;
+    if (a.split > 0) {
+      // Prefixes of one length, split by the host.
+      const int per_group = a.hkv * ((a.row_tiles[0] >> 1) * a.np + a.ns);
+      if (write) {
+        if (lane == 0) a.plan[0] = 1;
+        for (int g = lane; g < a.count[0]; g += 32)
+          table[g] = make_int2(g * per_group, a.np | a.ns << 16);
+      } else if (cta < a.split) {
+        gi = quotient(cta, per_group);
+        direct(cta - gi * per_group, a.np, a.ns);
+        return;
       }
-      ctas *= a.hkv;
-      const int rest = quotient_up(wo, m * unit_cost(0));
-      const unsigned fits = __ballot_sync(0xffffffffu, ctas + rest <= a.grid);
-      if (fits) {
-        const int src = __ffs((int)fits) - 1;
-        m = __shfl_sync(0xffffffffu, m, src);
-        split = __shfl_sync(0xffffffffu, ctas, src);
+      if (a.own_len == nullptr) {
+        // Own parts of one length too: all in closed form.
+        kind = 1;
+        range = a.range;
+        load();
+        const int per = fam.length(tiles) * a.hkv, places = chunks * fam.sets * a.hkv * 2;
+        if (write) {
+          for (int i = lane; i < a.count[1]; i += 32)
+            table[a.count[0] + i] = make_int2(i * places, chunks);
+          return;
+        }
+        const Cut cut(per * a.count[1], max(a.grid - a.split, 1));
+        snap = cut.q >> 4;
+        b0 = cut.start(cta - a.split);
+        b1 = cut.start(cta - a.split + 1);
+        gi = per ? quotient(b0, per) : 0;
+        pos = gi * per;
+        place = gi * places;
+        seek();
+        return;
       }
     }
-    // Work on the line, and a lower bound of its ranges' length.
-    const int on_line = wo + (split ? 0 : wp), ctas = a.grid - split;
-    range = max(kMinRange, quotient(on_line, max(ctas, 1)));
+    // This lane's group and sequence (the first 32).
+    const int t0 = lane < a.count[0] && a.split == 0 ? tiles_at(0, lane) : 0;
+    const int t1 = lane < a.count[1] ? tiles_at(1, lane) : 0;
+    const int2 s1 = sums(1, t1, nullptr);
+    int on_line = a.hkv * (s1.x * a.row_tiles[1] * unit_cost(1) +
+                           s1.y * ((a.row_tiles[1] + 1) >> 1) * kSegmentCost);
+    int split = a.split;
+    if (split == 0) {
+      const int wp = sums(0, t0, nullptr).x * a.hkv * a.row_tiles[0] * unit_cost(0);
+      split = search(t0, wp, on_line);
+      if (!split) on_line += wp;
+      if (write && lane == 0) a.plan[0] = split ? 1 : 0;
+    }
+    // A lower bound of the ranges' length, the line's length.
+    const int ctas = max(a.grid - split, 1);
+    range = max(kMinRange, quotient(on_line, ctas));
     int total = 0;
 #pragma unroll 1
     for (int k = split ? 1 : 0; k < 2; ++k) {
@@ -350,18 +442,15 @@ struct Walk {
       const int2 x = sums(k, k ? t1 : t0, &fam);
       total += a.hkv * (x.x * fam.rt * fam.unit + x.y * fam.sets * kSegmentCost);
     }
-    const Cut cut(total, max(ctas, 1));
+    const Cut cut(total, ctas);
     snap = cut.q >> 4;
-    one = cta < split;
-    b0 = one ? 0 : cut.start(cta - split);
-    b1 = one ? 0 : cut.start(cta - split + 1);
-    if (cta == 0 && lane == 0) a.plan[0] = split ? 1 : 0;
-    int2* table = reinterpret_cast<int2*>(a.plan + kPlanInts);
-    kind = gi = pos = place = 0;
+    const bool in_split = cta < split && !write;
+    b0 = in_split ? 0 : cut.start(max(cta - split, 0));
+    b1 = in_split ? 0 : cut.start(max(cta - split, 0) + 1);
     int base = 0;
 #pragma unroll 1
-    for (int k = 0; k < 2; ++k) {
-      const bool direct = k == 0 && split;
+    for (int k = a.split > 0 ? 1 : 0; k < 2; ++k) {
+      const bool is_split = k == 0 && split;
       int places = 0;
       fam.set(a, k, range);
       for (int i0 = 0; i0 < a.count[k]; i0 += 32) {
@@ -369,11 +458,12 @@ struct Walk {
         const int t = i0 ? (i < a.count[k] ? tiles_at(k, i) : 0) : (k ? t1 : t0);
         // Its length on the line (split: nothing), its places, its segments.
         int length = 0, mine = 0, segs = 0;
-        if (direct) {
-          const int in_pairs = pairs ? quotient_up(t, m >> 1) : 0;
-          const int in_single = single ? quotient_up(t, m) : 0;
-          mine = (pairs * in_pairs + in_single) * a.hkv;
-          segs = in_pairs | in_single << 16;
+        if (is_split) {
+          const int pairs = a.row_tiles[0] >> 1;
+          const int np = pairs ? quotient_up(t, m >> 1) : 0;
+          const int ns = a.row_tiles[0] & 1 ? quotient_up(t, m) : 0;
+          mine = (pairs * np + ns) * a.hkv;
+          segs = np | ns << 16;
         } else {
           segs = fam.count(t);
           length = fam.length(t) * a.hkv;
@@ -391,63 +481,31 @@ struct Walk {
         const int all = __shfl_sync(0xffffffffu, at, 31), all_places = __shfl_sync(0xffffffffu, pl, 31);
         at += base - length;
         pl += places - mine;
-        if (cta == 0 && i < a.count[k]) table[k * a.count[0] + i] = make_int2(pl, segs);
-        const bool hit = direct ? one && pl <= cta && cta < pl + mine
-                                : !one && at <= b0 && b0 < at + length;
-        const unsigned here = __ballot_sync(0xffffffffu, hit);
-        if (here) {
-          const int src = __ffs((int)here) - 1;
-          kind = k;
-          gi = i0 + src;
-          pos = __shfl_sync(0xffffffffu, at, src);
-          place = __shfl_sync(0xffffffffu, pl, src);
-          const int x = __shfl_sync(0xffffffffu, segs, src);
-          np = x & 0xffff;
-          ns = x >> 16;
-          if (cta != 0) {
-            k = 2;
-            break;
+        if (write) {
+          if (i < a.count[k]) table[k * a.count[0] + i] = make_int2(pl, segs);
+        } else {
+          const bool hit = is_split ? in_split && pl <= cta && cta < pl + mine
+                                    : !in_split && at <= b0 && b0 < at + length;
+          const unsigned here = __ballot_sync(0xffffffffu, hit);
+          if (here) {
+            const int src = __ffs((int)here) - 1;
+            kind = k;
+            gi = i0 + src;
+            pos = __shfl_sync(0xffffffffu, at, src);
+            place = __shfl_sync(0xffffffffu, pl, src);
+            const int x = __shfl_sync(0xffffffffu, segs, src);
+            if (is_split)
+              direct(cta - place, x & 0xffff, x >> 16);
+            else
+              seek();
+            return;
           }
         }
         base += all;
         places += all_places;
       }
     }
-    h = c = y = 0;
-    if (one) {
-      // Segments of a kv head: for each of the np parts all pairs, then the
-      // single's.
-      load();
-      const int per = pairs * np + ns;
-      const int x = cta - place;
-      h = quotient(x, per);
-      const int z = x - h * per;
-      only.kind = 0;
-      only.gi = gi;
-      only.h = h;
-      only.pair = z < pairs * np;
-      const int part = only.pair ? quotient(z, pairs) : z - pairs * np;
-      const int parts = only.pair ? np : ns;
-      only.rt = only.pair ? 2 * (z - part * pairs) : rt - 1;
-      only.t0 = quotient(part * tiles, parts);
-      only.n = quotient((part + 1) * tiles, parts) - only.t0;
-      only.len = len;
-      only.hist = tiles;
-      only.slot = cta;
-      only.whole = 0;
-      pos = b1;
-    } else if (b0 >= b1) {
-      pos = b1;   // nothing here
-    } else {
-      load();
-      const int per = fam.length(tiles);
-      h = quotient(b0 - pos, per);
-      pos += h * per;
-      const int full = fam.chunk_length(fam.chunk);
-      c = min(quotient(b0 - pos, full), chunks - 1);
-      pos += c * full;
-      place += (h * chunks + c) * fam.sets * 2;
-    }
+    pos = b1;   // nothing here
   }
   __device__ __forceinline__ void load() {
     fam.set(a, kind, range);
@@ -621,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kWalkWarp) {
     // --------------------------------------------------------------- walker
     role_begin();
-    Walk walk(a);
+    Walk walk(a, false);
     Seg s{};
     for (int at = 0;; ++at) {
       const bool more = walk.next(s);
@@ -633,6 +691,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!more) break;
     }
+  } else if (warp == kTableWarp) {
+    role_begin();
+    if (blockIdx.x == 0) Walk(a, true);
   } else if (warp >= kQWarp) {
     // ------------------------------------------------------------------- Q
     // Row tiles in the tensor cores' swizzled layout; a pair fills both
@@ -1364,6 +1425,36 @@ PrefixKArgs shape_args(const PrefixArgs& p, int sms, Layout* lay) {
   return a;
 }
 
+// The split of prefixes of one length (Walk::search for those on the device):
+// the smallest M, from the even share on, that fits the CTAs.  Own parts of
+// unknown length count as the longest: a line shorter than that ends early,
+// a longer one would hold up everything.
+void host_split(PrefixKArgs& a, bool lengths_given) {
+  a.split = a.np = a.ns = a.range = 0;
+  const long long tp = (a.n[0] + kTile - 1) / kTile;
+  const long long to = (a.n[1] + kTile - 1) / kTile + a.win_tiles;
+  const int rt = a.row_tiles[0], pairs = rt / 2, single = rt & 1;
+  if (lengths_given || tp == 0 || (long long)a.count[0] * a.hkv * ((rt + 1) / 2) > a.grid) return;
+  const long long wp = tp * rt * a.count[0] * a.hkv * unit_cost(0);
+  const long long wo = to * a.count[1] * a.hkv * a.row_tiles[1] * unit_cost(1) +
+                       (to > 0) * (long long)a.count[1] * a.hkv * ((a.row_tiles[1] + 1) / 2) * kSegmentCost;
+  const long long least = std::max<long long>(2, ((wp + wo + a.grid - 1) / a.grid + 3) / unit_cost(0));
+  for (long long m = least; m <= 3 * least; ++m) {
+    // A pair's tile is two units.
+    const long long np = pairs ? std::min(tp, (2 * tp + m - 1) / m) : 0;
+    const long long ns = single ? (tp + m - 1) / m : 0;
+    const long long split = a.count[0] * a.hkv * (pairs * np + ns);
+    const long long rest = (wo + m * unit_cost(0) - 1) / (m * unit_cost(0));
+    if (split + rest > a.grid) continue;
+    a.split = (int)split;
+    a.np = (int)np;
+    a.ns = (int)ns;
+    const long long tiles = to * a.count[1] * a.hkv * a.row_tiles[1] * unit_cost(1);
+    a.range = (int)std::max<long long>(kMinRange, tiles / std::max<long long>(1, a.grid - split));
+    return;
+  }
+}
+
 template <int D>
 cudaError_t run_prefix(const PrefixKArgs& k, const Maps& maps, const PrefixArgs& p,
                        cudaStream_t st) {
@@ -1400,6 +1491,7 @@ cudaError_t launch_attn_prefix(const PrefixArgs& p, int sms, void* ws, cudaStrea
   Layout lay;
   PrefixKArgs a = shape_args(p, sms, &lay);
   if (!p.has_win) a.win_tiles = 0;
+  host_split(a, p.prefix_len != nullptr);
   a.q = p.q;
   a.prefix_len = p.prefix_len;
   a.own_len = p.own_len;
