@@ -173,8 +173,8 @@ __global__ void __launch_bounds__(kForkThreads) kv_fork_kernel(const ForkArgs a)
 // ---- resize
 
 constexpr int kResizeThreads = 1024;
-constexpr int kResizeWarps = kResizeThreads / 32;
 constexpr int kResizeCluster = 8;
+constexpr int kDropBlock = 256;   // table entries a warp drops at a time
 
 struct ResizeShared {
   int seq[kResizeMaxList];
@@ -183,7 +183,7 @@ struct ResizeShared {
   int last[kResizeMaxList];     // last page to be copied (-1: none)
   int first[kResizeMaxList];    // rank of the entry's first free page
   int newlen[kResizeMaxList];
-  int scan[kResizeWarps];
+  int scan[32];
   int free_here;                // read by the other CTAs of the cluster
   int total;
   int base, free_all;
@@ -191,18 +191,17 @@ struct ResizeShared {
 
 // Exclusive sum of v over the CTA's threads; *total receives the sum.
 __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   int inc = v;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, inc, d);
     if (lane >= d) inc += y;
   }
-  __syncthreads();
   if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
-  int w = warp_sums[lane];   // kResizeWarps == 32
-  const int mine = w;
+  const int mine = lane < warps ? warp_sums[lane] : 0;
+  int w = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, w, d);
@@ -210,9 +209,8 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
   }
   const int below = __shfl_sync(0xffffffffu, w - mine, warp);
   const int all = __shfl_sync(0xffffffffu, w, 31);
-  __syncthreads();
   if (threadIdx.x == 0) *total = all;
-  __syncthreads();
+  __syncthreads();   // also: warp_sums may be written again
   return below + inc - v;
 }
 
@@ -222,6 +220,7 @@ __global__ void __launch_bounds__(kResizeThreads) kv_resize_kernel(const ResizeA
   cg::cluster_group cl = cg::this_cluster();
   const int rank = (int)cl.block_rank(), C = (int)cl.num_blocks();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int threads = blockDim.x, warps = threads >> 5;
   griddep_wait();
   griddep_launch_dependents();
 
@@ -250,13 +249,25 @@ __global__ void __launch_bounds__(kResizeThreads) kv_resize_kernel(const ResizeA
   }
   __syncthreads();
 
-  // Entries behind the new ends.
-  for (int i = rank * kResizeWarps + warp; i < a.n_list; i += C * kResizeWarps) {
+  // Entries behind the new ends, in blocks dealt to all warps of the cluster.
+  const int per_entry = (a.pages_per_seq + kDropBlock - 1) / kDropBlock;
+  for (int x = rank * warps + warp; x < a.n_list * per_entry; x += C * warps) {
+    const int i = x / per_entry, s0 = (x - i * per_entry) * kDropBlock;
+    const int lo = max(sh.have[i], s0), hi = min(sh.had[i], s0 + kDropBlock);
+    if (lo >= hi) continue;
     int* row = a.page_table + (long long)sh.seq[i] * a.pages_per_seq;
-    for (int s = sh.have[i] + lane; s < sh.had[i]; s += 32) {
-      const int pg = row[s];
-      if (pg >= 0 && pg < a.num_pages)
-        atomicSub(a.refcount + pg, 1);
+    int pg[kDropBlock / 32];
+#pragma unroll
+    for (int u = 0; u < kDropBlock / 32; ++u) {
+      const int s = lo + u * 32 + lane;
+      pg[u] = s < hi ? row[s] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kDropBlock / 32; ++u) {
+      const int s = lo + u * 32 + lane;
+      if (s >= hi) continue;
+      if (pg[u] >= 0 && pg[u] < a.num_pages)
+        atomicSub(a.refcount + pg[u], 1);
       else
         raise_flag(DUSTIN_DEVFLAG_PAGE_RANGE);
       row[s] = -1;
@@ -291,14 +302,14 @@ __global__ void __launch_bounds__(kResizeThreads) kv_resize_kernel(const ResizeA
     const int lo = min(rank * per, a.num_pages), hi = min(lo + per, a.num_pages);
     const int words = (hi - lo + 31) / 32;
 #pragma unroll 8
-    for (int wd = warp; wd < words; wd += kResizeWarps) {
+    for (int wd = warp; wd < words; wd += warps) {
       const int pg = lo + wd * 32 + lane;
       const bool is_free = pg < hi && __ldcg(a.refcount + pg) == 0;
       const unsigned bits = __ballot_sync(0xffffffffu, is_free);
       if (lane == 0) bitmap[wd] = bits;
     }
     __syncthreads();
-    const int m = (words + kResizeThreads - 1) / kResizeThreads;
+    const int m = (words + threads - 1) / threads;
     const int w0 = min(tid * m, words), w1 = min(w0 + m, words);
     int count = 0;
     for (int wd = w0; wd < w1; ++wd) count += __popc(bitmap[wd]);
@@ -419,12 +430,16 @@ cudaError_t launch_fork(const ForkArgs& a, cudaStream_t st) {
 
 cudaError_t launch_resize(const ResizeArgs& a, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  const int per = ((a.num_pages + kResizeCluster - 1) / kResizeCluster + 31) / 32;
-  const int smem_max = kResizeMaxPages / kResizeCluster / 8;
-  cudaError_t e = ensure_smem_attr(kv_resize_kernel, smem_max, done);
+  cudaError_t e = ensure_smem_attr(kv_resize_kernel, kResizeMaxPages / kResizeCluster / 8, done);
   if (e != cudaSuccess) return e;
-  e = launch_pdl_cluster(kv_resize_kernel, dim3(kResizeCluster), dim3(kResizeThreads),
-                         (size_t)per * sizeof(unsigned), st, (unsigned)kResizeCluster, a);
+  // A small update runs in one CTA: its barriers cost a tenth of a cluster's,
+  // and 8192 counts are eight loads a thread.
+  const bool small = a.num_pages <= 8192 && (long long)a.n_list * a.pages_per_seq <= 8192;
+  const int C = small ? 1 : kResizeCluster;
+  const int threads = small && a.n_list <= 256 ? 256 : kResizeThreads;
+  const int words = ((a.num_pages + C - 1) / C + 31) / 32;
+  e = launch_pdl_cluster(kv_resize_kernel, dim3((unsigned)C), dim3((unsigned)threads),
+                         (size_t)words * sizeof(unsigned), st, (unsigned)C, a);
   if (e == cudaSuccess) note_launches(1);
   return e;
 }

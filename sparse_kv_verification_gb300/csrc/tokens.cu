@@ -71,10 +71,12 @@ __device__ __forceinline__ float load1(const T* p) {
     return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short*>(p)) << 16);
 }
 
+__device__ __forceinline__ uint4 load16(const void* p) {
+  return __ldg(reinterpret_cast<const uint4*>(p));
+}
 // 16 bytes as floats.
 template <typename T>
-__device__ __forceinline__ void load_vec(const T* p, float (&x)[16 / sizeof(T)]) {
-  const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+__device__ __forceinline__ void to_floats(const uint4& u, float (&x)[16 / sizeof(T)]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -100,35 +102,81 @@ struct Row {
   }
 };
 
-// The calling lane's share of the mass in [lo, hi), float-float.
+// 16 bytes from byte `at` of the 32 in w (at: 0 .. 15, a multiple of the
+// element size, the same for the whole warp): words, then a half word.
+template <typename T>
+__device__ __forceinline__ uint4 extract16(const uint4& lo, const uint4& hi, int at) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if (at & 8)
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  if (at & 4)
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  if (sizeof(T) == 2 && (at & 2))
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __byte_perm(w[i], w[i + 1], 0x5432);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The calling lane's share of the mass in [lo, hi), float-float.  Rows start
+// at any element: 16-byte loads follow p's alignment, and q's bytes, aligned
+// otherwise, are put together from two of its 16-byte words (the second one
+// the next lane's first).
 template <typename T>
 __device__ Ff lane_mass(const Row<T>& r, long long lo, long long hi, int lane) {
   constexpr int V = 16 / sizeof(T);
   Ff acc{0.f, 0.f};
-  const bool vec = ((reinterpret_cast<uintptr_t>(r.p + lo) |
-                     (r.q ? reinterpret_cast<uintptr_t>(r.q + lo) : 0)) & 15u) == 0;
-  long long j = lo;
-  if (vec) {
-    const long long full = lo + (hi - lo) / (32 * V) * (32 * V);
+  const int head = (int)((16 - (reinterpret_cast<uintptr_t>(r.p + lo) & 15u)) & 15u) / (int)sizeof(T);
+  const long long j0 = min(hi, lo + head);
+  if (lo + lane < j0) acc = ff_add(acc, r.at(lo + lane));
+  const long long full = j0 + (hi - j0) / (32 * V) * (32 * V);
+  if (!r.q) {
 #pragma unroll 4
-    for (; j < full; j += 32 * V) {
+    for (long long j = j0; j < full; j += 32 * V) {
       const long long e = j + lane * V;
-      float pv[V], qv[V];
-      load_vec(r.p + e, pv);
-      if (r.q) {
-        load_vec(r.q + e, qv);
+      float pv[V];
+      to_floats<T>(load16(r.p + e), pv);
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc = ff_add(acc, rest_of(pv[i], qv[i]));
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          acc = ff_add(acc, Ff{e + i == r.gone ? 0.f : mass_of(pv[i]), 0.f});
+      for (int i = 0; i < V; ++i) acc = ff_add(acc, Ff{e + i == r.gone ? 0.f : mass_of(pv[i]), 0.f});
+    }
+  } else {
+    const int off = (int)(reinterpret_cast<uintptr_t>(r.q + j0) & 15u);
+#pragma unroll 2
+    for (long long j = j0; j < full; j += 32 * V) {
+      const long long e = j + lane * V;
+      const uint4 pw = load16(r.p + e);
+      const char* qa = reinterpret_cast<const char*>(r.q + e) - off;
+      uint4 qw = load16(qa);
+      if (off) {   // uniform
+        uint4 next;
+        next.x = __shfl_down_sync(0xffffffffu, qw.x, 1);
+        next.y = __shfl_down_sync(0xffffffffu, qw.y, 1);
+        next.z = __shfl_down_sync(0xffffffffu, qw.z, 1);
+        next.w = __shfl_down_sync(0xffffffffu, qw.w, 1);
+        // The last lane's second word holds an element of this range, too.
+        if (lane == 31) next = load16(qa + 16);
+        qw = extract16<T>(qw, next, off);
       }
+      float pv[V], qv[V];
+      to_floats<T>(pw, pv);
+      to_floats<T>(qw, qv);
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc = ff_add(acc, rest_of(pv[i], qv[i]));
     }
   }
-#pragma unroll 8
-  for (j += lane; j < hi; j += 32) acc = ff_add(acc, r.at(j));
+  for (long long j = full + lane; j < hi; j += 32) acc = ff_add(acc, r.at(j));
   return acc;
+}
+
+// Inclusive sums over 16 lanes (both halves of the warp alike), in lane order.
+__device__ __forceinline__ double scan16(double x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, x, d, 16);
+    if ((lane & 15) >= d) x += y;
+  }
+  return x;
 }
 
 struct Shared {
@@ -143,7 +191,7 @@ struct Shared {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_tokens_kernel(const TokenArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) verify_tokens_kernel(const TokenArgs a) {
   __shared__ Shared sh;
   cg::cluster_group cl = cg::this_cluster();
   const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
@@ -152,6 +200,8 @@ __global__ void __launch_bounds__(kThreads) verify_tokens_kernel(const TokenArgs
   griddep_wait();
   griddep_launch_dependents();
 
+  // Read early: it is needed at the end of a chain of loads.
+  const float u_here = warp == 0 ? __ldg(a.u_sample + bb) : 0.f;
   const T* p0 = static_cast<const T*>(a.p) + (long long)bb * a.stride_tb;
   const T* q0 = a.q ? static_cast<const T*>(a.q) + (long long)bb * a.stride_db : nullptr;
   const int* draft = a.draft ? a.draft + (long long)bb * (a.w - 1) : nullptr;
@@ -201,8 +251,8 @@ __global__ void __launch_bounds__(kThreads) verify_tokens_kernel(const TokenArgs
   row.p = p0 + (long long)n_acc * a.stride_tw;
   row.q = rejected && q0 ? q0 + (long long)n_acc * a.stride_dw : nullptr;
   row.gone = rejected && !q0 ? (long long)__ldg(draft + n_acc) : -1;
-  // fp64 sums below run in one thread: a warp's fp64 addition holds the
-  // unit for 16 cycles, whoever needs the result.
+  // fp64 sums below run in one warp: an fp64 addition holds the unit for 16
+  // cycles, whoever needs the result.
   for (int pass = 0; pass < 2; ++pass) {
     Ff acc = lane_mass(row, lo, hi, lane);
 #pragma unroll
@@ -211,38 +261,38 @@ __global__ void __launch_bounds__(kThreads) verify_tokens_kernel(const TokenArgs
                            __shfl_xor_sync(0xffffffffu, acc.c, d)});
     if (lane == 0) sh.warp_sum[warp] = ff_value(acc);
     __syncthreads();
-    if (tid == 0) {
-      double s = 0.0;
-      for (int i = 0; i < kWarps; ++i) s += sh.warp_sum[i];
-      sh.cta_sum = s;
+    // Warp 0: inclusive sums over the CTA's warps, then over the CTAs.
+    double mine = 0.0, run = 0.0;
+    if (warp == 0) {
+      mine = lane < kWarps ? sh.warp_sum[lane] : 0.0;
+      run = scan16(mine, lane);
+      if (lane == kWarps - 1) sh.cta_sum = run;
     }
     cl.sync();
-    if (tid == 0) {
-      double total = 0.0, before = 0.0;
-      for (int i = 0; i < C; ++i) {
-        if (i == rank) before = total;
-        total += *cl.map_shared_rank(&sh.cta_sum, i);
-      }
-      const double u = (double)__ldg(a.u_sample + bb);
+    if (warp == 0) {
+      const double theirs = lane < C ? *cl.map_shared_rank(&sh.cta_sum, lane) : 0.0;
+      const double upto = scan16(theirs, lane);
+      const double total = __shfl_sync(0xffffffffu, upto, kWarps - 1);
+      const double before = rank ? __shfl_sync(0xffffffffu, upto, rank - 1) : 0.0;
+      const double u = (double)u_here;
       double t = u > 0.0 ? u * total : 0.0;
       if (t >= total) t = total * (1.0 - 0x1p-53);
-      sh.total = total;
-      sh.t = t;
-      sh.walk = -1;
-      sh.last = -1;
-      sh.found = 0x7fffffff;
-      if (total > 0.0 && before <= t && t < before + sh.cta_sum) {
-        // The warp range that holds t; the last with mass if rounding at
-        // the upper end leaves none.
-        double at = before;
-        for (int i = 0; i < kWarps && !(at > t); ++i) {
-          const double s = sh.warp_sum[i];
-          if (s > 0.0) {
-            sh.walk = i;
-            sh.base = at;
-          }
-          at += s;
-        }
+      // The first range with mass that ends behind t, the last one with mass
+      // should rounding at the upper end leave none.
+      const double base = before + (run - mine);
+      const unsigned has = __ballot_sync(0xffffffffu, mine > 0.0);
+      const unsigned ends = __ballot_sync(0xffffffffu, mine > 0.0 && before + run > t);
+      const double after = __shfl_sync(0xffffffffu, upto, rank);
+      const bool owner = total > 0.0 && before <= t && t < after && has;
+      const int walk = owner ? (ends ? __ffs((int)ends) - 1 : 31 - __clz((int)has)) : -1;
+      const double at = __shfl_sync(0xffffffffu, base, walk < 0 ? 0 : walk);
+      if (lane == 0) {
+        sh.total = total;
+        sh.t = t;
+        sh.base = at;
+        sh.walk = walk;
+        sh.last = -1;
+        sh.found = 0x7fffffff;
       }
     }
     __syncthreads();
@@ -279,13 +329,12 @@ __global__ void __launch_bounds__(kThreads) verify_tokens_kernel(const TokenArgs
       const Ff prev{__shfl_up_sync(0xffffffffu, inc.s, 1), __shfl_up_sync(0xffffffffu, inc.c, 1)};
       if (lane == 31) sh.warp_sum[warp] = ff_value(inc);
       __syncthreads();
-      if (tid == 0) {
-        double s = c0 == wlo ? sh.base : sh.warp_base[kWarps];
-        for (int i = 0; i < kWarps; ++i) {
-          sh.warp_base[i] = s;
-          s += sh.warp_sum[i];
-        }
-        sh.warp_base[kWarps] = s;
+      if (warp == 0) {
+        const double from = c0 == wlo ? sh.base : sh.warp_base[kWarps];
+        const double upto = from + scan16(lane < kWarps ? sh.warp_sum[lane] : 0.0, lane);
+        __syncwarp();
+        if (lane == 0) sh.warp_base[0] = from;
+        if (lane < kWarps) sh.warp_base[lane + 1] = upto;
       }
       __syncthreads();
       if (sh.warp_base[warp] <= t && t < sh.warp_base[warp + 1]) {

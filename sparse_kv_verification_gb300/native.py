@@ -163,21 +163,17 @@ def kv_desc(k: torch.Tensor, v: Optional[torch.Tensor] = None,
     if v is not None and (v.shape != k.shape or v.stride() != k.stride()
                           or v.dtype != k.dtype):
         raise ValueError("v must match k in shape, strides and dtype")
-    desc = DustinKV()
-    desc.k = k.data_ptr()
-    desc.v = v.data_ptr() if v is not None else None
-    desc.stride_b, desc.stride_h, desc.stride_n = (k.stride(0), k.stride(1),
-                                                   k.stride(2))
+    table, page_size, pages_per_seq, num_pages = None, 0, 0, 0
     if page_table is not None:
         if page_table.dtype != torch.int32 or page_table.dim() != 2:
             raise ValueError("page_table must be int32 [b][pages_per_seq]")
         if page_table.stride(1) != 1:
             raise ValueError("page_table rows must be contiguous")
-        desc.page_table = page_table.data_ptr()
-        desc.page_size = k.shape[2]
-        desc.pages_per_seq = page_table.stride(0)
-        desc.num_pages = k.shape[0]
-    return desc
+        table, page_size = page_table.data_ptr(), k.shape[2]
+        pages_per_seq, num_pages = page_table.stride(0), k.shape[0]
+    sb, sh, sn, _ = k.stride()
+    return DustinKV(k.data_ptr(), None if v is None else v.data_ptr(), sb, sh, sn, table,
+                    page_size, pages_per_seq, num_pages)
 
 
 def workspace(nbytes: int, device) -> torch.Tensor:
@@ -558,16 +554,39 @@ def prepare_full_verify_attn(q, kv, h_kv, n, scale, o, lse, ws, stream=None,
 
 # ------------------------------------------------ attention, shared prefixes
 
-def _one_device(*ts):
-    """Device tensors (None allowed) of one device."""
-    _need_cuda(*ts)
-    if len({t.device for t in ts if t is not None}) > 1:
-        raise ValueError("tensors must live on one device")
+def _one_device(*ts) -> int:
+    """The device all of these tensors (None allowed) live on."""
+    index = -1
+    for t in ts:
+        if t is not None:
+            i = t.get_device()
+            if i < 0:
+                raise ValueError("tensors must live on a CUDA device")
+            if index >= 0 and i != index:
+                raise ValueError("tensors must live on one device")
+            index = i
+    return index
+
+
+def _run(fn, index: int, stream, *args) -> None:
+    """Calls fn(*args, stream) with device `index` current."""
+    raw = stream.cuda_stream if stream is not None else \
+        torch._C._cuda_getCurrentRawStream(index)
+    if torch.cuda.current_device() == index:
+        _check(fn(*args, raw))
+    else:
+        with torch.cuda.device(index):
+            _check(fn(*args, raw))
 
 
 def _int32(what, t, *shape):
-    if t.dtype != torch.int32 or not t.is_contiguous() or tuple(t.shape) != shape:
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous int32 {list(shape)}")
+
+
+def _float32(what, t, *shape):
+    if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous fp32 {list(shape)}")
 
 
 def dustin_prefix_verify_attn_workspace_size(b, groups, h_q, h_kv, d, w, n_prefix,
@@ -588,20 +607,23 @@ def dustin_prefix_verify_attn(q: torch.Tensor, prefix: Optional[DustinKV],
     `prefix`), each with own positions behind it (row i of `own`) and, with
     win, the window's causal block.  prefix_len int32 [groups] and own_len
     int32 [b] give lengths below n_prefix and n_own."""
-    _attn_checks(q, o, lse)
-    _one_device(q, o, lse, ws, prefix_len, own_len)
+    index = _one_device(q, o, lse, ws, prefix_len, own_len)
+    if q.dim() != 4 or q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("q must be contiguous bf16 [b][h_q][w][d]")
     b, h_q, w, d = q.shape
+    if o.shape != q.shape or o.dtype != torch.bfloat16 or not o.is_contiguous():
+        raise ValueError("o must be contiguous bf16 shaped like q")
+    _float32("lse", lse, b, h_q, w)
     if prefix_len is not None:
         _int32("prefix_len", prefix_len, groups)
     if own_len is not None:
         _int32("own_len", own_len, b)
     ref = lambda kv: None if kv is None else ctypes.byref(kv)
-    with torch.cuda.device(q.device):
-        _check(load().dustin_prefix_verify_attn(
-            b, groups, h_q, h_kv, d, w, n_prefix, n_own, q.data_ptr(), ref(prefix),
-            _ptr(prefix_len), ref(own), _ptr(own_len), ref(win), float(scale),
-            o.data_ptr(), lse.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),
-            int(flags), _stream(stream, q.device)))
+    _run(load().dustin_prefix_verify_attn, index, stream,
+         b, groups, h_q, h_kv, d, w, n_prefix, n_own, q.data_ptr(), ref(prefix),
+         _ptr(prefix_len), ref(own), _ptr(own_len), ref(win), scale, o.data_ptr(),
+         lse.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+         flags)
 
 
 # ------------------------------------------- verification of drafted tokens
@@ -617,41 +639,37 @@ def dustin_verify_tokens(p_target: torch.Tensor, p_draft: Optional[torch.Tensor]
     u_accept fp32 [b][w-1] (None if w is 1); u_sample fp32 [b].  tokens int32
     [b][w] receives the accepted drafts, the drawn token and -1 behind it,
     n_accepted int32 [b] the number of accepted drafts."""
-    _one_device(p_target, p_draft, draft, u_accept, u_sample, tokens, n_accepted,
-               n_draft)
-    if p_target.dim() != 3 or p_target.stride(2) != 1 and p_target.shape[2] > 1:
-        raise ValueError("p_target must be [b][w][vocab] with contiguous rows")
+    index = _one_device(p_target, p_draft, draft, u_accept, u_sample, tokens, n_accepted,
+                        n_draft)
+    if p_target.dim() != 3:
+        raise ValueError("p_target must be [b][w][vocab]")
     b, w, vocab = p_target.shape
-    if p_target.dtype not in (torch.float32, torch.bfloat16):
+    dtype = p_target.dtype
+    if dtype != torch.float32 and dtype != torch.bfloat16:
         raise ValueError("probabilities are fp32 or bf16")
-    if p_draft is not None and (
-            p_draft.dtype != p_target.dtype or tuple(p_draft.shape) != (b, w - 1, vocab)
-            or p_draft.stride(2) != 1 and vocab > 1):
-        raise ValueError("p_draft must be [b][w-1][vocab] of p_target's type with "
-                         "contiguous rows")
+    tb, tw, row = p_target.stride()
+    db, dw = 0, 0
+    if p_draft is not None:
+        if p_draft.dtype != dtype or p_draft.shape != (b, w - 1, vocab):
+            raise ValueError("p_draft must be [b][w-1][vocab] of p_target's type")
+        db, dw, row2 = p_draft.stride()
+        row = max(row, row2)
+    if row != 1 and vocab > 1:
+        raise ValueError("vocabulary rows must be contiguous")
     if w > 1:
         if draft is None or u_accept is None:
             raise ValueError("draft and u_accept are required")
         _int32("draft", draft, b, w - 1)
-        if u_accept.dtype != torch.float32 or not u_accept.is_contiguous() or \
-                tuple(u_accept.shape) != (b, w - 1):
-            raise ValueError("u_accept must be contiguous fp32 [b][w-1]")
-    if u_sample.dtype != torch.float32 or not u_sample.is_contiguous() or \
-            tuple(u_sample.shape) != (b,):
-        raise ValueError("u_sample must be contiguous fp32 [b]")
+        _float32("u_accept", u_accept, b, w - 1)
+    _float32("u_sample", u_sample, b)
     _int32("tokens", tokens, b, w)
     _int32("n_accepted", n_accepted, b)
     if n_draft is not None:
         _int32("n_draft", n_draft, b)
-    with torch.cuda.device(p_target.device):
-        _check(load().dustin_verify_tokens(
-            b, w, vocab,
-            DUSTIN_DTYPE_F32 if p_target.dtype == torch.float32 else DUSTIN_DTYPE_BF16,
-            p_target.data_ptr(), p_target.stride(0), p_target.stride(1), _ptr(p_draft),
-            0 if p_draft is None else p_draft.stride(0),
-            0 if p_draft is None else p_draft.stride(1), _ptr(draft), _ptr(n_draft),
-            _ptr(u_accept), u_sample.data_ptr(), tokens.data_ptr(),
-            n_accepted.data_ptr(), _stream(stream, p_target.device)))
+    _run(load().dustin_verify_tokens, index, stream, b, w, vocab,
+         DUSTIN_DTYPE_F32 if dtype == torch.float32 else DUSTIN_DTYPE_BF16,
+         p_target.data_ptr(), tb, tw, _ptr(p_draft), db, dw, _ptr(draft), _ptr(n_draft),
+         _ptr(u_accept), u_sample.data_ptr(), tokens.data_ptr(), n_accepted.data_ptr())
 
 
 # ------------------------------------------------- compaction, shared pages
@@ -661,7 +679,7 @@ def dustin_kv_compact(src: Sequence[DustinKV], dst: Sequence[DustinKV], h_kv: in
                       k_len: Optional[torch.Tensor] = None, stream=None) -> None:
     """Row i of each sequence and layer of dst becomes row idx[b][i] of src
     (idx int32 [b][k], i < k_len[b]); in place where dst is src."""
-    _one_device(idx, k_len)
+    index = _one_device(idx, k_len)
     if len(src) != len(dst):
         raise ValueError("one src and one dst cache per layer")
     if idx.dtype != torch.int32 or not idx.is_contiguous() or idx.dim() != 2:
@@ -669,21 +687,21 @@ def dustin_kv_compact(src: Sequence[DustinKV], dst: Sequence[DustinKV], h_kv: in
     b, k = idx.shape
     if k_len is not None:
         _int32("k_len", k_len, b)
-    sa, da = (DustinKV * len(src))(*src), (DustinKV * len(dst))(*dst)
-    with torch.cuda.device(idx.device):
-        _check(load().dustin_kv_compact(
-            len(src), b, h_kv, d, n, k, ctypes.addressof(sa), ctypes.addressof(da),
-            idx.data_ptr(), _ptr(k_len), _stream(stream, idx.device)))
+    sa = (DustinKV * len(src))(*src)
+    da = sa if dst is src else (DustinKV * len(dst))(*dst)
+    _run(load().dustin_kv_compact, index, stream, len(src), b, h_kv, d, n, k,
+         ctypes.addressof(sa), ctypes.addressof(da), idx.data_ptr(), _ptr(k_len))
 
 
 def _page_state(page_table, seq_len, refcount):
-    _one_device(page_table, seq_len, refcount)
     if page_table.dim() != 2:
         raise ValueError("page_table must be int32 [n_seqs][pages_per_seq]")
-    _int32("page_table", page_table, *page_table.shape)
-    _int32("seq_len", seq_len, page_table.shape[0])
-    _int32("refcount", refcount, refcount.numel())
-    return (page_table.shape[0], page_table.shape[1], refcount.numel())
+    n_seqs, per_seq = page_table.shape
+    _int32("page_table", page_table, n_seqs, per_seq)
+    _int32("seq_len", seq_len, n_seqs)
+    pages = refcount.numel()
+    _int32("refcount", refcount, pages)
+    return n_seqs, per_seq, pages
 
 
 def dustin_kv_fork(page_table: torch.Tensor, seq_len: torch.Tensor,
@@ -691,14 +709,12 @@ def dustin_kv_fork(page_table: torch.Tensor, seq_len: torch.Tensor,
                    child: torch.Tensor, stream=None) -> None:
     """Sequence child[f] (empty) shares all pages of sequence parent[f]."""
     n_seqs, ppseq, pages = _page_state(page_table, seq_len, refcount)
-    _one_device(page_table, parent, child)
+    index = _one_device(page_table, seq_len, refcount, parent, child)
     _int32("parent", parent, parent.numel())
     _int32("child", child, parent.numel())
-    with torch.cuda.device(page_table.device):
-        _check(load().dustin_kv_fork(
-            n_seqs, ppseq, page_size, pages, parent.numel(), parent.data_ptr(),
-            child.data_ptr(), page_table.data_ptr(), seq_len.data_ptr(),
-            refcount.data_ptr(), _stream(stream, page_table.device)))
+    _run(load().dustin_kv_fork, index, stream, n_seqs, ppseq, page_size, pages,
+         parent.numel(), parent.data_ptr(), child.data_ptr(), page_table.data_ptr(),
+         seq_len.data_ptr(), refcount.data_ptr())
 
 
 def dustin_kv_resize(page_table: torch.Tensor, seq_len: torch.Tensor,
@@ -711,17 +727,14 @@ def dustin_kv_resize(page_table: torch.Tensor, seq_len: torch.Tensor,
     full last page copied first (in the caches kvs; copies int32 [n][2]
     receives {old page, new page} or {-1, -1})."""
     n_seqs, ppseq, pages = _page_state(page_table, seq_len, refcount)
-    _one_device(page_table, seqs, new_len, copies)
+    index = _one_device(page_table, seq_len, refcount, seqs, new_len, copies)
     n = seqs.numel()
     _int32("seqs", seqs, n)
     if new_len is not None:
         _int32("new_len", new_len, n)
     _int32("copies", copies, n, 2)
     arr = (DustinKV * len(kvs))(*kvs) if kvs else None
-    with torch.cuda.device(page_table.device):
-        _check(load().dustin_kv_resize(
-            n_seqs, ppseq, page_size, pages, n, seqs.data_ptr(), _ptr(new_len),
-            page_table.data_ptr(), seq_len.data_ptr(), refcount.data_ptr(),
-            copies.data_ptr(), len(kvs), h_kv, d,
-            ctypes.addressof(arr) if kvs else None,
-            _stream(stream, page_table.device)))
+    _run(load().dustin_kv_resize, index, stream, n_seqs, ppseq, page_size, pages, n,
+         seqs.data_ptr(), _ptr(new_len), page_table.data_ptr(), seq_len.data_ptr(),
+         refcount.data_ptr(), copies.data_ptr(), len(kvs), h_kv, d,
+         ctypes.addressof(arr) if kvs else None)
