@@ -62,7 +62,7 @@ constexpr int kThreads = 16 * 32;
 // two warpgroups give up what they need beyond the launch's 128.
 struct Split {
   static constexpr int NT = kThreads, NPW = 8, NCW = 2 * kSoftmaxWarps;
-  static constexpr int PRODUCER_REGS = 88, CONSUMER_REGS = 168;
+  static constexpr int PRODUCER_REGS = 112, CONSUMER_REGS = 144;
 };
 constexpr int kMaskRing = 8;
 constexpr int kSegRing = 4;
@@ -77,8 +77,8 @@ struct Cfg {
 // A cache as the kernel sees it; the tensor maps come beside it.
 struct PrefixCache {
   const int* page_table;
-  int page_size, pages_per_seq, num_pages;
-  int box_rows;        // rows of one TMA box
+  int pages_per_seq, num_pages;
+  int runs;            // runs per page
   int zh, zb;          // 0 where that stride is 0: the coordinate stays 0
 };
 
@@ -96,6 +96,7 @@ struct PrefixKArgs {
   int rows[2];         // rows of one (group or sequence, kv head)
   int slot_rows[2];    // rows per stream of a partial's place
   int streams[2];      // streams per place (2 where the family has pairs)
+  int log_box[2];      // of the family's tiles, the window's included
   int per, gw, hq_w, hkv, w, win_tiles, grid;
   // Prefixes of one length: CTAs that have one segment of them each, segments
   // of a pair and of the single.  0: decided on the device, where the lengths
@@ -129,6 +130,16 @@ struct Seg {
     return pair ? 2 * t + 1 : t + 1 < n ? 2 * t + 2 : 2 * t + 1;
   }
 };
+
+// Shared-memory layout of a V tile: boxes of 2^log_box rows behind one
+// another, each with its 64-column halves behind one another.  (A K tile has
+// its halves of all 128 rows behind one another: rows that are a product's N
+// lie at one stride.)
+template <int D>
+__device__ __forceinline__ uint32_t v_row(int row, int log_box) {
+  return (uint32_t)((row >> log_box) << (log_box + (D == 128 ? 8 : 7))) +
+         (uint32_t)((row & ((1 << log_box) - 1)) << 7);
+}
 
 struct Control {
   float2 exchange[2][kTile];       // m, l of a single's streams
@@ -233,6 +244,13 @@ struct Cut {
   }
 };
 
+// Whether an equal share on the line, two segments to a CTA, ends before a
+// split into segments of m units does, for items whose row tiles all share
+// their K/V tiles anyway.
+__host__ __device__ constexpr bool on_line_is_shorter(long long m, long long share) {
+  return m * unit_cost(0) > share + share / 16 + kSegmentCost;
+}
+
 // A segment's tiles on the line: n of them, w apart, then its fixed cost.
 struct Span {
   int pos, n, w;
@@ -335,6 +353,7 @@ struct Walk {
     if (!fits) return 0;
     const int src = __ffs((int)fits) - 1;
     m = __shfl_sync(0xffffffffu, x, src);
+    if (rt <= 2 && on_line_is_shorter(m, share)) return 0;
     return __shfl_sync(0xffffffffu, ctas, src);
   }
   // The one segment of a split CTA, the x-th of group gi.  Of a kv head: for
@@ -755,6 +774,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok || sp->kind < 0) break;
       const Seg s = *sp;
       done_with(at);
+      const PrefixCache& cache = a.cache[s.kind];
+      const int log_box = a.log_box[s.kind], boxes = kTile >> log_box;
+      // Lane l loads run l % boxes of a tile, half l / boxes.  Its page: of
+      // the next K tile, and of the up to two tiles whose V is still to come.
+      const int run = lane & (boxes - 1), half = lane >> (7 - log_box);
+      auto page_of = [&](int t) -> int {
+        const int j = t * kTile + (run << log_box);
+        if (!cache.page_table || j >= s.len) return cache.num_pages;   // loads as zeros
+        const int x = j >> log_box;
+        return __ldg(cache.page_table + (long long)s.gi * cache.pages_per_seq +
+                     (cache.runs == 1 ? x : x / cache.runs));
+      };
+      int page_k = page_of(s.t0), page_v0 = 0, page_v1 = 0, pending = 0;
       int kt = 0, vt = 0;    // next K, V tile
       for (int x = 0; x < 2 * s.n; ++x) {
         const bool is_k = kt < s.n && s.k_at(kt) == x;
@@ -768,52 +800,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         const PrefixCache& c = a.cache[ci];
         const CUtensorMap* map = is_k ? &maps.k[ci] : &maps.v[ci];
         const int row0 = (window ? t - s.hist : t) * kTile;
-        if (lane == 0) mbar_arrive_expect_tx(bar, C::TILE_BYTES);
-        if (!c.page_table) {
-          __syncwarp();
-          if (lane < D / 64)
-            tma_load_4d(dst + lane * C::HALF, map, lane * 64, row0, s.h * c.zh, s.gi * c.zb, bar);
-        } else {
-          // One box per (run of box_rows positions, 64-column half); a run
-          // lies on one page.  Pages behind the end or outside the pool load
-          // as zeros (a coordinate past the map's extent).
-          unsigned bad = 0;
-          const int boxes = kTile / c.box_rows;
-          int page = c.num_pages, r = 0;
-          if (lane < boxes * (D / 64)) {
-            r = lane % boxes * c.box_rows;
-            const int j = row0 + r;
-            if (j < s.len) {
-              page = __ldg(c.page_table + (long long)s.gi * c.pages_per_seq + j / c.page_size);
-              if (page < 0 || page >= c.num_pages) {
-                page = c.num_pages;
-                bad = 1;
-                raise_flag(DUSTIN_DEVFLAG_PAGE_RANGE);
-              } else {
-                page *= c.zb;
-              }
-            }
-          }
+        int row = row0 + (run << log_box), outer = s.gi * c.zb;
+        if (c.page_table) {
+          int page = is_k ? page_k : page_v0;
+          const bool in = row < s.len, bad = in && (page < 0 || page >= c.num_pages);
           if (is_k) {
-            // Positions on bad pages, for the softmax.
-            const unsigned runs = __ballot_sync(0xffffffffu, bad != 0);
+            // Positions on pages outside the pool, for the softmax.
+            const unsigned all = __ballot_sync(0xffffffffu, bad && half == 0);
             if (lane < 4) {
               unsigned bits = 0;
-              if (runs)
+              if (all)
                 for (int i = 0; i < 32; ++i)
-                  if (runs >> ((lane * 32 + i) / c.box_rows) & 1) bits |= 1u << i;
+                  if (all >> ((lane * 32 + i) >> log_box) & 1) bits |= 1u << i;
               sh.bad[tile_count % kMaskRing][lane] = bits;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.mask_full[tile_count % kMaskRing]));
             ++tile_count;
+            if (bad) raise_flag(DUSTIN_DEVFLAG_PAGE_RANGE);
           }
-          __syncwarp();
-          if (lane < boxes * (D / 64)) {
-            const int half = lane / boxes;
-            tma_load_4d(dst + half * C::HALF + r * 128, map, half * 64,
-                        (row0 + r) % c.page_size, s.h * c.zh, page, bar);
-          }
+          // Past the map's extent: zeros.
+          outer = in && !bad ? page * c.zb : c.num_pages;
+          const int r = row >> log_box;
+          row = c.runs == 1 ? 0 : (r - r / c.runs * c.runs) << log_box;
+        }
+        if (is_k) {
+          if (pending)
+            page_v1 = page_k;
+          else
+            page_v0 = page_k;
+          ++pending;
+          if (kt < s.n) page_k = page_of(s.t0 + kt);
+        } else {
+          page_v0 = page_v1;
+          --pending;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(bar, C::TILE_BYTES);
+        __syncwarp();
+        if (is_k) {
+          if (half < D / 64)
+            tma_load_5d(dst + half * C::HALF + (run << (log_box + 7)), map, 0, row, half,
+                        s.h * c.zh, outer, bar);
+        } else if (half == 0) {
+          tma_load_5d(dst + v_row<D>(run << log_box, log_box), map, 0, row, 0, s.h * c.zh, outer,
+                      bar);
         }
         filled = min(filled + 1, C::SLOTS);
         if (++slot == C::SLOTS) {
@@ -839,7 +869,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kStep = C::TILE_BYTES >> 4;       // slots apart, in descriptor units
     const uint32_t on = elect_one();
     const uint64_t qd0 = smem_desc(q_buf, 16, 1024), kd0 = smem_desc(ring, 16, 1024);
-    const uint64_t vd0 = smem_desc(ring, C::HALF, 1024);
     int slot = 0, turn = 0;
     uint32_t phase = 0, q_phase0 = 0, q_phase1 = 0, p_phase = 0;   // p_phase: a bit per stream
     bool ok = true;
@@ -860,12 +889,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mma_commit(on, smem_u32(&sh.s_full[st][x]));
     };
+    uint64_t vd0 = 0;                                    // by the segment's boxes
+    int log_box = 7;
     auto pv = [&](int st, int x, int vslot, bool acc) {
-      const uint64_t vd = vd0 + vslot * kStep + x * (kHalf * 128 >> 4);
+      const uint64_t vd = vd0 + vslot * kStep;
 #pragma unroll
       for (int k = 0; k < kHalf / 16; ++k)
         mma_ts(on, tmem + 256 + st * 128, tmem + st * 128 + x * kHalf + k * 8,
-               vd + (uint32_t)(k * 2048 >> 4), kPv, acc || k > 0);
+               vd + (v_row<D>(x * kHalf + k * 16, log_box) >> 4), kPv, acc || k > 0);
     };
     auto release = [&](int at) { mma_commit(on, smem_u32(&sh.empty[at])); };
     // Buffer x of a stream is used once per tile: one phase for both.
@@ -894,6 +925,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kind = sp->kind, n = sp->n, paired = sp->pair;
       if (kind < 0) break;
       done_with(at);
+      log_box = a.log_box[kind];
+      vd0 = smem_desc(ring, 128u << log_box, 1024);
       if (paired) {
         // K0 for both, then per tile: V, next K, half by half, A then B.
         if (!(ok = q_ready(0) && full())) break;
@@ -1101,11 +1134,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = pwait_warp(&sh.full[vat % C::SLOTS], (vat / C::SLOTS) & 1, &sh.abort);
             if (!ok) break;
             const uint32_t v = ring + vat % C::SLOTS * C::TILE_BYTES;
+            const int log_box = a.log_box[s.kind];
             for (int i = valid * 8 + row; i < kTile * 8; i += 128)
 #pragma unroll
               for (int c = 0; c < D / 64; ++c)
-                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(v + c * C::HALF +
-                                                                                i * 16),
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(
+                                 v + v_row<D>(i >> 3, log_box) + (c << (log_box + 7)) + (i & 7) * 16),
                              "r"(0)
                              : "memory");
             fence_proxy_async_smem();
@@ -1354,19 +1388,21 @@ EncodeTiledFn encode_tiled() {
   return f;
 }
 
-// [outer][h_kv][rows][d] of one cache tensor as 64-column boxes.  An axis of
-// stride 0 becomes an axis of one element.
+// [outer][h_kv][halves][rows][64] of one cache tensor, in boxes of `halves`
+// 64-column halves of box_rows rows.  An axis of stride 0 becomes an axis of
+// one element.
 bool make_map(CUtensorMap* map, const __nv_bfloat16* base, int d, long long rows, long long heads,
-              long long outer, const KvView& kv, int box_rows) {
+              long long outer, const KvView& kv, int box_rows, int halves) {
   EncodeTiledFn enc = encode_tiled();
   if (!enc) return false;
-  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)rows,
+  const cuuint64_t dims[5] = {64, (cuuint64_t)rows, (cuuint64_t)(d / 64),
                               (cuuint64_t)(kv.sh ? heads : 1), (cuuint64_t)(kv.sb ? outer : 1)};
-  const cuuint64_t strides[3] = {(cuuint64_t)kv.sn * 2, (cuuint64_t)(kv.sh ? kv.sh : kv.sn) * 2,
+  const cuuint64_t strides[4] = {(cuuint64_t)kv.sn * 2, 128,
+                                 (cuuint64_t)(kv.sh ? kv.sh : kv.sn) * 2,
                                  (cuuint64_t)(kv.sb ? kv.sb : kv.sn) * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<__nv_bfloat16*>(base), dims,
+  const cuuint32_t box[5] = {64, (cuuint32_t)box_rows, (cuuint32_t)halves, 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<__nv_bfloat16*>(base), dims,
              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1426,19 +1462,21 @@ PrefixKArgs shape_args(const PrefixArgs& p, int sms, Layout* lay) {
 }
 
 // The split of prefixes of one length (Walk::search for those on the device):
-// the smallest M, from the even share on, that fits the CTAs.  Own parts of
-// unknown length count as the longest: a line shorter than that ends early,
-// a longer one would hold up everything.
-void host_split(PrefixKArgs& a, bool lengths_given) {
+// the smallest M, from the even share on, that fits the CTAs.  Own parts
+// whose lengths are on the device count as 5/8 of the longest: batches of
+// continuations lie between a third of that and all of it.
+void host_split(PrefixKArgs& a, bool lengths_given, bool own_given) {
   a.split = a.np = a.ns = a.range = 0;
   const long long tp = (a.n[0] + kTile - 1) / kTile;
-  const long long to = (a.n[1] + kTile - 1) / kTile + a.win_tiles;
+  const long long most = (a.n[1] + kTile - 1) / kTile;
+  const long long to = (own_given ? (5 * most + 7) / 8 : most) + a.win_tiles;
   const int rt = a.row_tiles[0], pairs = rt / 2, single = rt & 1;
   if (lengths_given || tp == 0 || (long long)a.count[0] * a.hkv * ((rt + 1) / 2) > a.grid) return;
   const long long wp = tp * rt * a.count[0] * a.hkv * unit_cost(0);
   const long long wo = to * a.count[1] * a.hkv * a.row_tiles[1] * unit_cost(1) +
                        (to > 0) * (long long)a.count[1] * a.hkv * ((a.row_tiles[1] + 1) / 2) * kSegmentCost;
-  const long long least = std::max<long long>(2, ((wp + wo + a.grid - 1) / a.grid + 3) / unit_cost(0));
+  const long long share = (wp + wo + a.grid - 1) / a.grid;
+  const long long least = std::max<long long>(2, (share + 3) / unit_cost(0));
   for (long long m = least; m <= 3 * least; ++m) {
     // A pair's tile is two units.
     const long long np = pairs ? std::min(tp, (2 * tp + m - 1) / m) : 0;
@@ -1446,6 +1484,7 @@ void host_split(PrefixKArgs& a, bool lengths_given) {
     const long long split = a.count[0] * a.hkv * (pairs * np + ns);
     const long long rest = (wo + m * unit_cost(0) - 1) / (m * unit_cost(0));
     if (split + rest > a.grid) continue;
+    if (rt <= 2 && on_line_is_shorter(m, share)) return;
     a.split = (int)split;
     a.np = (int)np;
     a.ns = (int)ns;
@@ -1491,7 +1530,7 @@ cudaError_t launch_attn_prefix(const PrefixArgs& p, int sms, void* ws, cudaStrea
   Layout lay;
   PrefixKArgs a = shape_args(p, sms, &lay);
   if (!p.has_win) a.win_tiles = 0;
-  host_split(a, p.prefix_len != nullptr);
+  host_split(a, p.prefix_len != nullptr, p.own_len != nullptr);
   a.q = p.q;
   a.prefix_len = p.prefix_len;
   a.own_len = p.own_len;
@@ -1506,25 +1545,27 @@ cudaError_t launch_attn_prefix(const PrefixArgs& p, int sms, void* ws, cudaStrea
   const KvView* views[3] = {p.n_prefix > 0 ? &p.prefix : nullptr, p.n_own > 0 ? &p.own : nullptr,
                             p.has_win ? &p.win : nullptr};
   const int rows[3] = {p.n_prefix, p.n_own, p.w};
+  a.log_box[0] = a.log_box[1] = 7;
+  for (int c = 0; c < 2; ++c)
+    if (views[c] && views[c]->page_table)   // the largest power of two that divides page and tile
+      for (a.log_box[c] = 4; a.log_box[c] < 7 && views[c]->page_size % (2 << a.log_box[c]) == 0;)
+        ++a.log_box[c];
   for (int c = 0; c < 3; ++c) {
     if (!views[c]) continue;
     const KvView& kv = *views[c];
     PrefixCache& pc = a.cache[c];
     const bool paged = kv.page_table != nullptr;
     pc.page_table = kv.page_table;
-    pc.page_size = kv.page_size;
     pc.pages_per_seq = kv.pages_per_seq;
     pc.num_pages = kv.num_pages;
-    pc.box_rows = kTile;
-    if (paged)   // the largest power of two that divides the page and the tile
-      for (pc.box_rows = 16; pc.box_rows < kTile && kv.page_size % (2 * pc.box_rows) == 0;)
-        pc.box_rows *= 2;
+    pc.runs = paged ? kv.page_size >> a.log_box[c] : 1;
     pc.zh = kv.sh ? 1 : 0;
     pc.zb = kv.sb ? 1 : 0;
     const long long outer = paged ? kv.num_pages : c == 0 ? p.groups : p.b;
     const long long r = paged ? kv.page_size : rows[c];
-    if (!make_map(&maps.k[c], kv.k, p.d, r, p.hkv, outer, kv, pc.box_rows) ||
-        !make_map(&maps.v[c], kv.v, p.d, r, p.hkv, outer, kv, pc.box_rows))
+    const int box = 1 << a.log_box[c ? 1 : 0];
+    if (!make_map(&maps.k[c], kv.k, p.d, r, p.hkv, outer, kv, box, 1) ||
+        !make_map(&maps.v[c], kv.v, p.d, r, p.hkv, outer, kv, box, p.d / 64))
       return cudaErrorNotSupported;
   }
   return p.d == 64 ? run_prefix<64>(a, maps, p, st) : run_prefix<128>(a, maps, p, st);

@@ -121,13 +121,13 @@ __device__ __forceinline__ void mma_commit(uint32_t on, uint32_t bar) {
       : "memory");
 }
 
-// ---- tiled TMA loads of a 4-D box, completing on `bar`
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int x, int y, int z,
-                                            int t, uint32_t bar) {
+// ---- tiled TMA loads of a 5-D box, completing on `bar`
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* map, int x, int y, int z,
+                                            int t, int u, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(t), "r"(bar)
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(t), "r"(u), "r"(bar)
       : "memory");
 }
 
