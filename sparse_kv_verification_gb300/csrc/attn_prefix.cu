@@ -56,7 +56,8 @@ __device__ unsigned int g_prefix_dev_flags;
 constexpr int kTile = 128;        // positions of a K/V tile, rows of a row tile
 constexpr int kHalf = 64;         // positions of an S buffer
 constexpr int kSoftmaxWarps = 4;  // per stream
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kWalkWarp = 10, kTableWarp = 11, kQWarp = 12, kQWarps = 4;
+constexpr int kMmaWarp = 0, kLoadWarp = 1, kWalkWarp = 2, kTableWarp = 3, kQWarp = 4, kQWarps = 4,
+              kSoftmaxWarp = 8;
 constexpr int kThreads = 16 * 32;
 // Registers: a softmax thread holds 64 scores and their weights; the other
 // two warpgroups give up what they need beyond the launch's 128.
@@ -64,6 +65,8 @@ struct Split {
   static constexpr int NT = kThreads, NPW = 8, NCW = 2 * kSoftmaxWarps;
   static constexpr int PRODUCER_REGS = 112, CONSUMER_REGS = 144;
 };
+// Weights of one half tile's row may add up to this.
+constexpr float kMostWeight = 256.f;
 constexpr int kMaskRing = 8;
 constexpr int kSegRing = 4;
 
@@ -144,7 +147,7 @@ __device__ __forceinline__ uint32_t v_row(int row, int log_box) {
 struct Control {
   float2 exchange[2][kTile];       // m, l of a single's streams
   unsigned long long full[10], empty[10];
-  unsigned long long q_full[2], q_empty[2], s_full[2][2], p_ready[2][2], o_final[2];
+  unsigned long long q_full[2], q_empty[2], s_full[2], p_ready[2][2], half_done[2], o_final[2];
   unsigned long long seg_full[kSegRing], seg_empty[kSegRing], mask_full[kMaskRing], drain;
   unsigned bad[kMaskRing][4];      // positions on pages outside the pool
   Seg seg[kSegRing];
@@ -606,13 +609,22 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// p = 2^(x * scale - m) as 16 bf16 pairs, the fp32 values added to sum, the
-// largest x to top.
+// The largest of 32 scores and top.
+__device__ __forceinline__ float max32(const uint32_t (&x)[32], float top) {
+  float a = top, b = __uint_as_float(x[0]);
+#pragma unroll
+  for (int i = 1; i < 29; i += 4) {
+    a = max3(a, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+    b = max3(b, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+  }
+  a = max3(a, __uint_as_float(x[29]), __uint_as_float(x[30]));
+  return max3(a, b, __uint_as_float(x[31]));
+}
+// p = 2^(x * scale - m) as 16 bf16 pairs, the fp32 values added to sum.
 __device__ __forceinline__ void exp32(const uint32_t (&x)[32], uint64_t scale, uint64_t minus_m,
-                                      uint64_t (&sum)[2], float& top, uint32_t* p) {
+                                      uint64_t (&sum)[2], uint32_t* p) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    top = max3(top, __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
     const uint64_t y = fma2(pack2(x[2 * i], x[2 * i + 1]), scale, minus_m);
     const float e0 = ex2(lo_of(y)), e1 = ex2(hi_of(y));
     sum[i & 1] = add2(sum[i & 1], pack2(__float_as_uint(e0), __float_as_uint(e1)));
@@ -657,10 +669,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&sh.q_full[s]), kQWarps);
       mbar_init(smem_u32(&sh.q_empty[s]), 1);
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(smem_u32(&sh.s_full[s][i]), 1);
-        mbar_init(smem_u32(&sh.p_ready[s][i]), kSoftmaxWarps);
-      }
+      mbar_init(smem_u32(&sh.s_full[s]), 1);
+      mbar_init(smem_u32(&sh.half_done[s]), 1);
+      for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.p_ready[s][i]), kSoftmaxWarps);
       mbar_init(smem_u32(&sh.o_final[s]), 1);
     }
     for (int i = 0; i < kMaskRing; ++i) mbar_init(smem_u32(&sh.mask_full[i]), 1);
@@ -694,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(smem_u32(&sh.seg_empty[at % kSegRing]));
   };
 
-  if (warp >= kMmaWarp) give_registers();   // one instruction for whole warpgroups
+  if (warp < kSoftmaxWarp) give_registers();   // one instruction for whole warpgroups
   if (warp == kWalkWarp) {
     // --------------------------------------------------------------- walker
     role_begin();
@@ -713,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kTableWarp) {
     role_begin();
     if (blockIdx.x == 0) Walk(a, true);
-  } else if (warp >= kQWarp) {
+  } else if (warp >= kQWarp && warp < kSoftmaxWarp) {
     // ------------------------------------------------------------------- Q
     // Row tiles in the tensor cores' swizzled layout; a pair fills both
     // buffers, singles take turns, so that the next one's rows are there
@@ -865,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The whole warp walks, one lane issues.  Slots are used in ring order: a
     // running position serves K and V alike.
     role_begin();
-    constexpr uint32_t kQk = mma_idesc(128, kHalf, false), kPv = mma_idesc(128, D, true);
+    constexpr uint32_t kQk = mma_idesc(128, kTile, false), kPv = mma_idesc(128, D, true);
     constexpr uint32_t kStep = C::TILE_BYTES >> 4;       // slots apart, in descriptor units
     const uint32_t on = elect_one();
     const uint64_t qd0 = smem_desc(q_buf, 16, 1024), kd0 = smem_desc(ring, 16, 1024);
@@ -879,15 +890,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     auto full = [&]() { return pwait_warp(&sh.full[slot], phase, &sh.abort); };
-    // Scores of 64 positions (rows x * 64 .. of a K tile) into buffer x.
-    auto qk = [&](int st, int x, int buf, int kslot) {
-      const uint64_t qd = qd0 + buf * kStep, kd = kd0 + kslot * kStep + x * (kHalf * 128 >> 4);
+    auto qk = [&](int st, int buf, int kslot) {
+      const uint64_t qd = qd0 + buf * kStep, kd = kd0 + kslot * kStep;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint32_t off = (uint32_t)((k / 4) * C::HALF + (k % 4) * 32) >> 4;
-        mma_ss(on, tmem + st * 128 + x * kHalf, qd + off, kd + off, kQk, k > 0);
+        mma_ss(on, tmem + st * 128, qd + off, kd + off, kQk, k > 0);
       }
-      mma_commit(on, smem_u32(&sh.s_full[st][x]));
+      mma_commit(on, smem_u32(&sh.s_full[st]));
     };
     uint64_t vd0 = 0;                                    // by the segment's boxes
     int log_box = 7;
@@ -895,11 +905,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t vd = vd0 + vslot * kStep;
 #pragma unroll
       for (int k = 0; k < kHalf / 16; ++k)
-        mma_ts(on, tmem + 256 + st * 128, tmem + st * 128 + x * kHalf + k * 8,
+        mma_ts(on, tmem + 256 + st * 128, tmem + st * 128 + x * (kHalf / 2) + k * 8,
                vd + (v_row<D>(x * kHalf + k * 16, log_box) >> 4), kPv, acc || k > 0);
     };
     auto release = [&](int at) { mma_commit(on, smem_u32(&sh.empty[at])); };
-    // Buffer x of a stream is used once per tile: one phase for both.
+    // Both halves of P come once per tile: one phase for both.
     auto p_ready = [&](int st, int x) {
       const bool r = pwait_warp(&sh.p_ready[st][x], p_phase >> st & 1, &sh.abort);
       tc_fence_after();
@@ -912,12 +922,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       return r;
     };
-    // A tile's second half done: no more scores follow in this stream.  After
-    // the first half of the last tile buffer 0 is signalled all the same: by
-    // it a softmax thread knows that the product before is complete.
-    auto tail = [&](int st, int x) {
-      mma_commit(on, x ? smem_u32(&sh.o_final[st]) : smem_u32(&sh.s_full[st][0]));
-    };
     for (int at = 0; ok; ++at) {
       const Seg* sp = segment(at);
       ok = sp != nullptr;
@@ -928,13 +932,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       log_box = a.log_box[kind];
       vd0 = smem_desc(ring, 128u << log_box, 1024);
       if (paired) {
-        // K0 for both, then per tile: V, next K, half by half, A then B.
+        // K0 for both, then per tile, A then B, V half by half and the next K.
         if (!(ok = q_ready(0) && full())) break;
-        qk(0, 0, 0, slot);
-        qk(0, 1, 0, slot);
+        qk(0, 0, slot);
         if (!(ok = q_ready(1))) break;
-        qk(1, 0, 1, slot);
-        qk(1, 1, 1, slot);
+        qk(1, 1, slot);
         release(slot);
         next_slot();
         for (int i = 0; ok && i < n; ++i) {
@@ -942,28 +944,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int vslot = slot;
           int kslot = 0;
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-#pragma unroll
-            for (int st = 0; st < 2; ++st) {
-              if (!(ok = ok && p_ready(st, x))) break;
-              if (x == 0 && st == 0) {
+          for (int st = 0; st < 2; ++st) {
+            if (!(ok = ok && p_ready(st, 0))) break;
+            if (st == 0) {
+              if (!(ok = full())) break;
+              next_slot();
+            }
+            pv(st, 0, vslot, i > 0);
+            mma_commit(on, smem_u32(&sh.half_done[st]));
+            if (!(ok = p_ready(st, 1))) break;
+            pv(st, 1, vslot, true);
+            if (st == 1) release(vslot);
+            if (more) {
+              if (st == 0) {
                 if (!(ok = full())) break;
+                kslot = slot;
                 next_slot();
               }
-              pv(st, x, vslot, i > 0 || x > 0);
-              if (x == 1 && st == 1) release(vslot);
-              if (more) {
-                if (x == 0 && st == 0) {
-                  if (!(ok = full())) break;
-                  kslot = slot;
-                  next_slot();
-                }
-                qk(st, x, st, kslot);
-                if (x == 1 && st == 1) release(kslot);
-              } else {
-                tail(st, x);
-                if (x == 1) mma_commit(on, smem_u32(&sh.q_empty[st]));
-              }
+              qk(st, st, kslot);
+              if (st == 1) release(kslot);
+            } else {
+              mma_commit(on, smem_u32(&sh.o_final[st]));
+              mma_commit(on, smem_u32(&sh.q_empty[st]));
             }
           }
           p_phase ^= 3;
@@ -975,40 +977,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = q_ready(buf))) break;
         for (int st = 0; st < min(n, 2); ++st) {
           if (!(ok = full())) break;
-          qk(st, 0, buf, slot);
-          qk(st, 1, buf, slot);
+          qk(st, buf, slot);
           release(slot);
           next_slot();
         }
         if (n <= 2) mma_commit(on, smem_u32(&sh.q_empty[buf]));
         for (int i = 0; ok && i < n; ++i) {
           const int st = i & 1;
-          const bool more = i + 2 < n;
-          const int vslot = slot;
-          int kslot = 0;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (!(ok = p_ready(st, x))) break;
-            if (x == 0) {
-              if (!(ok = full())) break;
-              next_slot();
-            }
-            pv(st, x, vslot, i > 1 || x > 0);
-            if (x) release(vslot);
-            if (more) {
-              if (x == 0) {
-                if (!(ok = full())) break;
-                kslot = slot;
-                next_slot();
-              }
-              qk(st, x, buf, kslot);
-              if (x) {
-                release(kslot);
-                if (i + 3 == n) mma_commit(on, smem_u32(&sh.q_empty[buf]));
-              }
-            } else {
-              tail(st, x);
-            }
+          if (!(ok = p_ready(st, 0) && full())) break;
+          pv(st, 0, slot, i > 1);
+          mma_commit(on, smem_u32(&sh.half_done[st]));
+          if (!(ok = p_ready(st, 1))) break;
+          pv(st, 1, slot, true);
+          release(slot);
+          next_slot();
+          if (i + 2 < n) {
+            if (!(ok = full())) break;
+            qk(st, buf, slot);
+            release(slot);
+            next_slot();
+            if (i + 3 == n) mma_commit(on, smem_u32(&sh.q_empty[buf]));
+          } else {
+            mma_commit(on, smem_u32(&sh.o_final[st]));
           }
           p_phase ^= 1u << st;
         }
@@ -1019,15 +1009,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(smem_u32(&sh.drain), 0, kWaitLimitCycles);
     }
     __syncwarp();
-  } else if (warp < kMmaWarp) {
+  } else {
     // -------------------------------------------------------------- softmax
     take_registers();
-    const int st = warp >> 2, row = tid & 127;
+    const int st = (warp - kSoftmaxWarp) >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // TMEM lane of the warp's first row
     const uint32_t tS = tmem + lanes + st * 128, tO = tmem + lanes + 256;
     const uint64_t scale2 = pack2(__float_as_uint(a.scale_log2), __float_as_uint(a.scale_log2));
     int ring0 = 0, tiles0 = 0;                 // ring position, paged tiles before the segment
-    uint32_t s_phase = 0, o_phase = 0;         // s_phase: a bit per buffer
+    uint32_t s_phase = 0, h_phase = 0, o_phase = 0;
     bool ok = true;
     for (int at = 0; ok; ++at) {
       const Seg* sp = segment(at);
@@ -1041,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = (warp & 3) * 32 < rows;           // the warp has rows
       const int t_row = s.kind ? (rt * kTile + row) % a.w : 0;   // window row of this row
       float m = -INFINITY;
-      uint64_t sum[2] = {0, 0};
+      uint64_t sum = 0;
       for (int step = 0; ok && step < steps; ++step) {
         const int tl = s.tile(st, step), t = s.t0 + tl;
         const bool window = s.kind && t >= s.hist;
@@ -1055,20 +1045,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                           ((tiles0 + tl) / kMaskRing) & 1, &sh.abort);
           if (!ok) break;
         }
+        ok = pwait_warp(&sh.s_full[st], s_phase, &sh.abort);
+        if (!ok) break;
+        s_phase ^= 1;
+        tc_fence_after();
 #pragma unroll 1
         for (int x = 0; x < 2; ++x) {
-          ok = pwait_warp(&sh.s_full[st][x], s_phase >> x & 1, &sh.abort);
-          if (!ok) break;
-          s_phase ^= 1u << x;
-          tc_fence_after();
           if (live) {
-            // The reference maximum m moves only when scores exceed it by
-            // more than a factor 2^8, so P is formed with the old one while
-            // the maximum is still being taken; where it does move (the
-            // first scores, then rarely), S, not overwritten yet, is read
-            // again.
+            // The reference m is a maximum of scores seen before.  It moves
+            // only when a row's weights 2^(s - m) of these 64 columns add up
+            // to more than 2^8 (or when it is not set yet), so no maximum is
+            // taken and O not scaled for most of them, and a weight never
+            // exceeds 2^8.
             const uint32_t tX = tS + x * kHalf;
             uint32_t p[32];
+            bool move = __any_sync(0xffffffffu, m == -INFINITY);
             for (;;) {
               uint32_t x0[32], x1[32];
               tmem_ld32(tX, x0);
@@ -1086,45 +1077,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                   mask_bits(x1, b1);
                 }
               }
+              if (move) {
+                const float top = max32(x1, max32(x0, -INFINITY)) * a.scale_log2;
+                const bool up = top > m;
+                const float f = up ? ex2(m - top) : 1.f;
+                if (up) m = top;
+                const uint64_t f2 = pack2(__float_as_uint(f), __float_as_uint(f));
+                sum = fma2(sum, f2, 0);
+                if (step > 0 || x > 0) {
+                  // O is scaled once the product before is complete.  That of
+                  // an earlier tile is: it was issued before these scores.
+                  if (x) {
+                    ok = pwait_warp(&sh.half_done[st], h_phase, &sh.abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                  }
+#pragma unroll 1
+                  for (int c = 0; c < D / 32; ++c) {
+                    const uint32_t to_o = tO + st * 128 + c * 32;
+                    uint32_t o[32];
+                    tmem_ld32(to_o, o);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                    tmem_st32(to_o, o);
+                  }
+                }
+              }
               const float ms = m == -INFINITY ? 0.f : -m;
               const uint64_t mm = pack2(__float_as_uint(ms), __float_as_uint(ms));
-              uint64_t to[2] = {sum[0], sum[1]};
-              float top0 = -INFINITY, top1 = -INFINITY;
-              exp32(x0, scale2, mm, to, top0, p);
-              exp32(x1, scale2, mm, to, top1, p + 16);
-              const float top = fmaxf(top0, top1) * a.scale_log2;
-              const bool up = m == -INFINITY ? top > m : top > m + kLazyRescale;
-              if (!__any_sync(0xffffffffu, up)) {
-                sum[0] = to[0];
-                sum[1] = to[1];
+              uint64_t part[2] = {0, 0};
+              exp32(x0, scale2, mm, part, p);
+              exp32(x1, scale2, mm, part, p + 16);
+              const uint64_t all = add2(part[0], part[1]);
+              move = __any_sync(0xffffffffu, lo_of(all) + hi_of(all) > kMostWeight);
+              if (!move) {
+                sum = add2(sum, all);
                 break;
-              }
-              const float f = up ? ex2(m - top) : 1.f;
-              if (up) m = top;
-              const uint64_t f2 = pack2(__float_as_uint(f), __float_as_uint(f));
-              sum[0] = fma2(sum[0], f2, 0);
-              sum[1] = fma2(sum[1], f2, 0);
-              if (step > 0 || x > 0) {
-                // O is scaled once the product before is complete: it was
-                // issued before the scores after these, or what is signalled
-                // in their place.
-                ok = pwait_warp(&sh.s_full[st][x ^ 1], s_phase >> (x ^ 1) & 1, &sh.abort);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                  const uint32_t to_o = tO + st * 128 + c * 32;
-                  uint32_t o[32];
-                  tmem_ld32(to_o, o);
-                  tc_wait_ld();
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                  tmem_st32(to_o, o);
-                }
               }
             }
             if (!ok) break;
-            tmem_st32(tX, p);
+            tmem_st32(tS + x * (kHalf / 2), p);
             tc_wait_st();
           }
           // V rows behind the end hold whatever the cache holds there, NaN
@@ -1148,12 +1141,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.p_ready[st][x]));
         }
+        h_phase ^= 1;
       }
       if (!ok) break;
       ring0 += 2 * s.n;
       if (paged) tiles0 += max(0, min(s.t0 + s.n, s.hist) - s.t0);
       if (steps == 0) continue;
-      s_phase ^= 1;                            // buffer 0 is signalled once more after the last scores
       ok = pwait_warp(&sh.o_final[st], o_phase, &sh.abort);
       if (!ok) break;
       o_phase ^= 1;
@@ -1165,8 +1158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int streams = a.streams[s.kind];
       const long long slot = (long long)s.slot * streams + (s.pair ? st : 0);
       float* out = a.ws_o[s.kind] + slot * sr * D + row * 4;
-      const uint64_t both = add2(sum[0], sum[1]);
-      float l = lo_of(both) + hi_of(both);
+      float l = lo_of(sum) + hi_of(sum);
       if (s.pair || s.n == 1) {
         if (live) {
 #pragma unroll
