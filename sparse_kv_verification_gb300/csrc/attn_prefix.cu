@@ -148,7 +148,7 @@ struct Control {
   float2 exchange[2][kTile];       // m, l of a single's streams
   unsigned long long full[10], empty[10];
   unsigned long long q_full[2], q_empty[2], s_full[2], p_ready[2][2], half_done[2], o_final[2];
-  unsigned long long seg_full[kSegRing], seg_empty[kSegRing], mask_full[kMaskRing], drain;
+  unsigned long long seg_full[kSegRing], seg_empty[kSegRing], mask_full[kMaskRing], meet, drain;
   unsigned bad[kMaskRing][4];      // positions on pages outside the pool
   Seg seg[kSegRing];
   int abort;
@@ -679,6 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&sh.seg_full[i]), 1);
       mbar_init(smem_u32(&sh.seg_empty[i]), 2 * kSoftmaxWarps + 2 + kQWarps);
     }
+    mbar_init(smem_u32(&sh.meet), 2 * kSoftmaxWarps);
     mbar_init(smem_u32(&sh.drain), 1);
     mbar_fence_init();
     sh.abort = 0;
@@ -1016,9 +1017,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // TMEM lane of the warp's first row
     const uint32_t tS = tmem + lanes + st * 128, tO = tmem + lanes + 256;
     const uint64_t scale2 = pack2(__float_as_uint(a.scale_log2), __float_as_uint(a.scale_log2));
+    const uint64_t one2 = pack2(0x3f800000u, 0x3f800000u);
     int ring0 = 0, tiles0 = 0;                 // ring position, paged tiles before the segment
-    uint32_t s_phase = 0, h_phase = 0, o_phase = 0;
+    uint32_t s_phase = 0, h_phase = 0, o_phase = 0, meet_phase = 0;
     bool ok = true;
+    auto meet = [&]() {   // of both streams
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.meet));
+      const bool r = pwait_warp(&sh.meet, meet_phase, &sh.abort);
+      meet_phase ^= 1;
+      return r;
+    };
     for (int at = 0; ok; ++at) {
       const Seg* sp = segment(at);
       if (!sp || sp->kind < 0) break;
@@ -1038,12 +1047,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int valid = s.len - t * kTile;
         // Columns [0, lim) of the tile count.
         const int lim = window ? min(a.w, t_row + 1) - (t - s.hist) * kTile : valid;
-        const bool masked = __any_sync(0xffffffffu, lim < kTile);
-        const bool bad = paged && !window;
-        if (bad) {
-          ok = pwait_warp(&sh.mask_full[(tiles0 + tl) % kMaskRing],
-                          ((tiles0 + tl) / kMaskRing) & 1, &sh.abort);
+        bool special = __any_sync(0xffffffffu, lim < kTile);   // columns that do not count
+        const unsigned* bad = nullptr;
+        if (paged && !window) {
+          const int k = (tiles0 + tl) % kMaskRing;
+          ok = pwait_warp(&sh.mask_full[k], ((tiles0 + tl) / kMaskRing) & 1, &sh.abort);
           if (!ok) break;
+          bad = sh.bad[k];
+          special |= (bad[0] | bad[1] | bad[2] | bad[3]) != 0;
         }
         ok = pwait_warp(&sh.s_full[st], s_phase, &sh.abort);
         if (!ok) break;
@@ -1056,34 +1067,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             // only when a row's weights 2^(s - m) of these 64 columns add up
             // to more than 2^8 (or when it is not set yet), so no maximum is
             // taken and O not scaled for most of them, and a weight never
-            // exceeds 2^8.
-            const uint32_t tX = tS + x * kHalf;
-            uint32_t p[32];
-            bool move = __any_sync(0xffffffffu, m == -INFINITY);
-            for (;;) {
-              uint32_t x0[32], x1[32];
+            // exceeds 2^8.  Masks are the slow path's alone: with them in the
+            // fast one, 512 rows x 32768 positions took 3% longer.
+            const uint32_t tX = tS + x * kHalf, tP = tS + x * (kHalf / 2);
+            bool slow = special || __any_sync(0xffffffffu, m == -INFINITY);
+            if (!slow) {
+              uint32_t x0[32], x1[32], p[32];
               tmem_ld32(tX, x0);
               tmem_ld32(tX + 32, x1);
               tc_wait_ld();
-              if (masked) {
-                mask32(x0, lim - x * kHalf);
-                mask32(x1, lim - x * kHalf - 32);
+              const uint64_t mm = pack2(__float_as_uint(-m), __float_as_uint(-m));
+              uint64_t part[2] = {0, 0};
+              exp32(x0, scale2, mm, part, p);
+              exp32(x1, scale2, mm, part, p + 16);
+              const uint64_t all = add2(part[0], part[1]);
+              slow = __any_sync(0xffffffffu, lo_of(all) + hi_of(all) > kMostWeight);
+              if (!slow) {
+                sum = add2(sum, all);
+                tmem_st32(tP, p);
               }
-              if (bad) {
-                const int k = (tiles0 + tl) % kMaskRing;
-                const unsigned b0 = sh.bad[k][2 * x], b1 = sh.bad[k][2 * x + 1];
-                if (b0 | b1) {
-                  mask_bits(x0, b0);
-                  mask_bits(x1, b1);
+            }
+            if (slow) {
+              auto load = [&](int c, uint32_t (&v)[32]) {
+                tmem_ld32(tX + c * 32, v);
+                tc_wait_ld();
+                if (special) {
+                  mask32(v, lim - x * kHalf - c * 32);
+                  if (bad) mask_bits(v, bad[2 * x + c]);
                 }
+              };
+              float top = -INFINITY;
+#pragma unroll 1
+              for (int c = 0; c < 2; ++c) {
+                uint32_t v[32];
+                load(c, v);
+                top = max32(v, top);
               }
-              if (move) {
-                const float top = max32(x1, max32(x0, -INFINITY)) * a.scale_log2;
-                const bool up = top > m;
+              top *= a.scale_log2;
+              const bool up = top > m;
+              if (__any_sync(0xffffffffu, up)) {
                 const float f = up ? ex2(m - top) : 1.f;
                 if (up) m = top;
-                const uint64_t f2 = pack2(__float_as_uint(f), __float_as_uint(f));
-                sum = fma2(sum, f2, 0);
+                sum = fma2(sum, pack2(__float_as_uint(f), __float_as_uint(f)), 0);
                 if (step > 0 || x > 0) {
                   // O is scaled once the product before is complete.  That of
                   // an earlier tile is: it was issued before these scores.
@@ -1104,20 +1129,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                   }
                 }
               }
+              // The scaled score rounded as the maximum was: a weight is at
+              // most 1 here, whatever the size of the scores.
               const float ms = m == -INFINITY ? 0.f : -m;
               const uint64_t mm = pack2(__float_as_uint(ms), __float_as_uint(ms));
               uint64_t part[2] = {0, 0};
-              exp32(x0, scale2, mm, part, p);
-              exp32(x1, scale2, mm, part, p + 16);
-              const uint64_t all = add2(part[0], part[1]);
-              move = __any_sync(0xffffffffu, lo_of(all) + hi_of(all) > kMostWeight);
-              if (!move) {
-                sum = add2(sum, all);
-                break;
+#pragma unroll 1
+              for (int c = 0; c < 2; ++c) {
+                uint32_t v[32], p[16];
+                load(c, v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  v[i] = __float_as_uint(__fmul_rn(__uint_as_float(v[i]), a.scale_log2));
+                exp32(v, one2, mm, part, p);
+                tmem_st16(tP + c * 16, p);   // over scores that are read
               }
+              sum = add2(sum, add2(part[0], part[1]));
             }
-            if (!ok) break;
-            tmem_st32(tS + x * (kHalf / 2), p);
             tc_wait_st();
           }
           // V rows behind the end hold whatever the cache holds there, NaN
@@ -1171,7 +1199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         sh.exchange[st][row] = make_float2(m, l);
-        named_bar_sync(1, 2 * kTile);          // both streams' O, m and l are there
+        if (!(ok = meet())) break;             // both streams' O, m and l are there
         const float2 y = sh.exchange[st ^ 1][row];
         const float big = fmaxf(m, y.x), ref = big == -INFINITY ? 0.f : big;
         const float f0 = ex2(m - ref), f1 = ex2(y.x - ref);
@@ -1195,7 +1223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tc_fence_before();
-        named_bar_sync(1, 2 * kTile);          // read before the next segment writes
+        if (!(ok = meet())) break;             // read before the next segment writes
       }
       if (row < rows && (s.pair || st == 0)) {
         float2* ml = a.ws_ml[s.kind] + slot * sr + row;
