@@ -28,17 +28,14 @@
 // (on the line: each of two parts) has its place, and
 // attn_prefix_combine_kernel adds each row's partials in a fixed order.
 //
-// Roles of the 16 warps: 0-3 and 4-7 softmax (one thread per row of stream
-// A / B), 8 issues tcgen05.mma, 9 TMA loads of K and V, 10 walks the CTA's
-// share and publishes its segments, 11 (of CTA 0) writes the plan for the
-// combine kernel, 12-15 copy Q rows.  S = Q K^T and O += P V
-// accumulate in tensor memory (512 columns: two S buffers of 64 positions and
-// an O per stream); P replaces S in place as bf16 and is read from there as
-// the A operand, so only Q, K and V live in shared memory.  With two S
-// buffers a stream's next scores are there before its P is consumed: a
-// softmax warp never waits for its own product, nor the tensor cores for one
-// softmax (with one buffer of 128 positions per stream, steps of 4400
-// cycles; see the figures at the kernel).
+// Roles of the 16 warps: 0 issues tcgen05.mma, 1 the TMA loads of K and V, 2
+// walks the CTA's share and publishes its segments, 3 (of CTA 0) writes the
+// plan for the combine kernel, 4-7 copy Q rows, 8-11 and 12-15 are the
+// softmax of stream A and B, one thread per row.  S = Q K^T and O += P V
+// accumulate in tensor memory (512 columns: per stream an S of 128 positions
+// and an O); P replaces S in place as bf16, half by half, and is read from
+// there as the A operand, so only Q, K and V live in shared memory.  While one
+// stream's softmax works, the tensor cores work for the other.
 #include <algorithm>
 #include <cuda.h>
 
@@ -1088,6 +1085,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             if (slow) {
+              // 32-column chunks with columns that count for some row
+              const int nc = !special ? 2
+                                      : __any_sync(0xffffffffu, lim > x * kHalf) +
+                                            __any_sync(0xffffffffu, lim > x * kHalf + 32);
               auto load = [&](int c, uint32_t (&v)[32]) {
                 tmem_ld32(tX + c * 32, v);
                 tc_wait_ld();
@@ -1098,7 +1099,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               };
               float top = -INFINITY;
 #pragma unroll 1
-              for (int c = 0; c < 2; ++c) {
+              for (int c = 0; c < nc; ++c) {
                 uint32_t v[32];
                 load(c, v);
                 top = max32(v, top);
@@ -1137,11 +1138,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
               for (int c = 0; c < 2; ++c) {
                 uint32_t v[32], p[16];
-                load(c, v);
+                if (c < nc) {
+                  load(c, v);
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  v[i] = __float_as_uint(__fmul_rn(__uint_as_float(v[i]), a.scale_log2));
-                exp32(v, one2, mm, part, p);
+                  for (int i = 0; i < 32; ++i)
+                    v[i] = __float_as_uint(__fmul_rn(__uint_as_float(v[i]), a.scale_log2));
+                  exp32(v, one2, mm, part, p);
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) p[i] = 0;
+                }
                 tmem_st16(tP + c * 16, p);   // over scores that are read
               }
               sum = add2(sum, add2(part[0], part[1]));

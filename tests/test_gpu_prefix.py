@@ -195,6 +195,31 @@ def test_large_scores_and_a_rising_maximum():
     np.testing.assert_allclose(H.f64(lse), want_lse, atol=4e-3, rtol=1e-6)
 
 
+@pytest.mark.parametrize("order", ["rising", "falling", "shuffled"])
+@pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** 20, 2.0 ** 40])
+def test_scores_past_the_exponents_range(order, size):
+    """Scores up to 2^87, whose fp32 steps are far larger than 1: the one
+    largest score takes the whole row, its V exactly, and nothing loops or
+    overflows.  Neighbouring keys differ by a step of bf16 (2^-8 of them at
+    least), so no other score is within the range of an exponential."""
+    c = Case(2, 1, 4, 1, 128, 2, 200, 0, win=False, seed=21)
+    at = {"rising": torch.arange(200), "falling": torch.arange(200).flip(0),
+          "shuffled": torch.randperm(200, generator=I.generator(5))}[order]
+    # 200 neighbours of bf16 from 1 on, in that order
+    keys = (torch.arange(200, dtype=torch.int32) + (0x3F80)).to(torch.int16).view(torch.bfloat16)
+    c.q.fill_(size)
+    c.kv[0][0] = (keys[at] * size).view(1, 1, 200, 1).expand(1, 1, 200, 128).contiguous()
+    c.stored = [[x.to(DEV) for x in kv] for kv in c.kv]
+    o, lse = c.run()
+    best = int(at.argmax())
+    want = c.kv[0][1][0, 0, best].to(DEV).expand_as(o)
+    assert torch.equal(o, want)
+    score = 128.0 * size * float(keys[-1]) * size * c.scale
+    # The sum of 128 equal products, the scale, the maximum in base 2 and back
+    # to base e: a rounding of 2^-24 each, of the scale's constant too.
+    np.testing.assert_allclose(H.f64(lse), score, rtol=8 * 2.0 ** -24)
+
+
 def test_cache_layouts():
     """[b][n][h][d] caches, one kv head's storage for all heads, one
     sequence's storage for all."""
