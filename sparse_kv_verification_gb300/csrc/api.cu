@@ -811,6 +811,9 @@ int dustin_full_verify_attn_window(int b, int h_q, int h_kv, int d, int w, int n
                   ws, ws_bytes, flags, stream);
 }
 
+// Partials are found by 31-bit indices of 16 bytes.
+static constexpr size_t kPrefixWorkspaceMost = size_t(1) << 35;
+
 static int check_prefix_shape(int b, int groups, int h_q, int h_kv, int d, int w, int n_prefix,
                               int n_own, const char* what) {
   if (groups < 1 || b % groups)
@@ -824,7 +827,8 @@ static int check_prefix_shape(int b, int groups, int h_q, int h_kv, int d, int w
   const double rows = (double)(h_q / h_kv) * w;
   if (h_kv * (groups * tiles * (rows * (b / groups) / 128 + 1) + b * own * (rows / 128 + 1)) >
           (double)(1 << 25) ||
-      rows * b * h_kv > (double)(1 << 30) || b > (1 << 20))
+      rows * b * h_kv > (double)(1 << 30) || b > (1 << 20) || n_prefix > (1 << 27) ||
+      n_own > (1 << 27))
     return fail(DUSTIN_ERR_SHAPE, "%s: problem too large", what);
   return DUSTIN_OK;
 }
@@ -848,7 +852,9 @@ size_t dustin_prefix_verify_attn_workspace_size(int b, int groups, int h_q, int 
   if (b <= 0 || check_prefix_shape(b, groups, h_q, h_kv, d, w, n_prefix, n_own,
                                    "dustin_prefix_verify_attn_workspace_size"))
     return 0;
-  return prefix_workspace(prefix_args(b, groups, h_q, h_kv, d, w, n_prefix, n_own), sm_count());
+  const size_t need = prefix_workspace(prefix_args(b, groups, h_q, h_kv, d, w, n_prefix, n_own),
+                                       sm_count());
+  return need > kPrefixWorkspaceMost ? 0 : need;
 }
 
 int dustin_prefix_verify_attn(int b, int groups, int h_q, int h_kv, int d, int w, int n_prefix,
@@ -877,6 +883,7 @@ int dustin_prefix_verify_attn(int b, int groups, int h_q, int h_kv, int d, int w
   if (win && (rc = check_win(win, d, what))) return rc;
   PrefixArgs p = prefix_args(b, groups, h_q, h_kv, d, w, n_prefix, n_own);
   const size_t need = prefix_workspace(p, sm_count());
+  if (need > kPrefixWorkspaceMost) return fail(DUSTIN_ERR_SHAPE, "%s: problem too large", what);
   if (!ws || ws_bytes < need || !aligned16(ws))
     return fail(DUSTIN_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu (16-byte aligned)", what,
                 ws_bytes, need);

@@ -642,13 +642,6 @@ __device__ __forceinline__ void mask_bits(uint32_t (&x)[32], unsigned bad) {
     if (bad >> i & 1) x[i] = 0xff800000u;
 }
 
-// 32 columns to `out`, four to a piece, pieces `apart` floats apart.
-__device__ __forceinline__ void store_pieces(float* out, int apart, const uint32_t* o) {
-#pragma unroll
-  for (int i = 0; i < 32; i += 4)
-    *reinterpret_cast<uint4*>(out + (i / 4) * apart) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_prefix_kernel(const __grid_constant__ PrefixKArgs a, const __grid_constant__ Maps maps) {
@@ -1185,22 +1178,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       o_phase ^= 1;
       tc_fence_after();
-      // Partials: a pair's streams write their rows each; a single's are
-      // merged, each writing half of the columns.  Pieces of four columns,
-      // rows side by side: full lines per store.
+      // Partials: a pair's streams write their rows each; of a single's merged
+      // ones, stream B writes the lower 16 rows of each warp.  Of 16 columns
+      // lane i % 4 of a row's four lanes has 2 i, 2 i + 1, 8 + 2 i, 9 + 2 i, and
+      // keeps them together: a row lies in one piece (its 64-column blocks
+      // behind one another), 64 bytes of it per store.
       const int sr = a.slot_rows[s.kind];
       const int streams = a.streams[s.kind];
       const long long slot = (long long)s.slot * streams + (s.pair ? st : 0);
-      float* out = a.ws_o[s.kind] + slot * sr * D + row * 4;
+      float* out = a.ws_o[s.kind] + slot * sr * D + (lane & 3) * 4;
       float l = lo_of(sum) + hi_of(sum);
+      const int first = (warp & 3) * 32 + (lane >> 2);
+      auto put = [&](int r, float* to, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+        if (r < rows) *reinterpret_cast<uint4*>(to + r * D) = make_uint4(x, y, z, w);
+      };
       if (s.pair || s.n == 1) {
         if (live) {
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tO + st * 128 + c * 32, o);
-            tc_wait_ld();
-            if (row < rows) store_pieces(out + c * 8 * (sr * 4), sr * 4, o);
+            for (int c = 0; c < D; c += 64) {
+              uint32_t o[32];
+              tmem_ld_16x64(tO + ((uint32_t)half << 20) + st * 128 + c, o);
+              tc_wait_ld();
+              const int r = first + half * 16;
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) {
+                put(r, out + c + i * 2, o[i], o[i + 1], o[i + 4], o[i + 5]);
+                put(r + 8, out + c + i * 2, o[i + 2], o[i + 3], o[i + 6], o[i + 7]);
+              }
+            }
           }
         }
       } else {
@@ -1213,18 +1220,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         l = l * f0 + y.y * f1;
         tc_fence_after();
         if (live) {
+          const int r = first + st * 16, from = (lane >> 2) + st * 16;
+          const float a0 = __shfl_sync(0xffffffffu, f0, from), a1 = __shfl_sync(0xffffffffu, f1, from);
+          const float b0 = __shfl_sync(0xffffffffu, f0, from + 8);
+          const float b1 = __shfl_sync(0xffffffffu, f1, from + 8);
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            const int col = st * (D / 2) + c * 32;
+          for (int c = 0; c < D; c += 64) {
+            const uint32_t at_o = tO + ((uint32_t)st << 20) + c;
             uint32_t o[32], z[32];
-            tmem_ld32(tO + st * 128 + col, o);
-            tmem_ld32(tO + (st ^ 1) * 128 + col, z);
+            tmem_ld_16x64(at_o + st * 128, o);
+            tmem_ld_16x64(at_o + (st ^ 1) * 128, z);
             tc_wait_ld();
-            if (row < rows) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                o[i] = __float_as_uint(fmaf(__uint_as_float(o[i]), f0, __uint_as_float(z[i]) * f1));
-              store_pieces(out + (col / 4) * (sr * 4), sr * 4, o);
+            for (int i = 0; i < 32; ++i)
+              o[i] = __float_as_uint(fmaf(__uint_as_float(o[i]), i & 2 ? b0 : a0,
+                                          __uint_as_float(z[i]) * (i & 2 ? b1 : a1)));
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              put(r, out + c + i * 2, o[i], o[i + 1], o[i + 4], o[i + 5]);
+              put(r + 8, out + c + i * 2, o[i + 2], o[i + 3], o[i + 6], o[i + 7]);
             }
           }
         }
@@ -1243,7 +1257,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc<512>(tmem);
 }
 
-// ---- combine: one thread per four columns of an output row
+// ---- combine: one thread per four columns of an output row, a row's threads
+// side by side
 
 struct CombineArgs {
   PrefixKArgs k;
@@ -1255,6 +1270,7 @@ struct CombineArgs {
 constexpr int kCombineThreads = 256;
 
 constexpr int kPartBatch = 64;
+constexpr int kInFlight = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads)
@@ -1265,11 +1281,14 @@ __global__ void __launch_bounds__(kCombineThreads)
   // columns in float4s, the family in bit 0).
   __shared__ float2 ml_of[ROWS][kPartBatch + 1];
   __shared__ unsigned at_of[ROWS][kPartBatch + 1];
-  __shared__ float weight_of[ROWS][kPartBatch];
+  __shared__ float weight_of[ROWS][kPartBatch + 1];
   __shared__ float m_of[ROWS], l_of[ROWS], rescale_of[ROWS];
   __shared__ int kept_of[ROWS];
   const PrefixKArgs& a = c.k;
-  const int piece = threadIdx.x / ROWS, mine = threadIdx.x % ROWS;
+  // Finding a batch's partials, neighbouring threads take neighbouring rows
+  // (their m and l lie together), adding them up, one row's columns.
+  const int turn = threadIdx.x / ROWS, mine = threadIdx.x % ROWS;
+  const int piece = threadIdx.x % PIECES, out_row = threadIdx.x / PIECES;
   const int row = blockIdx.x * ROWS + mine;
   const bool have = row < c.rows;
   const int seq = have ? quotient(row, a.hq_w, a.inv_hq_w) : 0;
@@ -1312,7 +1331,7 @@ __global__ void __launch_bounds__(kCombineThreads)
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   const int count = n[0] + n[1];
   for (int i0 = 0;; i0 += kPartBatch) {
-    for (int i = piece; i < kPartBatch; i += PIECES) {
+    for (int i = turn; i < kPartBatch; i += PIECES) {
       const int e = i0 + i;
       float2 ml = make_float2(-INFINITY, 0.f);
       unsigned at = 0;
@@ -1321,7 +1340,7 @@ __global__ void __launch_bounds__(kCombineThreads)
         const int x = k ? e : e - n[1];
         const int at_place = base[k] + (x >> two[k]) * stride[k] + (x & two[k]);
         const int slot = at_place * a.streams[k] + stream[k];
-        at = ((unsigned)slot * (a.slot_rows[k] * (D / 4)) + in_tile[k]) * 2 + k;
+        at = ((unsigned)slot * a.slot_rows[k] + in_tile[k]) * (D / 2) + k;
         ml = a.ws_ml[k][(long long)slot * a.slot_rows[k] + in_tile[k]];
       }
       ml_of[mine][i] = ml;
@@ -1363,32 +1382,44 @@ __global__ void __launch_bounds__(kCombineThreads)
       }
     }
     __syncthreads();
-    const float f = rescale_of[mine];
+    const float f = rescale_of[out_row];
     acc.x *= f;
     acc.y *= f;
     acc.z *= f;
     acc.w *= f;
-    const int kept = kept_of[mine];
-    const float4* from[2] = {reinterpret_cast<const float4*>(a.ws_o[0]) + piece * a.slot_rows[0],
-                             reinterpret_cast<const float4*>(a.ws_o[1]) + piece * a.slot_rows[1]};
-#pragma unroll 8
-    for (int i = 0; i < kept; ++i) {
-      const unsigned at = at_of[mine][i];
-      const float4 v = (at & 1 ? from[1] : from[0])[at >> 1];
-      const float wt = weight_of[mine][i];
-      acc.x = fmaf(wt, v.x, acc.x);
-      acc.y = fmaf(wt, v.y, acc.y);
-      acc.z = fmaf(wt, v.z, acc.z);
-      acc.w = fmaf(wt, v.w, acc.w);
+    const int kept = kept_of[out_row];
+    const float4* from[2] = {reinterpret_cast<const float4*>(a.ws_o[0]) + piece,
+                             reinterpret_cast<const float4*>(a.ws_o[1]) + piece};
+    for (int i = 0; i < kept; i += kInFlight) {
+      float4 v[kInFlight];
+#pragma unroll
+      for (int j = 0; j < kInFlight; ++j) {
+        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i + j < kept) {
+          const unsigned at = at_of[out_row][i + j];
+          v[j] = __ldcg((at & 1 ? from[1] : from[0]) + (at >> 1));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kInFlight; ++j) {
+        const float wt = i + j < kept ? weight_of[out_row][i + j] : 0.f;
+        acc.x = fmaf(wt, v[j].x, acc.x);
+        acc.y = fmaf(wt, v[j].y, acc.y);
+        acc.z = fmaf(wt, v[j].z, acc.z);
+        acc.w = fmaf(wt, v[j].w, acc.w);
+      }
     }
     if (!__syncthreads_or(count > i0 + kPartBatch)) break;   // also: the batch is read
   }
-  const float m = m_of[mine], l = l_of[mine];
-  if (!have) return;
+  const int to = blockIdx.x * ROWS + out_row;
+  if (to >= c.rows) return;
+  const float m = m_of[out_row], l = l_of[out_row];
   const float inv = m == -INFINITY ? 0.f : 1.f / l;
-  *reinterpret_cast<uint2*>(c.o + (long long)row * D + piece * 4) =
-      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (piece == 0) c.lse[row] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
+  // The columns' order of the partials.
+  uint32_t* out = reinterpret_cast<uint32_t*>(c.o + (long long)to * D) + piece / 4 * 8 + piece % 4;
+  out[0] = pack_bf16(acc.x * inv, acc.y * inv);
+  out[4] = pack_bf16(acc.z * inv, acc.w * inv);
+  if (piece == 0) c.lse[to] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // ---- host side
