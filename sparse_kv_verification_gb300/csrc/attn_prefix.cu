@@ -16,8 +16,8 @@
 // One persistent CTA per SM; lengths are on the device, so every CTA works
 // out its share itself (Walk).  Prefixes are split: each row tile pair's
 // tiles into np equal segments, the single's into ns (half as many, as its
-// tiles cost half), one segment to a CTA, np and ns from the smallest M
-// (units, row tile x K/V tile, per CTA) that fits the CTAs.  All pairs walk
+// tiles cost half), one segment to a CTA, np and ns from the M (units, row
+// tile x K/V tile, per CTA) whose longest CTA is the shortest.  All pairs walk
 // the same K/V tiles at the same time: a prefix of 32768 positions is as
 // large as L2, and with the row tiles one after another it came from HBM once
 // per pair of them (512 rows: 64 instead of 44 us for the loads alone).  The
@@ -37,6 +37,8 @@
 // there as the A operand, so only Q, K and V live in shared memory.  While one
 // stream's softmax works, the tensor cores work for the other.
 #include <algorithm>
+#include <climits>
+#include <climits>
 #include <cuda.h>
 
 #include "device_common.cuh"
@@ -221,10 +223,17 @@ __device__ __forceinline__ int quotient_up(int x, int d, float inv) {
 
 // Work is counted in quarters of a unit (one row tile on one tile of a
 // prefix).  An own tile costs more than that, its K and V coming for one row
-// tile alone, and a segment's start and end cost about two units.
+// tile alone, and a segment as much as 4.5 units beside its tiles: its Q, its
+// start and end, its partials and their part in the combination.  Measured:
+// with two units for a segment 32 sequences of four ragged prefixes take 89
+// instead of 75 us, a 7B-shaped step 28 instead of 25, two short sequences
+// 13.7 instead of 10.3; with six, 64 sequences with short own parts take 70
+// instead of 66.  At six quarters for an own tile, a 72B-shaped step with full
+// own parts takes 97 instead of 87.
 __host__ __device__ constexpr int unit_cost(int kind) { return kind ? 5 : 4; }
-constexpr int kSegmentCost = 8;
-constexpr int kMinRange = 24;
+constexpr int kSegmentCost = 18;
+// A range holds a segment of one tile at least.
+constexpr int kMinRange = kSegmentCost + 2 * unit_cost(1);
 
 // The line cut into n ranges of at least kMinRange: range c starts at
 // ceil(c * total / n), which is c * (total / n) + ceil(c * (total % n) / n),
@@ -245,10 +254,10 @@ struct Cut {
 };
 
 // Whether an equal share on the line, two segments to a CTA, ends before a
-// split into segments of m units does, for items whose row tiles all share
-// their K/V tiles anyway.
-__host__ __device__ constexpr bool on_line_is_shorter(long long m, long long share) {
-  return m * unit_cost(0) > share + share / 16 + kSegmentCost;
+// split that takes `longest`, for items whose row tiles all share their K/V
+// tiles anyway.
+__host__ __device__ constexpr bool on_line_is_shorter(long long longest, long long share) {
+  return longest > share + share / 16 + 2 * kSegmentCost;
 }
 
 // A segment's tiles on the line: n of them, w apart, then its fixed cost.
@@ -348,12 +357,15 @@ struct Walk {
       ctas += pairs * quotient(t + (x >> 1) - 1, x >> 1, inv_p) + single * quotient(t + x - 1, x, inv_s);
     }
     ctas *= a.hkv;
-    const unsigned fits =
-        __ballot_sync(0xffffffffu, ctas + quotient_up(wo, x * unit_cost(0)) <= a.grid);
-    if (!fits) return 0;
-    const int src = __ffs((int)fits) - 1;
+    const int own = a.grid - ctas;       // CTAs left
+    const bool fits = wo ? own > 0 : own >= 0;
+    const unsigned longest =
+        fits ? (unsigned)max(x * unit_cost(0) + kSegmentCost, wo ? quotient_up(wo, own) : 0) : ~0u;
+    const unsigned least_of = __reduce_min_sync(0xffffffffu, longest);
+    if (least_of == ~0u) return 0;
+    const int src = __ffs((int)__ballot_sync(0xffffffffu, longest == least_of)) - 1;
     m = __shfl_sync(0xffffffffu, x, src);
-    if (rt <= 2 && on_line_is_shorter(m, share)) return 0;
+    if (rt <= 2 && on_line_is_shorter(least_of, share)) return 0;
     return __shfl_sync(0xffffffffu, ctas, src);
   }
   // The one segment of a split CTA, the x-th of group gi.  Of a kv head: for
@@ -1519,8 +1531,8 @@ PrefixKArgs shape_args(const PrefixArgs& p, int sms, Layout* lay) {
 }
 
 // The split of prefixes of one length (Walk::search for those on the device):
-// the smallest M, from the even share on, that fits the CTAs.  Own parts
-// whose lengths are on the device count as 5/8 of the longest: batches of
+// the M, from the even share on, whose longest CTA is the shortest, the own
+// parts taking equal shares of the CTAs left.  Own parts whose lengths are on the device count as 5/8 of the longest: batches of
 // continuations lie between a third of that and all of it.
 void host_split(PrefixKArgs& a, bool lengths_given, bool own_given) {
   a.split = a.np = a.ns = a.range = 0;
@@ -1534,21 +1546,29 @@ void host_split(PrefixKArgs& a, bool lengths_given, bool own_given) {
                        (to > 0) * (long long)a.count[1] * a.hkv * ((a.row_tiles[1] + 1) / 2) * kSegmentCost;
   const long long share = (wp + wo + a.grid - 1) / a.grid;
   const long long least = std::max<long long>(2, (share + 3) / unit_cost(0));
+  long long best = LLONG_MAX;
   for (long long m = least; m <= 3 * least; ++m) {
     // A pair's tile is two units.
     const long long np = pairs ? std::min(tp, (2 * tp + m - 1) / m) : 0;
     const long long ns = single ? (tp + m - 1) / m : 0;
     const long long split = a.count[0] * a.hkv * (pairs * np + ns);
-    const long long rest = (wo + m * unit_cost(0) - 1) / (m * unit_cost(0));
-    if (split + rest > a.grid) continue;
-    if (rt <= 2 && on_line_is_shorter(m, share)) return;
+    const long long own = a.grid - split;   // CTAs left
+    if (own < (wo > 0)) continue;
+    const long long longest =
+        std::max(m * unit_cost(0) + kSegmentCost, wo > 0 ? (wo + own - 1) / own : 0);
+    if (longest >= best) continue;
+    best = longest;
     a.split = (int)split;
     a.np = (int)np;
     a.ns = (int)ns;
-    const long long tiles = to * a.count[1] * a.hkv * a.row_tiles[1] * unit_cost(1);
-    a.range = (int)std::max<long long>(kMinRange, tiles / std::max<long long>(1, a.grid - split));
+  }
+  if (!a.split) return;
+  if (rt <= 2 && on_line_is_shorter(best, share)) {
+    a.split = 0;
     return;
   }
+  const long long tiles = to * a.count[1] * a.hkv * a.row_tiles[1] * unit_cost(1);
+  a.range = (int)std::max<long long>(kMinRange, tiles / std::max<long long>(1, a.grid - a.split));
 }
 
 template <int D>
