@@ -377,8 +377,12 @@ int dustin_full_verify_attn_window(int b, int h_q, int h_kv, int d, int w, int n
  * the window is finite.  Pages outside the pool are left out
  * (DUSTIN_DEVFLAG_PAGE_RANGE).  DUSTIN_ATTN_KV_READY is accepted, without
  * effect.  Sums are taken in a fixed order: equal calls give equal bits.
- * Limits: as dustin_sparse_verify_attn; kv strides below 2^39 elements.
- * Workspace: dustin_prefix_verify_attn_workspace_size (with or without win).
+ * Limits: as dustin_sparse_verify_attn; kv strides below 2^39 elements; b <=
+ * 2^20; n_prefix, n_own <= 2^27; 2^25 products of 128 rows with 128 positions
+ * in all; a workspace of 2^35 bytes.  Beyond them: DUSTIN_ERR_SHAPE.
+ * Workspace: dustin_prefix_verify_attn_workspace_size (with or without win);
+ * its content need not be kept, and calls that may run at the same time (two
+ * streams, two captured graphs) have one each.
  */
 size_t dustin_prefix_verify_attn_workspace_size(int b, int groups, int h_q, int h_kv,
                                                 int d, int w, int n_prefix, int n_own);
@@ -408,7 +412,8 @@ int dustin_prefix_verify_attn(int b, int groups, int h_q, int h_kv, int d, int w
  * are independent uniforms in [0, 1).  With p_draft NULL the drafts are
  * taken as certain (q is 1 at the draft, 0 elsewhere), as for drafts found
  * by lookup.  Entries that are negative, NaN or infinite have no mass.  The
- * sums carry about 48 bits.  u_sample <= 0 or NaN counts as 0, >= 1 as the
+ * sums carry about 48 bits (a row's masses add up to less than 2^127, as
+ * probabilities do).  u_sample <= 0 or NaN counts as 0, >= 1 as the
  * last token with mass; a NaN in u_accept rejects.  A draft outside
  * [0, vocab) is rejected and raises DUSTIN_DEVFLAG_INDEX_RANGE.
  *
@@ -422,7 +427,8 @@ int dustin_prefix_verify_attn(int b, int groups, int h_q, int h_kv, int d, int w
  *              the target's row has no mass at all), then -1
  *   n_accepted int32 [b]: a
  * draft and u_accept may be NULL when w == 1.  Rows may start at any
- * element; rows that start on 16-byte boundaries are read fastest.
+ * element; they are read in aligned words of 16 bytes, so bytes beside a row
+ * may be read too (never used).
  * b == 0 is a no-op.  Limits: vocab >= 1, b <= 2^27.  No workspace. */
 int dustin_verify_tokens(int b, int w, int vocab, int dtype, const void* p_target,
                          int64_t stride_tb, int64_t stride_tw, const void* p_draft,
@@ -450,7 +456,8 @@ int dustin_verify_tokens(int b, int w, int vocab, int dtype, const void* p_targe
  * written (so a shared prefix that is kept whole may lie on shared pages).
  * Otherwise (DUSTIN_DEVFLAG_INDEX_ORDER) that sequence's rows are
  * unspecified.  Out of place, src and dst rows must not overlap, and an
- * index may repeat.  Limits: d in {64, 128}; k <= n in place. */
+ * index may repeat.  Rows of dst are distinct: a stride of 0 is refused, two
+ * sequences' rows on one page are the caller's to avoid.  Limits: d in {64, 128}; k <= n in place. */
 int dustin_kv_compact(int n_layers, int b, int h_kv, int d, int n, int k,
                       const dustin_kv* src, const dustin_kv* dst, const int32_t* idx,
                       const int32_t* k_len, void* stream);
@@ -489,8 +496,8 @@ int dustin_kv_compact(int n_layers, int b, int h_kv, int d, int n, int k,
  * DUSTIN_DEVFLAG_INDEX_RANGE; a page id outside the pool is skipped and
  * raises DUSTIN_DEVFLAG_PAGE_RANGE.
  *   copies  int32 [n_list][2], device, fully overwritten
- * Limits: n_list <= 1024, num_pages <= 2^22, pages_per_seq * page_size and
- * n_seqs * pages_per_seq < 2^31; page_size as in dustin_kv.  Calls on one
+ * Limits: n_list <= 1024, num_pages <= 2^22, pages_per_seq * page_size
+ * <= 2^30, n_seqs * pages_per_seq < 2^31; page_size as in dustin_kv.  Calls on one
  * state are ordered by the stream; none may overlap another. */
 int dustin_kv_fork(int n_seqs, int pages_per_seq, int page_size, int num_pages,
                    int n_forks, const int32_t* parent, const int32_t* child,

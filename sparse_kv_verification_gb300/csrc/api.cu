@@ -976,13 +976,18 @@ int dustin_kv_compact(int n_layers, int b, int h_kv, int d, int n, int k,
     if ((src[l].page_table != nullptr) != (src[0].page_table != nullptr) ||
         (dst[l].page_table != nullptr) != (dst[0].page_table != nullptr))
       return fail(DUSTIN_ERR_INVALID_ARG, "%s: layers mix paged and contiguous caches", what);
+    // Rows that lie on one another have no one content.
+    if ((dst[l].stride_h == 0 && h_kv > 1) ||
+        (dst[l].stride_b == 0 && (dst[l].page_table ? dst[l].num_pages : b) > 1))
+      return fail(DUSTIN_ERR_SHAPE, "%s: layer %d: rows of dst share storage", what, l);
     const bool same_table = src[l].page_table == dst[l].page_table;
     if ((src[l].k == dst[l].k && same_table) != in_place ||
         (src[l].v == dst[l].v && same_table) != in_place)
       return fail(DUSTIN_ERR_INVALID_ARG, "%s: layer %d: all of K and V in place, or none", what, l);
     if (in_place && (src[l].stride_b != dst[l].stride_b || src[l].stride_h != dst[l].stride_h ||
                      src[l].stride_n != dst[l].stride_n || src[l].page_size != dst[l].page_size ||
-                     src[l].num_pages != dst[l].num_pages))
+                     src[l].num_pages != dst[l].num_pages ||
+                     src[l].pages_per_seq != dst[l].pages_per_seq))
       return fail(DUSTIN_ERR_INVALID_ARG, "%s: layer %d: one cache in two layouts", what, l);
   }
   CompactArgs a;
@@ -1015,7 +1020,7 @@ static int check_pages(int n_seqs, int pages_per_seq, int page_size, int num_pag
   if (page_size < 16 || page_size % 16)
     return fail(DUSTIN_ERR_UNSUPPORTED, "%s: page_size %d (must be a positive multiple of 16)",
                 what, page_size);
-  if ((long long)pages_per_seq * page_size > 0x7fffffffLL ||
+  if ((long long)pages_per_seq * page_size > (1LL << 30) ||
       (long long)n_seqs * pages_per_seq > 0x7fffffffLL)
     return fail(DUSTIN_ERR_SHAPE, "%s: problem too large", what);
   if (num_pages > kResizeMaxPages)

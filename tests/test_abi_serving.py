@@ -115,3 +115,23 @@ def test_prefix_attention_refusals(lib):
     size = lib.dustin_prefix_verify_attn_workspace_size
     assert size(4, 2, 8, 2, 128, 4, 256, 64) > 0
     assert size(4, 3, 8, 2, 128, 4, 256, 64) == 0 and size(0, 1, 8, 2, 128, 4, 256, 64) == 0
+
+
+def test_refusals_of_shared_rows_and_sizes(lib):
+    def compact(src, dst, b=2, hkv=2, k=32):
+        return lib.dustin_kv_compact(1, b, hkv, 128, 256, k, ctypes.byref(src), ctypes.byref(dst),
+                                     FAKE, None, None)
+    other = FAKE + 0x1000000
+    for name in ("stride_b", "stride_h", "stride_n"):
+        assert compact(desc(), desc(base=other, **{name: 0})) == 2
+    assert compact(desc(True), desc(True, base=other, stride_b=0)) == 2
+    assert compact(desc(True), desc(True, pages_per_seq=32)) == 1     # in place, another table
+    assert lib.dustin_kv_fork(2, (1 << 26) + 1, 16, 64, 1, FAKE, FAKE, FAKE, FAKE, FAKE, None) == 2
+
+    size = lib.dustin_prefix_verify_attn_workspace_size
+    assert size(1, 1, 1, 1, 64, 1, 1 << 27, 0) > 0
+    assert size(1, 1, 1, 1, 64, 1, (1 << 27) + 1, 0) == 0
+    assert size(1, 1, 1, 1, 64, 1, 0, (1 << 27) + 1) == 0
+    assert size((1 << 20) + 1, 1, 1, 1, 64, 1, 0, 16) == 0
+    # 2^20 sequences of 128 rows: a place of 64 KB per part of one
+    assert size(1 << 20, 1, 128, 1, 128, 1, 0, 16) == 0
