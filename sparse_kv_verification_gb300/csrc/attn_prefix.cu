@@ -38,7 +38,6 @@
 // stream's softmax works, the tensor cores work for the other.
 #include <algorithm>
 #include <climits>
-#include <climits>
 #include <cuda.h>
 
 #include "device_common.cuh"
@@ -53,7 +52,7 @@ namespace {
 __device__ unsigned int g_prefix_dev_flags;
 
 constexpr int kTile = 128;        // positions of a K/V tile, rows of a row tile
-constexpr int kHalf = 64;         // positions of an S buffer
+constexpr int kHalf = 64;         // positions whose P is handed over at a time
 constexpr int kSoftmaxWarps = 4;  // per stream
 constexpr int kMmaWarp = 0, kLoadWarp = 1, kWalkWarp = 2, kTableWarp = 3, kQWarp = 4, kQWarps = 4,
               kSoftmaxWarp = 8;
@@ -1062,101 +1061,112 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         s_phase ^= 1;
         tc_fence_after();
+        auto hand_over = [&](int x) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.p_ready[st][x]));
+        };
+        // The reference m is a maximum of scores seen before.  It moves only
+        // when a row's weights 2^(s - m) of 64 columns add up to more than 2^8
+        // (or when it is not set yet), so no maximum is taken and O not scaled
+        // for most of them, and a weight never exceeds 2^8.  Masks are the
+        // slow path's alone, and its code is there once, for both halves
+        // (512 rows x 32768 positions: masks in the fast path 70 us, without
+        // 62; the fast path unrolled over the halves 57).
 #pragma unroll 1
         for (int x = 0; x < 2; ++x) {
-          if (live) {
-            // The reference m is a maximum of scores seen before.  It moves
-            // only when a row's weights 2^(s - m) of these 64 columns add up
-            // to more than 2^8 (or when it is not set yet), so no maximum is
-            // taken and O not scaled for most of them, and a weight never
-            // exceeds 2^8.  Masks are the slow path's alone: with them in the
-            // fast one, 512 rows x 32768 positions took 3% longer.
-            const uint32_t tX = tS + x * kHalf, tP = tS + x * (kHalf / 2);
-            bool slow = special || __any_sync(0xffffffffu, m == -INFINITY);
-            if (!slow) {
-              uint32_t x0[32], x1[32], p[32];
-              tmem_ld32(tX, x0);
-              tmem_ld32(tX + 32, x1);
-              tc_wait_ld();
-              const uint64_t mm = pack2(__float_as_uint(-m), __float_as_uint(-m));
-              uint64_t part[2] = {0, 0};
-              exp32(x0, scale2, mm, part, p);
-              exp32(x1, scale2, mm, part, p + 16);
-              const uint64_t all = add2(part[0], part[1]);
-              slow = __any_sync(0xffffffffu, lo_of(all) + hi_of(all) > kMostWeight);
-              if (!slow) {
-                sum = add2(sum, all);
-                tmem_st32(tP, p);
-              }
-            }
-            if (slow) {
-              // 32-column chunks with columns that count for some row
-              const int nc = !special ? 2
-                                      : __any_sync(0xffffffffu, lim > x * kHalf) +
-                                            __any_sync(0xffffffffu, lim > x * kHalf + 32);
-              auto load = [&](int c, uint32_t (&v)[32]) {
-                tmem_ld32(tX + c * 32, v);
+          if (!special && !__any_sync(0xffffffffu, live && m == -INFINITY)) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              if (x != y) continue;
+              if (live) {
+                uint32_t x0[32], x1[32], p[32];
+                tmem_ld32(tS + y * kHalf, x0);
+                tmem_ld32(tS + y * kHalf + 32, x1);
                 tc_wait_ld();
-                if (special) {
-                  mask32(v, lim - x * kHalf - c * 32);
-                  if (bad) mask_bits(v, bad[2 * x + c]);
-                }
-              };
-              float top = -INFINITY;
-#pragma unroll 1
-              for (int c = 0; c < nc; ++c) {
-                uint32_t v[32];
-                load(c, v);
-                top = max32(v, top);
+                const uint64_t mm = pack2(__float_as_uint(-m), __float_as_uint(-m));
+                uint64_t part[2] = {0, 0};
+                exp32(x0, scale2, mm, part, p);
+                exp32(x1, scale2, mm, part, p + 16);
+                const uint64_t all = add2(part[0], part[1]);
+                if (__any_sync(0xffffffffu, lo_of(all) + hi_of(all) > kMostWeight)) break;
+                sum = add2(sum, all);
+                tmem_st32(tS + y * (kHalf / 2), p);
+                tc_wait_st();
               }
-              top *= a.scale_log2;
-              const bool up = top > m;
-              if (__any_sync(0xffffffffu, up)) {
-                const float f = up ? ex2(m - top) : 1.f;
-                if (up) m = top;
-                sum = fma2(sum, pack2(__float_as_uint(f), __float_as_uint(f)), 0);
-                if (step > 0 || x > 0) {
-                  // O is scaled once the product before is complete.  That of
-                  // an earlier tile is: it was issued before these scores.
-                  if (x) {
-                    ok = pwait_warp(&sh.half_done[st], h_phase, &sh.abort);
-                    if (!ok) break;
-                    tc_fence_after();
-                  }
-#pragma unroll 1
-                  for (int c = 0; c < D / 32; ++c) {
-                    const uint32_t to_o = tO + st * 128 + c * 32;
-                    uint32_t o[32];
-                    tmem_ld32(to_o, o);
-                    tc_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                    tmem_st32(to_o, o);
-                  }
-                }
-              }
-              // The scaled score rounded as the maximum was: a weight is at
-              // most 1 here, whatever the size of the scores.
-              const float ms = m == -INFINITY ? 0.f : -m;
-              const uint64_t mm = pack2(__float_as_uint(ms), __float_as_uint(ms));
-              uint64_t part[2] = {0, 0};
-#pragma unroll 1
-              for (int c = 0; c < 2; ++c) {
-                uint32_t v[32], p[16];
-                if (c < nc) {
-                  load(c, v);
-#pragma unroll
-                  for (int i = 0; i < 32; ++i)
-                    v[i] = __float_as_uint(__fmul_rn(__uint_as_float(v[i]), a.scale_log2));
-                  exp32(v, one2, mm, part, p);
-                } else {
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) p[i] = 0;
-                }
-                tmem_st16(tP + c * 16, p);   // over scores that are read
-              }
-              sum = add2(sum, add2(part[0], part[1]));
+              hand_over(y);
+              x = y + 1;
             }
+            if (x == 2) break;
+          }
+          if (live) {
+            const uint32_t tX = tS + x * kHalf, tP = tS + x * (kHalf / 2);
+            // 32-column chunks with columns that count for some row
+            const int nc = !special ? 2
+                                    : __any_sync(0xffffffffu, lim > x * kHalf) +
+                                          __any_sync(0xffffffffu, lim > x * kHalf + 32);
+            auto load = [&](int c, uint32_t (&v)[32]) {
+              tmem_ld32(tX + c * 32, v);
+              tc_wait_ld();
+              if (special) {
+                mask32(v, lim - x * kHalf - c * 32);
+                if (bad) mask_bits(v, bad[2 * x + c]);
+              }
+            };
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < nc; ++c) {
+              uint32_t v[32];
+              load(c, v);
+              top = max32(v, top);
+            }
+            top *= a.scale_log2;
+            const bool up = top > m;
+            if (__any_sync(0xffffffffu, up)) {
+              const float f = up ? ex2(m - top) : 1.f;
+              if (up) m = top;
+              sum = fma2(sum, pack2(__float_as_uint(f), __float_as_uint(f)), 0);
+              if (step > 0 || x > 0) {
+                // O is scaled once the product before is complete.  That of
+                // an earlier tile is: it was issued before these scores.
+                if (x) {
+                  ok = pwait_warp(&sh.half_done[st], h_phase, &sh.abort);
+                  if (!ok) break;
+                  tc_fence_after();
+                }
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                  const uint32_t to_o = tO + st * 128 + c * 32;
+                  uint32_t o[32];
+                  tmem_ld32(to_o, o);
+                  tc_wait_ld();
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                  tmem_st32(to_o, o);
+                }
+              }
+            }
+            // The scaled score rounded as the maximum was: a weight is at
+            // most 1 here, whatever the size of the scores.
+            const float ms = m == -INFINITY ? 0.f : -m;
+            const uint64_t mm = pack2(__float_as_uint(ms), __float_as_uint(ms));
+            uint64_t part[2] = {0, 0};
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+              uint32_t v[32], p[16];
+              if (c < nc) {
+                load(c, v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  v[i] = __float_as_uint(__fmul_rn(__uint_as_float(v[i]), a.scale_log2));
+                exp32(v, one2, mm, part, p);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) p[i] = 0;
+              }
+              tmem_st16(tP + c * 16, p);   // over scores that are read
+            }
+            sum = add2(sum, add2(part[0], part[1]));
             tc_wait_st();
           }
           // V rows behind the end hold whatever the cache holds there, NaN
@@ -1176,9 +1186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                              : "memory");
             fence_proxy_async_smem();
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sh.p_ready[st][x]));
+          hand_over(x);
         }
         h_phase ^= 1;
       }
