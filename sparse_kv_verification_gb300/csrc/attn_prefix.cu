@@ -641,16 +641,11 @@ __device__ __forceinline__ void exp32(const uint32_t (&x)[32], uint64_t scale, u
     p[i] = pack_bf16(e0, e1);
   }
 }
-// Columns [lim, 32) of x do not count.
-__device__ __forceinline__ void mask32(uint32_t (&x)[32], int lim) {
+// Columns whose bits are set do not count.
+__device__ __forceinline__ void mask_bits(uint32_t (&x)[32], unsigned dead) {
 #pragma unroll
   for (int i = 0; i < 32; ++i)
-    if (i >= lim) x[i] = 0xff800000u;   // -inf
-}
-__device__ __forceinline__ void mask_bits(uint32_t (&x)[32], unsigned bad) {
-#pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if (bad >> i & 1) x[i] = 0xff800000u;
+    if (dead >> i & 1) x[i] = 0xff800000u;   // -inf
 }
 
 template <int D>
@@ -1109,8 +1104,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld32(tX + c * 32, v);
               tc_wait_ld();
               if (special) {
-                mask32(v, lim - x * kHalf - c * 32);
-                if (bad) mask_bits(v, bad[2 * x + c]);
+                const int left = lim - x * kHalf - c * 32;
+                unsigned dead = left >= 32 ? 0u : left <= 0 ? ~0u : ~0u << left;
+                if (bad) dead |= bad[2 * x + c];
+                if (__any_sync(0xffffffffu, dead)) mask_bits(v, dead);
               }
             };
             float top = -INFINITY;
