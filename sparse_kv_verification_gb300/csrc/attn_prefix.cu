@@ -28,9 +28,9 @@
 // (on the line: each of two parts) has its place, and
 // attn_prefix_combine_kernel adds each row's partials in a fixed order.
 //
-// Roles of the 16 warps: 0 issues tcgen05.mma, 1 the TMA loads of K and V, 2
-// walks the CTA's share and publishes its segments, 3 (of CTA 0) writes the
-// plan for the combine kernel, 4-7 copy Q rows, 8-11 and 12-15 are the
+// Roles of the 16 warps: 0 issues tcgen05.mma, 1 and 7 the TMA loads of K and
+// V, 2 walks the CTA's share and publishes its segments, 3 (of CTA 0) writes
+// the plan for the combine kernel, 4-6 copy Q rows, 8-11 and 12-15 are the
 // softmax of stream A and B, one thread per row.  S = Q K^T and O += P V
 // accumulate in tensor memory (512 columns: per stream an S of 128 positions
 // and an O); P replaces S in place as bf16, half by half, and is read from
@@ -54,8 +54,8 @@ __device__ unsigned int g_prefix_dev_flags;
 constexpr int kTile = 128;        // positions of a K/V tile, rows of a row tile
 constexpr int kHalf = 64;         // positions whose P is handed over at a time
 constexpr int kSoftmaxWarps = 4;  // per stream
-constexpr int kMmaWarp = 0, kLoadWarp = 1, kWalkWarp = 2, kTableWarp = 3, kQWarp = 4, kQWarps = 4,
-              kSoftmaxWarp = 8;
+constexpr int kMmaWarp = 0, kLoadWarp = 1, kWalkWarp = 2, kTableWarp = 3, kQWarp = 4, kQWarps = 3,
+              kLoadWarp2 = 7, kSoftmaxWarp = 8;
 constexpr int kThreads = 16 * 32;
 // Registers: a softmax thread holds 64 scores and their weights; the other
 // two warpgroups give up what they need beyond the launch's 128.
@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kMaskRing; ++i) mbar_init(smem_u32(&sh.mask_full[i]), 1);
     for (int i = 0; i < kSegRing; ++i) {
       mbar_init(smem_u32(&sh.seg_full[i]), 1);
-      mbar_init(smem_u32(&sh.seg_empty[i]), 2 * kSoftmaxWarps + 2 + kQWarps);
+      mbar_init(smem_u32(&sh.seg_empty[i]), 2 * kSoftmaxWarps + 3 + kQWarps);
     }
     mbar_init(smem_u32(&sh.meet), 2 * kSoftmaxWarps);
     mbar_init(smem_u32(&sh.drain), 1);
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kTableWarp) {
     role_begin();
     if (blockIdx.x == 0) Walk(a, true);
-  } else if (warp >= kQWarp && warp < kSoftmaxWarp) {
+  } else if (warp >= kQWarp && warp < kQWarp + kQWarps) {
     // ------------------------------------------------------------------- Q
     // Row tiles in the tensor cores' swizzled layout; a pair fills both
     // buffers, singles take turns, so that the next one's rows are there
@@ -743,12 +743,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++fills[buf];
         constexpr int CPR = D / 8, STEP = 32 * kQWarps / CPR;   // 16-byte pieces, rows per pass
         const int piece = tid - kQWarp * 32, c = piece % CPR;
-        static_assert(STEP % 8 == 0, "a thread's rows share their place in the swizzle");
-        int r = piece / CPR;
-        uint32_t dst = q_buf + buf * C::TILE_BYTES + (c / 8) * C::HALF + r * 128 +
-                       ((c % 8 ^ (r & 7)) << 4);
+        const uint32_t dst = q_buf + buf * C::TILE_BYTES + (c / 8) * C::HALF;
         const __nv_bfloat16* src = a.q + (long long)s.h * a.gw * D + c * 8;
-        for (; r < rows; r += STEP, dst += STEP * 128) {
+        for (int r = piece / CPR; r < rows; r += STEP) {
           int seq = s.gi, in_seq = first + r;
           if (s.kind == 0) {
             const int rr = in_seq;
@@ -758,7 +755,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             seq = s.gi * a.per + q;
             in_seq = rr - q * a.gw;
           }
-          cp_async_16_full(dst, src + ((long long)seq * a.hq_w + in_seq) * D);
+          cp_async_16_full(dst + r * 128 + ((c % 8 ^ (r & 7)) << 4),
+                           src + ((long long)seq * a.hq_w + in_seq) * D);
         }
         cp_async_commit();
         cp_async_wait<0>();
@@ -769,9 +767,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       if (!s.pair) turn ^= 1;
     }
-  } else if (warp == kLoadWarp) {
+  } else if (warp == kLoadWarp || warp == kLoadWarp2) {
     // --------------------------------------------------------- K and V loads
+    // Two warps, each with half of a tile's boxes: a warp's lanes issue their
+    // boxes one after another (pages of 16 make 24 of them a tile: with one warp
+    // own parts on such pages were read at 5.0 TB/s, with two at 6.0).
     role_begin();
+    const bool second = warp == kLoadWarp2;
     int slot = 0, tile_count = 0;
     uint32_t phase = 0;
     int filled = 0;          // slots filled at least once
@@ -812,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c.page_table) {
           int page = is_k ? page_k : page_v0;
           const bool in = row < s.len, bad = in && (page < 0 || page >= c.num_pages);
-          if (is_k) {
+          if (is_k && !second) {
             // Positions on pages outside the pool, for the softmax.
             const unsigned all = __ballot_sync(0xffffffffu, bad && half == 0);
             if (lane < 4) {
@@ -843,13 +845,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           page_v0 = page_v1;
           --pending;
         }
-        if (lane == 0) mbar_arrive_expect_tx(bar, C::TILE_BYTES);
+        if (!second && lane == 0) mbar_arrive_expect_tx(bar, C::TILE_BYTES);
         __syncwarp();
         if (is_k) {
-          if (half < D / 64)
+          if (half < D / 64 && (D == 128 ? half : run & 1) == second)
             tma_load_5d(dst + half * C::HALF + (run << (log_box + 7)), map, 0, row, half,
                         s.h * c.zh, outer, bar);
-        } else if (half == 0) {
+        } else if (half == 0 && (run & 1) == second) {
           tma_load_5d(dst + v_row<D>(run << log_box, log_box), map, 0, row, 0, s.h * c.zh, outer,
                       bar);
         }
@@ -865,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < filled; ++i) {
         slot = slot == 0 ? C::SLOTS - 1 : slot - 1;
         if (slot == C::SLOTS - 1) phase ^= 1;
-        mbar_wait(smem_u32(&sh.full[slot]), phase, kWaitLimitCycles);
+        if (!mbar_wait(smem_u32(&sh.full[slot]), phase, kWaitLimitCycles)) break;
       }
     }
   } else if (warp == kMmaWarp) {
