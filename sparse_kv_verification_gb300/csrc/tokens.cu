@@ -18,6 +18,12 @@
 //  * The CTA whose range holds u * total walks it again (one warp's share,
 //    1/(16 C) of the row, from L2) with a block scan of the same sums.
 // One launch, no workspace, no atomics but the error flag's.
+//
+// Bound by latency: the chain launch, draft's probabilities, row, cluster
+// barrier, second walk.  Measured (one call after the other): 16 rows of
+// 152064 in fp32, drafts rejected at random, 12.9 us (its 19.4 MB alone take
+// 2.9), 64 rows of 50257 in bf16 at odd alignments 14.0, one row of 32000
+// 8.1.  (Read element by element, the odd rows took 20.9.)
 #include <algorithm>
 #include <cooperative_groups.h>
 
