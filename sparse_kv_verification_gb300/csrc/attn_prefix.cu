@@ -15,9 +15,9 @@
 //
 // One persistent CTA per SM; lengths are on the device, so every CTA works
 // out its share itself (Walk).  Prefixes are split: each row tile pair's
-// tiles into np equal segments, the single's into ns (half as many, as its
-// tiles cost half), one segment to a CTA, np and ns from the M (units, row
-// tile x K/V tile, per CTA) whose longest CTA is the shortest.  All pairs walk
+// tiles into np equal segments, the single's into ns (fewer, as its tiles
+// cost less), one segment to a CTA, np and ns from the M (cost of the tiles of
+// a segment) whose longest CTA is the shortest.  All pairs walk
 // the same K/V tiles at the same time: a prefix of 32768 positions is as
 // large as L2, and with the row tiles one after another it came from HBM once
 // per pair of them (512 rows: 64 instead of 44 us for the loads alone).  The
@@ -220,19 +220,22 @@ __device__ __forceinline__ int quotient_up(int x, int d, float inv) {
   return quotient(x + d - 1, d, inv);
 }
 
-// Work is counted in quarters of a unit (one row tile on one tile of a
-// prefix).  An own tile costs more than that, its K and V coming for one row
-// tile alone, and a segment as much as 4.5 units beside its tiles: its Q, its
-// start and end, its partials and their part in the combination.  Measured:
-// with two units for a segment 32 sequences of four ragged prefixes take 89
-// instead of 75 us, a 7B-shaped step 28 instead of 25, two short sequences
-// 13.7 instead of 10.3; with six, 64 sequences with short own parts take 70
-// instead of 66.  At six quarters for an own tile, a 72B-shaped step with full
-// own parts takes 97 instead of 87.
-__host__ __device__ constexpr int unit_cost(int kind) { return kind ? 5 : 4; }
-constexpr int kSegmentCost = 18;
-// A range holds a segment of one tile at least.
-constexpr int kMinRange = kSegmentCost + 2 * unit_cost(1);
+// Work is counted in eighths of a pair's K/V tile.  A tile for one row tile
+// alone costs more than half of that (its K and V come for it alone, and its
+// two streams wait for one another's tensor core time less evenly), and a
+// segment as much as two tiles beside its own: its Q, its start and end, its
+// partials and their part in the combination.  Measured: with 8 for a segment
+// 32 sequences of four ragged prefixes take 89 instead of 75 us, a 7B-shaped
+// step 28 instead of 25, two short sequences 13.7 instead of 10.3; with 24, 64
+// sequences with short own parts take 70 instead of 66.
+constexpr int kPairCost = 8, kSingleCost = 5, kSegmentCost = 18;
+// One K/V tile for rt row tiles.
+__host__ __device__ constexpr int tile_cost(int rt) { return (rt >> 1) * kPairCost + (rt & 1) * kSingleCost; }
+// A range holds a segment of two tiles of a single (a few own positions and the
+// window) or one of a pair at least: with one tile, two short sequences take
+// 11.7 instead of 9.6 us.
+constexpr int kMinRange = kSegmentCost + 2 * kSingleCost;
+static_assert(kMinRange >= kSegmentCost + kPairCost, "a segment fits a range");
 
 // The line cut into n ranges of at least kMinRange: range c starts at
 // ceil(c * total / n), which is c * (total / n) + ceil(c * (total % n) / n),
@@ -278,28 +281,28 @@ struct Span {
 // Items of one family on the line: per (group or sequence, kv head) chunks of
 // `chunk` tiles, each with one segment per set (pairs, then the single).
 struct Family {
-  int rt, pairs, sets, unit, chunk;
+  int rt, pairs, sets, tile, chunk;
   float inv;
   __device__ __forceinline__ void set(const PrefixKArgs& a, int kind, int range) {
     rt = a.row_tiles[kind];
     pairs = rt >> 1;
     sets = (rt + 1) >> 1;
-    unit = unit_cost(kind);
+    tile = tile_cost(rt);
     // The most tiles whose segment fits a range.
-    chunk = max(1, quotient(range - kSegmentCost, pairs ? 2 * unit : unit));
+    chunk = max(1, quotient(range - kSegmentCost, pairs ? kPairCost : kSingleCost));
     inv = __frcp_rn((float)chunk);
   }
   __device__ __forceinline__ int count(int tiles) const {
     return quotient(tiles + chunk - 1, chunk, inv);
   }
   // Length on the line of a chunk of m tiles; of all tiles of one kv head.
-  __device__ __forceinline__ int chunk_length(int m) const { return m * rt * unit + sets * kSegmentCost; }
+  __device__ __forceinline__ int chunk_length(int m) const { return m * tile + sets * kSegmentCost; }
   __device__ __forceinline__ int length(int tiles) const {
-    return tiles * rt * unit + count(tiles) * sets * kSegmentCost;
+    return tiles * tile + count(tiles) * sets * kSegmentCost;
   }
   // Set y of a chunk of m tiles at pos.
   __device__ __forceinline__ Span segment(int m, int y, int pos) const {
-    return {pos + y * (m * 2 * unit + kSegmentCost), m, y < pairs ? 2 * unit : unit};
+    return {pos + y * (m * kPairCost + kSegmentCost), m, y < pairs ? kPairCost : kSingleCost};
   }
 };
 
@@ -312,7 +315,7 @@ struct Walk {
   const PrefixKArgs& a;
   Family fam;
   int snap, b0, b1, range;
-  int m;                                // device search: tiles of a single's segment
+  int m;                                // device search: the most a segment's tiles cost
   int kind, gi, h, c, y;
   int pos, place, len, tiles, chunks;   // pos, place: of chunk c and its first segment
   bool one;                             // a split CTA: its segment is in `only`
@@ -347,19 +350,19 @@ struct Walk {
     if (wp == 0 || a.count[0] * a.hkv * ((rt + 1) >> 1) > a.grid) return 0;
     // Candidates from the even share on, lane 0 first.
     const int share = quotient_up(wp + wo, a.grid, a.inv_grid);
-    const int least = max(4, quotient_up(share, unit_cost(0)));
-    int x = (least + quotient(least * lane, 24) + 1) & ~1;
-    const float inv_s = __frcp_rn((float)x), inv_p = __frcp_rn((float)(x >> 1));
+    const int least = max(16, share);
+    const int x = least + quotient(least * lane, 24);
+    const float inv = __frcp_rn((float)x);
     int ctas = 0;
     for (int g = 0; g < a.count[0]; ++g) {
       const int t = g < 32 ? __shfl_sync(0xffffffffu, t0, g) : tiles_at(0, g);
-      ctas += pairs * quotient(t + (x >> 1) - 1, x >> 1, inv_p) + single * quotient(t + x - 1, x, inv_s);
+      ctas += pairs * quotient_up(t * kPairCost, x, inv) + single * quotient_up(t * kSingleCost, x, inv);
     }
     ctas *= a.hkv;
     const int own = a.grid - ctas;       // CTAs left
     const bool fits = wo ? own > 0 : own >= 0;
     const unsigned longest =
-        fits ? (unsigned)max(x * unit_cost(0) + kSegmentCost, wo ? quotient_up(wo, own) : 0) : ~0u;
+        fits ? (unsigned)max(x + kSegmentCost, wo ? quotient_up(wo, own) : 0) : ~0u;
     const unsigned least_of = __reduce_min_sync(0xffffffffu, longest);
     if (least_of == ~0u) return 0;
     const int src = __ffs((int)__ballot_sync(0xffffffffu, longest == least_of)) - 1;
@@ -453,11 +456,11 @@ struct Walk {
     const int t0 = lane < a.count[0] && a.split == 0 ? tiles_at(0, lane) : 0;
     const int t1 = lane < a.count[1] ? tiles_at(1, lane) : 0;
     const int2 s1 = sums(1, t1, nullptr);
-    int on_line = a.hkv * (s1.x * a.row_tiles[1] * unit_cost(1) +
+    int on_line = a.hkv * (s1.x * tile_cost(a.row_tiles[1]) +
                            s1.y * ((a.row_tiles[1] + 1) >> 1) * kSegmentCost);
     int split = a.split;
     if (split == 0) {
-      const int wp = sums(0, t0, nullptr).x * a.hkv * a.row_tiles[0] * unit_cost(0);
+      const int wp = sums(0, t0, nullptr).x * a.hkv * tile_cost(a.row_tiles[0]);
       split = search(t0, wp, on_line);
       if (!split) on_line += wp;
       if (write && lane == 0) a.plan[0] = split ? 1 : 0;
@@ -470,7 +473,7 @@ struct Walk {
     for (int k = split ? 1 : 0; k < 2; ++k) {
       fam.set(a, k, range);
       const int2 x = sums(k, k ? t1 : t0, &fam);
-      total += a.hkv * (x.x * fam.rt * fam.unit + x.y * fam.sets * kSegmentCost);
+      total += a.hkv * (x.x * fam.tile + x.y * fam.sets * kSegmentCost);
     }
     const Cut cut(total, ctas);
     snap = cut.q >> 4;
@@ -490,8 +493,8 @@ struct Walk {
         int length = 0, mine = 0, segs = 0;
         if (is_split) {
           const int pairs = a.row_tiles[0] >> 1;
-          const int np = pairs ? quotient_up(t, m >> 1) : 0;
-          const int ns = a.row_tiles[0] & 1 ? quotient_up(t, m) : 0;
+          const int np = pairs ? quotient_up(t * kPairCost, m) : 0;
+          const int ns = a.row_tiles[0] & 1 ? quotient_up(t * kSingleCost, m) : 0;
           mine = (pairs * np + ns) * a.hkv;
           segs = np | ns << 16;
         } else {
@@ -1539,8 +1542,9 @@ PrefixKArgs shape_args(const PrefixArgs& p, int sms, Layout* lay) {
 
 // The split of prefixes of one length (Walk::search for those on the device):
 // the M, from the even share on, whose longest CTA is the shortest, the own
-// parts taking equal shares of the CTAs left.  Own parts whose lengths are on the device count as 5/8 of the longest: batches of
-// continuations lie between a third of that and all of it.
+// parts taking equal shares of the CTAs left.  Own parts whose lengths are on
+// the device count as 5/8 of the longest: batches of continuations lie between
+// a third of that and all of it.
 void host_split(PrefixKArgs& a, bool lengths_given, bool own_given) {
   a.split = a.np = a.ns = a.range = 0;
   const long long tp = (a.n[0] + kTile - 1) / kTile;
@@ -1548,21 +1552,21 @@ void host_split(PrefixKArgs& a, bool lengths_given, bool own_given) {
   const long long to = (own_given ? (5 * most + 7) / 8 : most) + a.win_tiles;
   const int rt = a.row_tiles[0], pairs = rt / 2, single = rt & 1;
   if (lengths_given || tp == 0 || (long long)a.count[0] * a.hkv * ((rt + 1) / 2) > a.grid) return;
-  const long long wp = tp * rt * a.count[0] * a.hkv * unit_cost(0);
-  const long long wo = to * a.count[1] * a.hkv * a.row_tiles[1] * unit_cost(1) +
+  const long long wp = tp * tile_cost(rt) * a.count[0] * a.hkv;
+  const long long wo = to * a.count[1] * a.hkv * tile_cost(a.row_tiles[1]) +
                        (to > 0) * (long long)a.count[1] * a.hkv * ((a.row_tiles[1] + 1) / 2) * kSegmentCost;
   const long long share = (wp + wo + a.grid - 1) / a.grid;
-  const long long least = std::max<long long>(2, (share + 3) / unit_cost(0));
+  const long long least = std::max<long long>(16, share);
   long long best = LLONG_MAX;
-  for (long long m = least; m <= 3 * least; ++m) {
-    // A pair's tile is two units.
-    const long long np = pairs ? std::min(tp, (2 * tp + m - 1) / m) : 0;
-    const long long ns = single ? (tp + m - 1) / m : 0;
+  for (int i = 0; i <= 128; ++i) {
+    const long long m = least + least * i / 64;
+    const long long np = pairs ? (tp * kPairCost + m - 1) / m : 0;
+    const long long ns = single ? (tp * kSingleCost + m - 1) / m : 0;
     const long long split = a.count[0] * a.hkv * (pairs * np + ns);
     const long long own = a.grid - split;   // CTAs left
     if (own < (wo > 0)) continue;
     const long long longest =
-        std::max(m * unit_cost(0) + kSegmentCost, wo > 0 ? (wo + own - 1) / own : 0);
+        std::max(m + kSegmentCost, wo > 0 ? (wo + own - 1) / own : 0);
     if (longest >= best) continue;
     best = longest;
     a.split = (int)split;
@@ -1574,7 +1578,7 @@ void host_split(PrefixKArgs& a, bool lengths_given, bool own_given) {
     a.split = 0;
     return;
   }
-  const long long tiles = to * a.count[1] * a.hkv * a.row_tiles[1] * unit_cost(1);
+  const long long tiles = to * a.count[1] * a.hkv * tile_cost(a.row_tiles[1]);
   a.range = (int)std::max<long long>(kMinRange, tiles / std::max<long long>(1, a.grid - a.split));
 }
 
