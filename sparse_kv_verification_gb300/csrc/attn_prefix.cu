@@ -1521,13 +1521,15 @@ PrefixKArgs shape_args(const PrefixArgs& p, int sms, Layout* lay) {
   size_t at = 0;
   for (int k = 0; k < 2; ++k) {
     // Places on the line: two per segment, a segment per set and chunk.  A
-    // chunk has as many tiles as a range allows (at least one), so beside one
-    // per item there are at most about four segments per CTA (the most at
-    // ranges just above kMinRange; towards one with longer ones).
+    // range r is at least a CTA's even share of the tiles' cost, and a chunk
+    // costs a set more than r - kSegmentCost - kPairCost, or is one tile: so
+    // beside one per item there are at most (r + 1) / 6.5 segments per CTA for
+    // r up to 33 (chunks of one tile, a pair and a single), fewer beyond.
+    static_assert(kPairCost == 8 && kSingleCost == 5 && kSegmentCost == 18, "six segments a CTA");
     a.streams[k] = a.row_tiles[k] > 1 ? 2 : 1;
     const size_t items = (size_t)a.count[k] * a.hkv * ((a.row_tiles[k] + 1) / 2);
     const size_t tiles = (a.n[k] + kTile - 1) / kTile + (k ? a.win_tiles : 0);
-    const size_t segs = std::min(items * tiles, items + 4 * (size_t)a.grid);
+    const size_t segs = std::min(items * tiles, items + 6 * (size_t)a.grid);
     const size_t rows = std::max<size_t>(2 * segs, a.grid) * a.streams[k] * a.slot_rows[k];
     lay->o[k] = at;
     at += align256(rows * p.d * sizeof(float));

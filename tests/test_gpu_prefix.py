@@ -324,3 +324,54 @@ def test_long_prefix_against_fp64_on_the_gpu():
         err = (o[i].double() - p @ v).abs()
         assert bool((err <= 2.0 ** -8 * (p @ v.abs() + (p @ v).abs()) + 2.0 ** -13).all())
         assert float((lse[i].double() - torch.logsumexp(x, -1)).abs().max()) <= 2e-4
+
+
+def ragged(n, most, seed, always=()):
+    lens = torch.randint(0, most + 1, (n,), generator=I.generator(seed)).tolist()
+    lens[:len(always)] = always
+    return lens
+
+
+PLANS = {   # b, groups, h_q, h_kv, d, w, n_prefix, n_own, page, prefix lengths, own lengths
+    # more prefixes than CTAs: all on the line
+    "prefixes on the line": (200, 200, 8, 1, 64, 2, 700, 100, 16, ragged(200, 700, 1, (0, 700, 1)),
+                             ragged(200, 100, 2)),
+    # lengths on the device: the split is searched there
+    "ragged prefixes": (12, 4, 40, 8, 128, 5, 6000, 300, 64, [6000, 1, 0, 4500],
+                        ragged(12, 300, 3, (0, 300))),
+    "40 ragged groups": (80, 40, 4, 1, 64, 3, 3001, 64, 0, ragged(40, 3001, 4, (3001, 0)), None),
+    "one long prefix among empty ones": (3, 3, 16, 2, 128, 4, 20000, 40, 0, [0, 20000, 1],
+                                         [40, 0, 7]),
+    # lengths known to the host, two pairs of row tiles and a single
+    "pairs and a single": (16, 1, 64, 8, 128, 5, 5000, 400, 16, None, ragged(16, 400, 5, (0, 400))),
+    "pairs and a single, equal lengths": (16, 1, 64, 8, 64, 5, 5000, 130, 0, None, None),
+    # own parts cut over many CTAs, several row tiles of one sequence
+    "a long own part": (2, 1, 8, 1, 64, 3, 0, 30000, 48, None, [30000, 17]),
+    "own row tile pairs": (2, 1, 64, 1, 128, 5, 1000, 3000, 0, None, [3000, 129]),
+    # three row tiles over 387 tiles: segments of one tile, the most there are
+    "segments of one tile": (1, 1, 64, 1, 64, 5, 0, 49400, 0, None, None),
+    "segments of one tile, ragged": (1, 1, 64, 1, 64, 5, 0, 60000, 16, None, [49400]),
+    "equal own parts": (16, 2, 16, 2, 128, 1, 0, 2048, 64, None, None),
+}
+
+
+@pytest.mark.parametrize("plan", PLANS)
+def test_plans(plan):
+    """The ways the work is shared out, at sizes where CTAs hold parts of
+    items, against fp64 on the GPU."""
+    b, groups, hq, hkv, d, w, n_p, n_o, page, plen, olen = PLANS[plan]
+    c = Case(b, groups, hq, hkv, d, w, n_p, n_o, page=page, prefix_len=plen, own_len=olen, seed=31)
+    o, lse = c.run()
+    f = lambda x: x.to(DEV).double()
+    diagonal = torch.ones(w, w, dtype=torch.bool, device=DEV).triu(1)
+    for i in range(b):
+        g = i // (b // groups)
+        ends = (plen[g] if plen else n_p, olen[i] if olen else n_o)
+        k, v = (torch.cat([f(c.kv[0][x])[g, :, :ends[0]], f(c.kv[1][x])[i, :, :ends[1]],
+                           f(c.win[x])[i]], 1).repeat_interleave(hq // hkv, 0) for x in range(2))
+        x = f(c.q)[i] @ k.transpose(1, 2) * c.scale
+        x[:, :, -w:].masked_fill_(diagonal, -np.inf)
+        p = torch.softmax(x, -1)
+        err = (o[i].double() - p @ v).abs()
+        assert bool((err <= 2.0 ** -8 * (p @ v.abs() + (p @ v).abs()) + 2.0 ** -13).all()), i
+        assert float((lse[i].double() - torch.logsumexp(x, -1)).abs().max()) <= 2e-4, i
