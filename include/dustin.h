@@ -378,7 +378,7 @@ int dustin_full_verify_attn_window(int b, int h_q, int h_kv, int d, int w, int n
  * (DUSTIN_DEVFLAG_PAGE_RANGE).  DUSTIN_ATTN_KV_READY is accepted, without
  * effect.  Sums are taken in a fixed order: equal calls give equal bits.
  * Limits: as dustin_sparse_verify_attn; kv strides below 2^39 elements; b <=
- * 2^20; n_prefix, n_own <= 2^27; 2^25 products of 128 rows with 128 positions
+ * 2^20; n_prefix, n_own <= 2^27; 2^23 products of 128 rows with 128 positions
  * in all; a workspace of 2^35 bytes.  Beyond them: DUSTIN_ERR_SHAPE.
  * Workspace: dustin_prefix_verify_attn_workspace_size (with or without win);
  * its content need not be kept, and calls that may run at the same time (two

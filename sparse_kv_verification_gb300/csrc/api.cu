@@ -822,11 +822,12 @@ static int check_prefix_shape(int b, int groups, int h_q, int h_kv, int d, int w
     return fail(DUSTIN_ERR_SHAPE, "%s: n_prefix=%d", what, n_prefix);
   int rc = check_attn_shape(b, h_q, h_kv, d, w, n_own, what);
   if (rc) return rc;
-  // The line of (row tile, K/V tile) pairs is counted in 32 bits.
+  // The line of (row tile, K/V tile) pairs is counted in 32 bits, and a CTA's
+  // share of it stays where a product in fp32 finds a quotient to within one.
   const double tiles = n_prefix / 128 + 1.0, own = n_own / 128 + w / 128 + 2.0;
   const double rows = (double)(h_q / h_kv) * w;
   if (h_kv * (groups * tiles * (rows * (b / groups) / 128 + 1) + b * own * (rows / 128 + 1)) >
-          (double)(1 << 25) ||
+          (double)(1 << 23) ||
       rows * b * h_kv > (double)(1 << 30) || b > (1 << 20) || n_prefix > (1 << 27) ||
       n_own > (1 << 27))
     return fail(DUSTIN_ERR_SHAPE, "%s: problem too large", what);

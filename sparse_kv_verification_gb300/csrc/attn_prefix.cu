@@ -206,8 +206,9 @@ __device__ __forceinline__ int length_of(const PrefixKArgs& a, int kind, int gi)
 __device__ __forceinline__ int tiles_of(const PrefixKArgs& a, int kind, int len) {
   return (len + kTile - 1) / kTile + (kind ? a.win_tiles : 0);
 }
-// Quotient of x >= 0 by d > 0 from inv, 1 / d in fp32: below 2^21 (which the
-// host's limits ensure) the estimate is at most one off.
+// Quotient of x >= 0 by d > 0 from inv, 1 / d in fp32: below 2^22 (which the
+// host's limits ensure) three roundings of 2^-24 leave the estimate at most one
+// off.
 __device__ __forceinline__ int quotient(int x, int d, float inv) {
   const int q = (int)((float)x * inv), r = x - q * d;
   return q + (r >= d) - (r < 0);
