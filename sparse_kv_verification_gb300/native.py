@@ -158,20 +158,22 @@ def kv_desc(k: torch.Tensor, v: Optional[torch.Tensor] = None,
     """Describes a KV cache.  Contiguous: k (and v) [b][h_kv][n][d].
     Paged: k (and v) are pools [pages][h_kv][page_size][d] and page_table is
     int32 [b][pages_per_seq].  K and V must share strides."""
-    if k.dtype != torch.bfloat16 or k.dim() != 4 or k.stride(3) != 1:
+    strides = k.stride()
+    if k.dtype != torch.bfloat16 or len(strides) != 4 or strides[3] != 1:
         raise ValueError("k must be a bf16 4-D tensor with a contiguous last dim")
-    if v is not None and (v.shape != k.shape or v.stride() != k.stride()
-                          or v.dtype != k.dtype):
+    if v is not None and (v.shape != k.shape or v.stride() != strides
+                          or v.dtype != torch.bfloat16):
         raise ValueError("v must match k in shape, strides and dtype")
     table, page_size, pages_per_seq, num_pages = None, 0, 0, 0
     if page_table is not None:
-        if page_table.dtype != torch.int32 or page_table.dim() != 2:
+        rows = page_table.stride()
+        if page_table.dtype != torch.int32 or len(rows) != 2:
             raise ValueError("page_table must be int32 [b][pages_per_seq]")
-        if page_table.stride(1) != 1:
+        if rows[1] != 1:
             raise ValueError("page_table rows must be contiguous")
-        table, page_size = page_table.data_ptr(), k.shape[2]
-        pages_per_seq, num_pages = page_table.stride(0), k.shape[0]
-    sb, sh, sn, _ = k.stride()
+        num_pages, _, page_size, _ = k.shape
+        table, pages_per_seq = page_table.data_ptr(), rows[0]
+    sb, sh, sn, _ = strides
     return DustinKV(k.data_ptr(), None if v is None else v.data_ptr(), sb, sh, sn, table,
                     page_size, pages_per_seq, num_pages)
 
@@ -572,7 +574,7 @@ def _run(fn, index: int, stream, *args) -> None:
     """Calls fn(*args, stream) with device `index` current."""
     raw = stream.cuda_stream if stream is not None else \
         torch._C._cuda_getCurrentRawStream(index)
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         _check(fn(*args, raw))
     else:
         with torch.cuda.device(index):
