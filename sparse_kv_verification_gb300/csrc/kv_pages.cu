@@ -183,8 +183,11 @@ constexpr int kResizeThreads = 1024;
 constexpr int kResizeCluster = 8;
 constexpr int kDropBlock = 256;   // table entries a warp drops at a time
 
+constexpr int kNames = 2 * kResizeMaxList;   // a power of two, half empty
+
 struct ResizeShared {
   int seq[kResizeMaxList];
+  int name[kNames], first_named[kNames];   // sequences by hash, their first entries
   int had[kResizeMaxList];      // pages before; -1: entry left out
   int have[kResizeMaxList];     // pages after
   int last[kResizeMaxList];     // last page to be copied (-1: none)
@@ -235,11 +238,25 @@ __global__ void __launch_bounds__(kResizeThreads) kv_resize_kernel(const ResizeA
   const long long cap = (long long)a.pages_per_seq * a.page_size;
   int old = 0, now = 0, seq = -1;
   bool ok = false;
+  for (int i = tid; i < kNames; i += threads) {
+    sh.name[i] = -1;
+    sh.first_named[i] = kResizeMaxList;
+  }
+  __syncthreads();
+  int at = 0;
   if (tid < a.n_list) {
     seq = __ldg(a.seqs + tid);
     sh.seq[tid] = seq;
     ok = seq >= 0 && seq < a.n_seqs;
     if (ok) {
+      // Its place: the next free one from its hash (1024 names leave half of
+      // them free).  Comparing with every entry before took 10 us of 1024.
+      at = (int)(((unsigned)seq * 2654435761u) >> 16) & (kNames - 1);
+      for (int i = 0; i < kNames; ++i, at = (at + 1) & (kNames - 1)) {
+        const int there = atomicCAS(&sh.name[at], -1, seq);
+        if (there == -1 || there == seq) break;
+      }
+      atomicMin(&sh.first_named[at], tid);
       now = a.new_len ? __ldg(a.new_len + tid) : 0;
       old = __ldcg(a.seq_len + seq);
       ok = now >= 0 && now <= cap && old >= 0 && old <= cap;
@@ -247,8 +264,7 @@ __global__ void __launch_bounds__(kResizeThreads) kv_resize_kernel(const ResizeA
   }
   __syncthreads();
   if (tid < a.n_list) {
-    for (int j = 0; j < tid; ++j)
-      if (sh.seq[j] == seq) ok = false;
+    if (ok && sh.first_named[at] != tid) ok = false;
     if (!ok && rank == 0) raise_flag(DUSTIN_DEVFLAG_INDEX_RANGE);
     sh.newlen[tid] = now;
     sh.had[tid] = ok ? (old + a.page_size - 1) / a.page_size : -1;
