@@ -27,7 +27,7 @@
 //    for, one CTA per (list entry, layer, K or V).
 // Measured, a turn of a serving loop (release, fork, grow with its copies): 64
 // samples of four prompts of 32749 positions on pages of 16, four layers of 8
-// heads, 37.6 us; four samples of one prompt of 2051 14.7.  Every launch is
+// heads, 35.7 us; four samples of one prompt of 2051 14.2.  Every launch is
 // bound by its latency: the pages' rows copied take 0.6 us of bandwidth.
 #include <algorithm>
 #include <cooperative_groups.h>
@@ -352,17 +352,26 @@ __global__ void __launch_bounds__(kResizeThreads) kv_resize_kernel(const ResizeA
     __syncthreads();
     free_all = sh.free_all;
     r += sh.base;
-    for (int wd = w0; wd < w1 && r < wanted; ++wd) {
-      unsigned bits = bitmap[wd];
-      while (bits && r < wanted) {
-        const int pg = lo + wd * 32 + __ffs((int)bits) - 1;
-        bits &= bits - 1;
-        // The entry whose ranks hold r: the last with first <= r.  Entries
+    // A warp gives out its threads' words one after another, a lane to a page:
+    // the free pages of the lowest numbers often lie in a few words.
+    unsigned todo = __ballot_sync(0xffffffffu, count > 0 && r < wanted);
+    while (todo) {
+      const int src = __ffs((int)todo) - 1;
+      todo &= todo - 1;
+      int before = __shfl_sync(0xffffffffu, r, src);
+      const int s0 = __shfl_sync(0xffffffffu, w0, src), s1 = __shfl_sync(0xffffffffu, w1, src);
+      for (int wd = s0; wd < s1 && before < wanted; ++wd) {
+        const unsigned bits = bitmap[wd];
+        const int mine = before + __popc(bits & ((1u << lane) - 1));
+        before += __popc(bits);
+        if (!(bits >> lane & 1) || mine >= wanted) continue;
+        const int pg = lo + wd * 32 + lane;
+        // The entry whose ranks hold it: the last with first <= mine.  Entries
         // without need share their first with the next one, which is later.
         int x = 0, y = a.n_list - 1;
         while (x < y) {
           const int mid = (x + y + 1) >> 1;
-          if (sh.first[mid] <= r)
+          if (sh.first[mid] <= mine)
             x = mid;
           else
             y = mid - 1;
@@ -370,7 +379,7 @@ __global__ void __launch_bounds__(kResizeThreads) kv_resize_kernel(const ResizeA
         const int end = x + 1 < a.n_list ? sh.first[x + 1] : wanted;
         if (end <= free_all) {   // the whole entry is served
           const int cow = sh.last[x] >= 0 ? 1 : 0;
-          const int slot = r - sh.first[x] - cow;
+          const int slot = mine - sh.first[x] - cow;
           a.page_table[(long long)sh.seq[x] * a.pages_per_seq + sh.had[x] + slot] = pg;
           a.refcount[pg] = 1;
           if (slot < 0) {
@@ -378,7 +387,6 @@ __global__ void __launch_bounds__(kResizeThreads) kv_resize_kernel(const ResizeA
             a.copies[2 * x + 1] = pg;
           }
         }
-        ++r;
       }
     }
   }
@@ -455,11 +463,13 @@ cudaError_t launch_resize(const ResizeArgs& a, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   cudaError_t e = ensure_smem_attr(kv_resize_kernel, kResizeMaxPages / kResizeCluster / 8, done);
   if (e != cudaSuccess) return e;
-  // A small update runs in one CTA: its barriers cost a tenth of a cluster's,
-  // and 8192 counts are eight loads a thread.
-  const bool small = a.num_pages <= 8192 && (long long)a.n_list * a.pages_per_seq <= 8192;
+  // A small update runs in one CTA, whose barriers cost less than a cluster's.
+  // Measured, 8 entries grown by a page and released: of 1024 pages 8.4 us in
+  // one CTA, 9.3 in the cluster, of 4096 10.9 and 9.3; 32 entries of 1024 pages
+  // 10.5 and 9.7.
+  const bool small = a.num_pages <= 1024 && a.n_list <= 16 && (long long)a.n_list * a.pages_per_seq <= 8192;
   const int C = small ? 1 : kResizeCluster;
-  const int threads = small && a.n_list <= 256 ? 256 : kResizeThreads;
+  const int threads = small ? 256 : kResizeThreads;
   const int words = ((a.num_pages + C - 1) / C + 31) / 32;
   e = launch_pdl_cluster(kv_resize_kernel, dim3((unsigned)C), dim3((unsigned)threads),
                          (size_t)words * sizeof(unsigned), st, (unsigned)C, a);
