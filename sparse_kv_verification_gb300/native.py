@@ -649,15 +649,17 @@ def dustin_verify_tokens(p_target: torch.Tensor, p_draft: Optional[torch.Tensor]
     dtype = p_target.dtype
     if dtype != torch.float32 and dtype != torch.bfloat16:
         raise ValueError("probabilities are fp32 or bf16")
+    # Checked one by one: an expanded row (stride 0) would be read past its end.
     tb, tw, row = p_target.stride()
+    if row != 1 and vocab > 1:
+        raise ValueError("p_target's vocabulary rows must be contiguous")
     db, dw = 0, 0
     if p_draft is not None:
         if p_draft.dtype != dtype or p_draft.shape != (b, w - 1, vocab):
             raise ValueError("p_draft must be [b][w-1][vocab] of p_target's type")
-        db, dw, row2 = p_draft.stride()
-        row = max(row, row2)
-    if row != 1 and vocab > 1:
-        raise ValueError("vocabulary rows must be contiguous")
+        db, dw, row = p_draft.stride()
+        if row != 1 and vocab > 1 and w > 1:
+            raise ValueError("p_draft's vocabulary rows must be contiguous")
     if w > 1:
         if draft is None or u_accept is None:
             raise ValueError("draft and u_accept are required")
