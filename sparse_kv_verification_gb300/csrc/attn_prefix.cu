@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < C::SLOTS; ++i) {
-      mbar_init(smem_u32(&sh.full[i]), 1);
+      mbar_init(smem_u32(&sh.full[i]), 2);   // both load warps
       mbar_init(smem_u32(&sh.empty[i]), 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -775,7 +775,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // --------------------------------------------------------- K and V loads
     // Two warps, each with half of a tile's boxes: a warp's lanes issue their
     // boxes one after another (pages of 16 make 24 of them a tile: with one warp
-    // own parts on such pages were read at 5.0 TB/s, with two at 6.0).
+    // own parts on such pages were read at 5.0 TB/s, with two at 6.0).  Both
+    // arrive on every slot, the second one also where it has no box of the tile
+    // (tiles of one box: no half of V, at d 64 none of K either): a warp that
+    // fell a lap of the ring behind would wait for a phase already gone.
     role_begin();
     const bool second = warp == kLoadWarp2;
     int slot = 0, tile_count = 0;
@@ -849,7 +852,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           page_v0 = page_v1;
           --pending;
         }
-        if (!second && lane == 0) mbar_arrive_expect_tx(bar, C::TILE_BYTES);
+        if (lane == 0) {
+          if (second)
+            mbar_arrive(bar);
+          else
+            mbar_arrive_expect_tx(bar, C::TILE_BYTES);
+        }
         __syncwarp();
         if (is_k) {
           if (half < D / 64 && (D == 128 ? half : run & 1) == second)

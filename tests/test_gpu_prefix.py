@@ -375,3 +375,28 @@ def test_plans(plan):
         err = (o[i].double() - p @ v).abs()
         assert bool((err <= 2.0 ** -8 * (p @ v.abs() + (p @ v).abs()) + 2.0 ** -13).all()), i
         assert float((lse[i].double() - torch.logsumexp(x, -1)).abs().max()) <= 2e-4, i
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [0, 128])
+def test_tiles_of_one_box(d, page):
+    """Tiles loaded as one box (contiguous caches, pages of 128): the second of
+    the two load warps has no box of V, at d 64 none of K either, and must keep
+    up with the ring all the same.  Many laps, short and long segments, launch
+    after launch: no wait runs out, equal bits."""
+    g = I.generator(d + page)
+    own = torch.randint(0, 4, (24,), generator=g).mul(100).tolist()
+    c = Case(24, 1, 4, 1, d, 3, 2500, 300, page=page, own_len=own, seed=d)
+    long = Case(1, 1, 16, 8, d, 2, 0, 60000, page=page, win=False, seed=d + 1)
+    first = c.check()
+    q, a, ws = c.q.to(DEV), c.args(), c.workspace()
+    lq, la, lws = long.q.to(DEV), long.args(), long.workspace()
+    o, lse = torch.empty_like(first[0]), torch.empty_like(first[1])
+    lo, llse = torch.empty_like(lq), torch.empty(lq.shape[:3], device=DEV)
+    for _ in range(100):
+        N.dustin_prefix_verify_attn(q=q, o=o, lse=lse, ws=ws, **a)
+        N.dustin_prefix_verify_attn(q=lq, o=lo, lse=llse, ws=lws, **la)
+    H.sync()
+    assert flags() == 0
+    assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+    assert all(torch.equal(x, y) for x, y in zip((lo, llse), long.run()))
