@@ -358,7 +358,8 @@ int dustin_full_verify_attn_window(int b, int h_q, int h_kv, int d, int w, int n
  *                of scale * q . K, times V;   lse = log sum exp (natural)
  * for g = i / (b / groups).  The prefix is read once per kv head and row
  * tile of 256 query rows, not once per sequence.  A row that sees no
- * position gives o = 0, lse = -inf.
+ * position, or only scores of -inf, gives o = 0, lse = -inf.  A row with a
+ * score that is NaN or +inf gives NaN, o and lse.
  *
  *   q           bf16 [b][h_q][w][d], device (contiguous); o like q; lse fp32
  *               [b][h_q][w]

@@ -1392,7 +1392,9 @@ __global__ void __launch_bounds__(kCombineThreads)
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
       const float ref = top == -INFINITY ? 0.f : top;
-      const bool s0 = p0.x != -INFINITY, s1 = p1.x != -INFINITY;   // else O may be unwritten
+      // A sum of 0: nothing seen, O may be unwritten.  Not so where it is NaN,
+      // whatever the maximum (which leaves NaN scores out): that is kept.
+      const bool s0 = p0.y != 0.f, s1 = p1.y != 0.f;
       const float w0 = ex2(p0.x - ref), w1 = ex2(p1.x - ref);
       float sum = (s0 ? w0 * p0.y : 0.f) + (s1 ? w1 * p1.y : 0.f);
 #pragma unroll
@@ -1463,12 +1465,12 @@ __global__ void __launch_bounds__(kCombineThreads)
   const int to = blockIdx.x * ROWS + out_row;
   if (to >= c.rows) return;
   const float m = m_of[out_row], l = l_of[out_row];
-  const float inv = m == -INFINITY ? 0.f : 1.f / l;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   // The columns' order of the partials.
   uint32_t* out = reinterpret_cast<uint32_t*>(c.o + (long long)to * D) + piece / 4 * 8 + piece % 4;
   out[0] = pack_bf16(acc.x * inv, acc.y * inv);
   out[4] = pack_bf16(acc.z * inv, acc.w * inv);
-  if (piece == 0) c.lse[to] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
+  if (piece == 0) c.lse[to] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // ---- host side

@@ -400,3 +400,67 @@ def test_tiles_of_one_box(d, page):
     assert flags() == 0
     assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
     assert all(torch.equal(x, y) for x, y in zip((lo, llse), long.run()))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [0, 16])
+@pytest.mark.parametrize("where", ["one row of q", "one sequence of q", "a key of the prefix",
+                                   "a key of one sequence", "a key of one window"])
+def test_nan_scores_stay_nan(where, page, d):
+    """A row with a NaN score is NaN, o and lse, also where all its scores are
+    NaN or its other parts see nothing; the other rows are what they are.  The
+    shape has row tile pairs and a single, segments of one tile and of several."""
+    c = Case(7, 1, 16, 2, d, 5, 900, 300, page=page, prefix_len=[897], seed=d + page,
+             own_len=[300, 0, 129, 1, 257, 0, 40])
+    clean = c.run()
+    nan = float("nan")
+    if where == "one row of q":
+        c.q[2, 9, 3, 5] = nan
+    elif where == "one sequence of q":
+        c.q[1] = nan
+    else:
+        i, at, j = {"a key of the prefix": (0, 0, 600), "a key of one sequence": (4, 1, 200),
+                    "a key of one window": (5, 2, 1)}[where]
+        x = (c.kv + [c.win])[at][0]
+        x[i, 1, j, 7] = nan
+        if at == 2:
+            c.dev_win[0].copy_(x)
+        elif page:
+            c.stored[at][0][int(c.tables[at][i, j // page]), 1, j % page, 7] = nan
+        else:
+            c.stored[at][0].copy_(torch.where(torch.isnan(c.stored[at][0]), c.stored[at][0],
+                                              x.to(DEV)))
+    o, lse = c.run()
+    want_o, want_lse, spread = c.oracle()
+    bad = np.isnan(want_lse)
+    assert bad.any() and not bad.all()
+    np.testing.assert_array_equal(np.isnan(want_o), np.broadcast_to(bad[..., None], want_o.shape))
+    np.testing.assert_array_equal(np.isnan(H.f64(lse)), bad)
+    np.testing.assert_array_equal(np.isnan(H.f64(o)), np.isnan(want_o))
+    good = ~bad
+    err = np.abs(H.f64(o) - want_o)[good]
+    assert np.all(err <= (2.0 ** -8 * (spread + np.abs(want_o)) + 2.0 ** -13)[good])
+    np.testing.assert_allclose(H.f64(lse)[good], want_lse[good], atol=2e-4, rtol=0)
+    assert not torch.isnan(clean[0]).any() and flags() == 0
+
+
+def test_nan_and_infinite_scores_of_rows_with_little_to_see():
+    """A NaN in the only position a row sees, in any part; scores of -inf alone
+    are as nothing seen, one of +inf is NaN."""
+    for n_p, n_o, win in ((1, 0, False), (0, 1, False), (0, 0, True), (40, 3, False)):
+        c = Case(3, 1, 4, 2, 64, 1, n_p, n_o, win=win, seed=n_p)
+        c.q[1] = float("nan")
+        o, lse = c.run()
+        nan = torch.isnan(lse).cpu()
+        assert nan[1].all() and not nan[[0, 2]].any()
+        assert torch.isnan(o[1]).all() and not torch.isnan(o[[0, 2]]).any()
+    c = Case(2, 1, 2, 1, 64, 1, 200, 3, win=False, seed=1, own_len=[0, 3])
+    c.q.fill_(1.0)
+    c.stored[0][0].fill_(float("-inf"))
+    o, lse = c.run()                                 # sequence 1 still sees its own three
+    assert not o[0].any() and torch.isneginf(lse[0]).all()
+    s = (c.q[1, 0, 0].double() @ c.kv[1][0][1, 0].double().T) * c.scale
+    assert abs(float(torch.logsumexp(s, -1)) - float(lse[1, 0, 0])) < 2e-4
+    c.stored[0][0][0, 0, 150] = float("inf")
+    o, lse = c.run()
+    assert torch.isnan(o).all() and torch.isnan(lse).all()
