@@ -280,16 +280,19 @@ __global__ void __launch_bounds__(kThreads, 2) verify_tokens_kernel(const TokenA
       const double upto = scan16(theirs, lane);
       const double total = __shfl_sync(0xffffffffu, upto, kWarps - 1);
       const double before = rank ? __shfl_sync(0xffffffffu, upto, rank - 1) : 0.0;
-      const double u = (double)u_here;
-      double t = u > 0.0 ? u * total : 0.0;
-      if (t >= total) t = total * (1.0 - 0x1p-53);
+      // From u = 1 on, the last token with mass, however little: its mass need
+      // not show in the sums, so no finite t finds it.
+      const bool top = u_here >= 1.f;
+      const double t = top ? (double)INFINITY : u_here > 0.f ? (double)u_here * total : 0.0;
       // The first range with mass that ends behind t, the last one with mass
       // should rounding at the upper end leave none.
       const double base = before + (run - mine);
       const unsigned has = __ballot_sync(0xffffffffu, mine > 0.0);
       const unsigned ends = __ballot_sync(0xffffffffu, mine > 0.0 && before + run > t);
       const double after = __shfl_sync(0xffffffffu, upto, rank);
-      const bool owner = total > 0.0 && before <= t && t < after && has;
+      const unsigned ctas = __ballot_sync(0xffffffffu, theirs > 0.0);
+      const bool owner = top ? ctas && 31 - __clz((int)ctas) == rank
+                             : total > 0.0 && before <= t && t < after && has;
       const int walk = owner ? (ends ? __ffs((int)ends) - 1 : 31 - __clz((int)has)) : -1;
       const double at = __shfl_sync(0xffffffffu, base, walk < 0 ? 0 : walk);
       if (lane == 0) {

@@ -167,6 +167,29 @@ def test_tokens_captured_graph_replays():
         np.testing.assert_array_equal(tok.cpu().numpy(), want[0])
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [70, 5000, 40000])
+def test_tokens_u_of_one_takes_the_last_token_with_mass(vocab, dtype):
+    """However little mass the tail has: 1e-20 beside 1 changes no running sum
+    of 53 bits, and is the last token all the same.  Tails in the same range as
+    the rest, in another warp's, in another CTA's."""
+    tails = [3, 40, vocab // 2 + 1, vocab - 1]
+    p = torch.zeros((2 * len(tails), 2, vocab))
+    for i, t in enumerate(tails):
+        p[2 * i:2 * i + 2, :, 2] = 1.0
+        p[2 * i:2 * i + 2, :, t] = 1e-20
+    p = p.to(dtype)
+    us = torch.tensor([1.0, float(np.nextafter(np.float32(1), np.float32(0)))]).repeat(len(tails))
+    draft = torch.zeros((len(us), 1), dtype=torch.int32)
+    tok, acc = check_tokens(p, None, draft, torch.ones((len(us), 1)), us, None)
+    assert tok[0::2, 0].tolist() == tails and tok[1::2, 0].tolist() == [2] * len(tails)
+    # The same out of a residual, and with u beyond 1.
+    q = torch.zeros((len(us), 1, vocab))
+    q[:, 0, 0] = 1.0
+    tok, _ = check_tokens(p, q.to(dtype), draft, torch.ones((len(us), 1)), us * 2, None)
+    assert tok[:, 0].tolist() == [t for t in tails for _ in range(2)]
+
+
 # ----------------------------------------------------------------- compaction
 
 def caches(b, hkv, n, d, page, layers, seed, spare=3):
