@@ -192,7 +192,7 @@ struct Shared {
   double total, base, t;
   int accepted;
   int walk;                       // warp range to walk (-1: another CTA's)
-  int last;                       // last positive entry seen by the walk
+  int last;                       // last positive entry that starts at or below t
   int found;
 };
 
@@ -286,7 +286,10 @@ __global__ void __launch_bounds__(kThreads, 2) verify_tokens_kernel(const TokenA
       const double t = top ? (double)INFINITY : u_here > 0.f ? (double)u_here * total : 0.0;
       // The first range with mass that ends behind t, the last one with mass
       // should rounding at the upper end leave none.
-      const double base = before + (run - mine);
+      // A range starts where the one below ends, and never beyond t: the walk
+      // would find every sum past t at once.
+      const double below = __shfl_up_sync(0xffffffffu, run, 1);
+      const double base = fmin(lane ? before + below : before, t);
       const unsigned has = __ballot_sync(0xffffffffu, mine > 0.0);
       const unsigned ends = __ballot_sync(0xffffffffu, mine > 0.0 && before + run > t);
       const double after = __shfl_sync(0xffffffffu, upto, rank);
@@ -321,13 +324,14 @@ __global__ void __launch_bounds__(kThreads, 2) verify_tokens_kernel(const TokenA
     for (long long c0 = wlo; c0 < whi; c0 += kThreads * E) {
       Ff x[E];
       Ff mine{0.f, 0.f};
+      int with_mass = -1;   // the thread's last such entry
       const long long j0 = c0 + tid * E;
 #pragma unroll
       for (int i = 0; i < E; ++i) x[i] = j0 + i < whi ? row.at(j0 + i) : Ff{0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < E; ++i) {
         mine = ff_add(mine, x[i]);
-        if (x[i].s > 0.f) atomicMax(&sh.last, (int)(j0 + i));
+        if (x[i].s > 0.f) with_mass = (int)(j0 + i);
       }
       Ff inc = mine;
 #pragma unroll
@@ -346,6 +350,10 @@ __global__ void __launch_bounds__(kThreads, 2) verify_tokens_kernel(const TokenA
         if (lane < kWarps) sh.warp_base[lane + 1] = upto;
       }
       __syncthreads();
+      const bool ends = sh.warp_base[kWarps] > t;   // uniform
+      // Should the sums of a warp's entries, added one by one, not pass t where
+      // its whole sum does: its last entry, or what lies below.
+      if (with_mass >= 0 && (!ends || sh.warp_base[warp] <= t)) atomicMax(&sh.last, with_mass);
       if (sh.warp_base[warp] <= t && t < sh.warp_base[warp + 1]) {
         const double mybase = sh.warp_base[warp];
         if (mybase + ff_value(inc) > t) {
@@ -360,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_tokens_kernel(const TokenA
           }
         }
       }
-      if (sh.warp_base[kWarps] > t) break;   // uniform
+      if (ends) break;
     }
     __syncthreads();
     if (tid == 0)

@@ -1,6 +1,8 @@
 """The serving operators on the GPU against their oracle: drafted tokens,
 cache compaction, shared pages.  Their results are whole numbers and moved
 rows: every comparison is exact."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -188,6 +190,42 @@ def test_tokens_u_of_one_takes_the_last_token_with_mass(vocab, dtype):
     q[:, 0, 0] = 1.0
     tok, _ = check_tokens(p, q.to(dtype), draft, torch.ones((len(us), 1)), us * 2, None)
     assert tok[:, 0].tolist() == [t for t in tails for _ in range(2)]
+
+
+def test_tokens_u_on_the_border_of_two_ranges():
+    """t = u * total equal to the sum below a warp's range (8 entries here),
+    where the range's start found as (sum to its end) - (its own sum) rounds to
+    more than t.  Exactly: C_1 = 1 + 2^-52 = t, so token 8 is the first behind."""
+    e = {0: 1.0, 1: 2.0 ** -52, 8: 1.0, 9: 2.0 ** -51, 16: 2.0, 24: 2.0 ** -52}
+    p = torch.zeros((1, 1, 128))
+    for j, x in e.items():
+        p[0, 0, j] = x
+    exact, total, below = {}, sum(Fraction(x) for x in e.values()), Fraction(0)
+    for j, x in e.items():
+        below += Fraction(x)
+        exact[j] = below
+    assert min(j for j in e if exact[j] > total / 4) == 8 and exact[1] == total / 4
+    below, mine = 1 + 2.0 ** -52, 1 + 2.0 ** -51
+    assert (below + mine) - mine > below             # in 53 bits
+    none = torch.zeros((1, 0))
+    tok, _ = run_tokens(p, None, none.int(), none, torch.tensor([0.25]), None)
+    assert tok.tolist() == [[8]]
+
+
+def test_tokens_sums_that_round_differently_one_by_one():
+    """(1 + 2^-53) + 2^-53 is 1 = t in 53 bits, 1 + (2^-53 + 2^-53) is more: the
+    warp that holds t has no entry behind it, and the draw stays with its
+    entries, or those before, not with the ranges above."""
+    e = {0: 1.0, 517: 2.0 ** -53, 645: 2.0 ** -53, 773: 1.0, 900: 1.0, 1024: 1.0}
+    p = torch.zeros((200, 1, 8192))                  # 200 rows: one CTA each, 512 entries a warp
+    for j, x in e.items():
+        p[:, 0, j] = x
+    total, below = sum(Fraction(x) for x in e.values()), Fraction(0)
+    exact = [j for j in e if (below := below + Fraction(e[j])) > total * Fraction(0.2)]
+    none = torch.zeros((200, 0))
+    for u, want in ((0.2, exact[:1]), (0.25, (517, 645))):
+        tok, _ = run_tokens(p, None, none.int(), none, torch.full((200,), u), None)
+        assert set(tok[:, 0].tolist()) <= set(want)
 
 
 # ----------------------------------------------------------------- compaction
