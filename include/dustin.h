@@ -412,10 +412,12 @@ int dustin_prefix_verify_attn(int b, int groups, int h_q, int h_kv, int d, int w
  * So the tokens follow the target's distribution if u_accept and u_sample
  * are independent uniforms in [0, 1).  With p_draft NULL the drafts are
  * taken as certain (q is 1 at the draft, 0 elsewhere), as for drafts found
- * by lookup.  Entries that are negative, NaN or infinite have no mass.  The
- * sums carry about 48 bits (a row's masses add up to less than 2^127, as
- * probabilities do).  u_sample <= 0 or NaN counts as 0, >= 1 as the
- * last token with mass; a NaN in u_accept rejects.  A draft outside
+ * by lookup.  Entries that are negative, NaN or infinite have no mass: they
+ * count as 0, in the acceptance too, so no u_accept >= 0 accepts a draft
+ * without mass in the target's row.  The sums carry about 48 bits (a row's
+ * masses add up to less than 2^127, as probabilities do).  u_sample <= 0 or
+ * NaN counts as 0, >= 1 as the last token with mass; a NaN in u_accept
+ * rejects.  A draft outside
  * [0, vocab) is rejected and raises DUSTIN_DEVFLAG_INDEX_RANGE.
  *
  *   p_target   [b][w][vocab] of `dtype` (DUSTIN_DTYPE_*), device; row (i, t)

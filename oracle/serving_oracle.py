@@ -40,8 +40,8 @@ def verify_tokens(p, q, draft, n_draft, u_accept, u_sample):
             x = int(draft[i, a])
             if not 0 <= x < vocab:
                 break
-            qx = 1.0 if q is None else q[i, a, x]
-            if not u_accept[i, a] * qx < p[i, a, x]:
+            qx = 1.0 if q is None else _mass(q[i, a, x])
+            if not u_accept[i, a] * qx < _mass(p[i, a, x]):
                 break
             tokens[i, a] = x
             a += 1

@@ -223,8 +223,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_tokens_kernel(const TokenA
         const int x = __ldg(draft + i);
         if (x >= 0 && x < a.vocab) {
           const double u = (double)__ldg(a.u_accept + (long long)bb * (a.w - 1) + i);
-          const double pv = (double)load1(p0 + (long long)i * a.stride_tw + x);
-          const double qv = q0 ? (double)load1(q0 + (long long)i * a.stride_dw + x) : 1.0;
+          const double pv = (double)mass_of(load1(p0 + (long long)i * a.stride_tw + x));
+          const double qv = q0 ? (double)mass_of(load1(q0 + (long long)i * a.stride_dw + x)) : 1.0;
           ok = u * qv < pv;
         } else if (rank == 0) {
           atomicOr(&g_tokens_dev_flags, DUSTIN_DEVFLAG_INDEX_RANGE);

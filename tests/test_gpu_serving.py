@@ -228,6 +228,27 @@ def test_tokens_sums_that_round_differently_one_by_one():
         assert set(tok[:, 0].tolist()) <= set(want)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_tokens_entries_without_mass_at_the_draft(dtype):
+    """Negative, NaN and infinite entries count as 0 in the acceptance too: such
+    a target entry accepts no draft, such a draft entry every one with mass."""
+    nan, inf, vocab = float("nan"), float("inf"), 40
+    none = [0.0, -0.25, -0.75, nan, inf, -inf]
+    pairs = [(x, y) for x in none + [0.5] for y in none + [0.5]]
+    p = torch.zeros((len(pairs), 2, vocab))
+    q = torch.zeros((len(pairs), 1, vocab))
+    p[:, 0, 30], p[:, 1, 31] = 0.5, 1.0
+    for i, (x, y) in enumerate(pairs):
+        p[i, 0, 7], q[i, 0, 7] = x, y
+    draft = torch.full((len(pairs), 1), 7, dtype=torch.int32)
+    ua, us = torch.full((len(pairs), 1), 0.9), torch.zeros(len(pairs))
+    tok, acc = check_tokens(p.to(dtype), q.to(dtype), draft, ua, us, None)
+    assert acc.tolist() == [int(x == 0.5) for x, _ in pairs]
+    assert tok[:, 0].tolist() == [7 if x == 0.5 else 30 for x, _ in pairs]
+    tok, acc = check_tokens(p.to(dtype), None, draft, ua * 0.5, us, None)
+    assert acc.tolist() == [int(x == 0.5) for x, _ in pairs]
+
+
 # ----------------------------------------------------------------- compaction
 
 def caches(b, hkv, n, d, page, layers, seed, spare=3):

@@ -84,3 +84,12 @@ def test_prefix_attention_is_full_attention_over_joined_keys():
     np.testing.assert_allclose(lse, rl, atol=1e-12)
     o, lse = S.prefix_attention(q, kp, vp, ko, vo, 2, 0.3, prefix_len=[0, 0], own_len=[0] * 4)
     assert not o.any() and np.all(np.isneginf(lse))
+
+
+@pytest.mark.parametrize("p,q,want", [(-0.25, -0.75, 0), (float("inf"), 0.5, 0), (float("nan"), 0.0, 0),
+                                      (0.0, -1.0, 0), (0.5, float("nan"), 1), (0.5, float("inf"), 1)])
+def test_entries_without_mass_count_as_zero_in_the_acceptance(p, q, want):
+    rows = np.array([[[p, 0.5], [0.0, 1.0]]])
+    _, a = S.verify_tokens(rows, np.array([[[q, 0.5]]]), np.array([[0]]), None, np.array([[0.9]]),
+                           np.array([0.0]))
+    assert a.tolist() == [want]
