@@ -249,6 +249,39 @@ def test_tokens_entries_without_mass_at_the_draft(dtype):
     assert acc.tolist() == [int(x == 0.5) for x, _ in pairs]
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [32768, 50001])
+def test_tokens_edges_across_ctas(vocab, dtype):
+    """Rows spread over eight CTAs: residuals without mass (summed again from
+    the target's row), rows without mass, one-hot rows at the far end, u at 0,
+    1 and NaN in each."""
+    us = torch.tensor([0.0, 0.37, 0.9999, 1.0, float("nan")])
+    n, g = len(us), I.generator(vocab)
+    kinds = 6
+    p = torch.softmax(3 * torch.randn((kinds * n, 2, vocab), generator=g), -1)
+    q = p[:, :1].clone()
+    ua = torch.ones((kinds * n, 1))
+    draft = torch.randint(0, vocab, (kinds * n, 1), generator=g).int()
+    at = [slice(i * n, (i + 1) * n) for i in range(kinds)]
+    # kind 0: p equal to q, rejected: the residual is empty
+    p[at[1]] = 0                                     # no mass at all
+    p[at[2], 0] = 0
+    p[at[2], 0, vocab - 1] = 0.25                    # one-hot, no mass in the first CTAs
+    q[at[3]] = 1.0                                   # p below q everywhere but in one place
+    q[at[3], 0, vocab - 5] = 0
+    draft[at[3]] = 1
+    p[at[4], 0, vocab // 16:] = 0                    # mass in the first CTA alone
+    q[at[4]] = 0
+    q[at[4], 0, vocab // 16:] = 1.0
+    draft[at[4]] = vocab - 1
+    q[at[5]] = 0                                     # accepted: the next row
+    p, q = p.to(dtype), q.to(dtype)
+    tok, acc = check_tokens(p, q, draft, ua, us.repeat(kinds), None)
+    assert not acc[:5 * n].any() and acc[5 * n:].all()
+    assert (tok[at[1], 0] == -1).all() and (tok[at[2], 0] == vocab - 1).all()
+    assert (tok[at[3], 0] == vocab - 5).all() and (tok[at[4], 0] < vocab // 16).all()
+
+
 # ----------------------------------------------------------------- compaction
 
 def caches(b, hkv, n, d, page, layers, seed, spare=3):
