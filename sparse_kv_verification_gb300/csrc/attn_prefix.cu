@@ -43,6 +43,7 @@
 #include "device_common.cuh"
 #include "dustin.h"
 #include "internal.h"
+#include "quotient.h"
 #include "tcgen05.cuh"
 
 namespace dustin {
@@ -206,20 +207,10 @@ __device__ __forceinline__ int length_of(const PrefixKArgs& a, int kind, int gi)
 __device__ __forceinline__ int tiles_of(const PrefixKArgs& a, int kind, int len) {
   return (len + kTile - 1) / kTile + (kind ? a.win_tiles : 0);
 }
-// Quotient of x >= 0 by d > 0 from inv, 1 / d in fp32: below 2^22 (which the
-// host's limits ensure) three roundings of 2^-24 leave the estimate at most one
-// off.
-__device__ __forceinline__ int quotient(int x, int d, float inv) {
-  const int q = (int)((float)x * inv), r = x - q * d;
-  return q + (r >= d) - (r < 0);
-}
-__device__ __forceinline__ int quotient(int x, int d) {
-  return quotient(x, d, __frcp_rn((float)d));
-}
-__device__ __forceinline__ int quotient_up(int x, int d) { return quotient(x + d - 1, d); }
-__device__ __forceinline__ int quotient_up(int x, int d, float inv) {
-  return quotient(x + d - 1, d, inv);
-}
+// Of the quotients below (quotient.h), those of the whole line by some CTAs have
+// no bound but the line's length (below 2^28), where the CTAs are few: on devices
+// of a few SMs, or where a split leaves few.  The others are counts of tiles,
+// heads, sequences or CTAs, which the host's limits keep below 2^22.
 
 // Work is counted in eighths of a pair's K/V tile.  A tile for one row tile
 // alone costs more than half of that (its K and V come for it alone, and its
@@ -247,8 +238,8 @@ struct Cut {
   __device__ __forceinline__ Cut(int line, int ctas) {
     total = line;
     n = max(1, min(ctas, total / kMinRange));
-    inv = __frcp_rn((float)n);
-    q = quotient(total, n, inv);
+    inv = reciprocal(n);
+    q = quotient_wide(total, n, inv);
     r = total - q * n;
   }
   __device__ __forceinline__ int start(int c) const {
@@ -290,8 +281,9 @@ struct Family {
     sets = (rt + 1) >> 1;
     tile = tile_cost(rt);
     // The most tiles whose segment fits a range.
-    chunk = max(1, quotient(range - kSegmentCost, pairs ? kPairCost : kSingleCost));
-    inv = __frcp_rn((float)chunk);
+    const int room = range - kSegmentCost;
+    chunk = max(1, pairs ? room / kPairCost : room / kSingleCost);
+    inv = reciprocal(chunk);
   }
   __device__ __forceinline__ int count(int tiles) const {
     return quotient(tiles + chunk - 1, chunk, inv);
@@ -350,10 +342,10 @@ struct Walk {
     const int rt = a.row_tiles[0], pairs = rt >> 1, single = rt & 1;
     if (wp == 0 || a.count[0] * a.hkv * ((rt + 1) >> 1) > a.grid) return 0;
     // Candidates from the even share on, lane 0 first.
-    const int share = quotient_up(wp + wo, a.grid, a.inv_grid);
+    const int share = quotient_wide(wp + wo + a.grid - 1, a.grid, a.inv_grid);
     const int least = max(16, share);
-    const int x = least + quotient(least * lane, 24);
-    const float inv = __frcp_rn((float)x);
+    const int x = least + least / 24 * lane + least % 24 * lane / 24;   // by 24ths
+    const float inv = reciprocal(x);
     int ctas = 0;
     for (int g = 0; g < a.count[0]; ++g) {
       const int t = g < 32 ? __shfl_sync(0xffffffffu, t0, g) : tiles_at(0, g);
@@ -363,7 +355,7 @@ struct Walk {
     const int own = a.grid - ctas;       // CTAs left
     const bool fits = wo ? own > 0 : own >= 0;
     const unsigned longest =
-        fits ? (unsigned)max(x + kSegmentCost, wo ? quotient_up(wo, own) : 0) : ~0u;
+        fits ? (unsigned)max(x + kSegmentCost, wo ? quotient_wide(wo + own - 1, own) : 0) : ~0u;
     const unsigned least_of = __reduce_min_sync(0xffffffffu, longest);
     if (least_of == ~0u) return 0;
     const int src = __ffs((int)__ballot_sync(0xffffffffu, longest == least_of)) - 1;
@@ -385,7 +377,7 @@ struct Walk {
     only.pair = z < pairs * np;
     const int part = only.pair ? quotient(z, pairs) : z - pairs * np;
     const int parts = only.pair ? np : ns;
-    const float inv = __frcp_rn((float)parts);
+    const float inv = reciprocal(parts);
     only.rt = only.pair ? 2 * (z - part * pairs) : rt - 1;
     only.t0 = quotient(part * tiles, parts, inv);
     only.n = quotient((part + 1) * tiles, parts, inv) - only.t0;
@@ -468,7 +460,7 @@ struct Walk {
     }
     // A lower bound of the ranges' length, the line's length.
     const int ctas = max(a.grid - split, 1);
-    range = max(kMinRange, quotient(on_line, ctas));
+    range = max(kMinRange, quotient_wide(on_line, ctas));
     int total = 0;
 #pragma unroll 1
     for (int k = split ? 1 : 0; k < 2; ++k) {
