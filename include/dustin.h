@@ -460,7 +460,8 @@ int dustin_verify_tokens(int b, int w, int vocab, int dtype, const void* p_targe
  * Otherwise (DUSTIN_DEVFLAG_INDEX_ORDER) that sequence's rows are
  * unspecified.  Out of place, src and dst rows must not overlap, and an
  * index may repeat.  Rows of dst are distinct: a stride of 0 is refused, two
- * sequences' rows on one page are the caller's to avoid.  Limits: d in {64, 128}; k <= n in place. */
+ * sequences' rows on one page are the caller's to avoid.  Limits: d in {64,
+ * 128}; k <= n in place; k <= 2^30; b * h_kv * min(n_layers, 128) <= 2^24. */
 int dustin_kv_compact(int n_layers, int b, int h_kv, int d, int n, int k,
                       const dustin_kv* src, const dustin_kv* dst, const int32_t* idx,
                       const int32_t* k_len, void* stream);

@@ -965,8 +965,9 @@ int dustin_kv_compact(int n_layers, int b, int h_kv, int d, int n, int k,
     return fail(DUSTIN_ERR_INVALID_ARG, "%s: src, dst and idx are required", what);
   if ((reinterpret_cast<uintptr_t>(idx) | reinterpret_cast<uintptr_t>(k_len)) & 3u)
     return fail(DUSTIN_ERR_ALIGNMENT, "%s: idx and k_len need 4-byte alignment", what);
-  // Units of one launch, times the ranges a unit may be cut into.
-  if ((long long)b * h_kv * std::min(n_layers, kCompactMaxLayers) > (1LL << 24))
+  // Units of one launch, times the ranges a unit may be cut into; list entries
+  // are counted in 32 bits, beyond k by up to a chunk per range.
+  if ((long long)b * h_kv * std::min(n_layers, kCompactMaxLayers) > (1LL << 24) || k > (1 << 30))
     return fail(DUSTIN_ERR_SHAPE, "%s: problem too large", what);
   const bool in_place = src[0].k == dst[0].k && src[0].page_table == dst[0].page_table;
   if (in_place && k > n)

@@ -135,3 +135,11 @@ def test_refusals_of_shared_rows_and_sizes(lib):
     assert size((1 << 20) + 1, 1, 1, 1, 64, 1, 0, 16) == 0
     # 2^20 sequences of 128 rows: a place of 64 KB per part of one
     assert size(1 << 20, 1, 128, 1, 128, 1, 0, 16) == 0
+
+
+def test_compact_refuses_lists_past_its_32_bit_counts(lib):
+    src, dst = desc(), desc(base=FAKE + 0x1000000)
+    for k in ((1 << 30) + 1, 0x7fffffff):
+        assert lib.dustin_kv_compact(1, 2, 2, 128, 256, k, ctypes.byref(src), ctypes.byref(dst), FAKE,
+                                     None, None) == 2
+    assert "too large" in lib.dustin_last_error().decode()
