@@ -16,9 +16,10 @@
 //    of 16, four layers of 4 sequences and heads, 10.3 us (64 CTAs, the
 //    latency of four chunks).
 //  * kv_fork_kernel: one CTA per fork; table row copied, counts raised.
-//  * kv_resize_kernel: one cluster of 8 CTAs does the whole update of the
-//    table, the lengths and the reference counts (a few microseconds of
-//    latency, far from any bandwidth): each CTA derives the same plan from
+//  * kv_resize_kernel: one cluster of 8 CTAs (for small pools and lists one CTA
+//    of 256 threads) does the whole update of the table, the lengths and the
+//    reference counts (a few microseconds of latency, far from any bandwidth):
+//    each CTA derives the same plan from
 //    the list, releases its share of the dropped entries, and reads its
 //    slice of the reference counts into a bitmap of free pages; ranks in
 //    page order come from population counts, so the pages given out do not
@@ -192,7 +193,6 @@ struct ResizeShared {
   int have[kResizeMaxList];     // pages after
   int last[kResizeMaxList];     // last page to be copied (-1: none)
   int first[kResizeMaxList];    // rank of the entry's first free page
-  int newlen[kResizeMaxList];
   int scan[32];
   int free_here;                // read by the other CTAs of the cluster
   int total;
@@ -266,7 +266,6 @@ __global__ void __launch_bounds__(kResizeThreads) kv_resize_kernel(const ResizeA
   if (tid < a.n_list) {
     if (ok && sh.first_named[at] != tid) ok = false;
     if (!ok && rank == 0) raise_flag(DUSTIN_DEVFLAG_INDEX_RANGE);
-    sh.newlen[tid] = now;
     sh.had[tid] = ok ? (old + a.page_size - 1) / a.page_size : -1;
     sh.have[tid] = (now + a.page_size - 1) / a.page_size;
   }

@@ -17,7 +17,9 @@
 //    result does not depend on timing.
 //  * The CTA whose range holds u * total walks it again (one warp's share,
 //    1/(16 C) of the row, from L2) with a block scan of the same sums.
-// One launch, no workspace, no atomics but the error flag's.
+// One launch, no workspace, no atomics on device memory but the error flag's
+// (the walk's maximum and minimum of entry numbers are shared memory's, and do
+// not depend on their order).
 //
 // Bound by latency: the chain launch, draft's probabilities, row, cluster
 // barrier, second walk.  Measured (one call after the other): 16 rows of
