@@ -38,13 +38,13 @@
 // stream's softmax works, the tensor cores work for the other.
 #include <algorithm>
 #include <climits>
-#include <cuda.h>
 
 #include "device_common.cuh"
 #include "dustin.h"
 #include "internal.h"
 #include "quotient.h"
 #include "tcgen05.cuh"
+#include "tensor_map.h"
 
 namespace dustin {
 
@@ -1466,27 +1466,6 @@ __global__ void __launch_bounds__(kCombineThreads)
 }
 
 // ---- host side
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                   CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled() {
-  static std::atomic<EncodeTiledFn> fn{nullptr};
-  EncodeTiledFn f = fn.load(std::memory_order_acquire);
-  if (f) return f;
-  void* p = nullptr;
-  cudaDriverEntryPointQueryResult q;
-  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                       &q) == cudaSuccess &&
-      q == cudaDriverEntryPointSuccess && p) {
-    f = reinterpret_cast<EncodeTiledFn>(p);
-    fn.store(f, std::memory_order_release);
-  }
-  return f;
-}
 
 // [outer][h_kv][halves][rows][64] of one cache tensor, in boxes of `halves`
 // 64-column halves of box_rows rows.  An axis of stride 0 becomes an axis of

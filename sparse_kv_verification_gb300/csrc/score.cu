@@ -22,7 +22,6 @@
 // evict-last L2 policy and pass 2 drops each 128-byte line from L2 after
 // reading it, so they are read from L2 and never written back to DRAM
 // (72B-shaped step: target scoring 93.1 -> 89.0 us, draft 57.0 -> 56.3 us).
-#include <cuda.h>
 
 #include <algorithm>
 #include <atomic>
@@ -32,6 +31,7 @@
 #include "device_common.cuh"
 #include "dustin.h"
 #include "internal.h"
+#include "tensor_map.h"
 
 namespace dustin {
 
@@ -633,31 +633,6 @@ __global__ void __launch_bounds__(TmaCfg<D>::NT)
     }
     named_bar_sync(1, kWarps * 32);
   }
-}
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                   CUtensorMapFloatOOBfill);
-
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no link
-// against the driver library); null if unavailable.
-EncodeTiledFn encode_tiled() {
-  static std::atomic<EncodeTiledFn> fn{nullptr};
-  static std::atomic<int> tried{0};
-  EncodeTiledFn f = fn.load(std::memory_order_acquire);
-  if (f || tried.load()) return f;
-  void* p = nullptr;
-  cudaDriverEntryPointQueryResult q;
-  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                       cudaEnableDefault, &q) == cudaSuccess &&
-      q == cudaDriverEntryPointSuccess && p) {
-    f = reinterpret_cast<EncodeTiledFn>(p);
-    fn.store(f, std::memory_order_release);
-  }
-  tried.store(1);
-  return f;
 }
 
 // Tensor maps of every pair; false if one cannot be encoded (or, paged, if
