@@ -378,6 +378,10 @@ int dustin_full_verify_attn_window(int b, int h_q, int h_kv, int d, int w, int n
  * the window is finite.  Pages outside the pool are left out
  * (DUSTIN_DEVFLAG_PAGE_RANGE).  DUSTIN_ATTN_KV_READY is accepted, without
  * effect.  Sums are taken in a fixed order: equal calls give equal bits.
+ * Precision: scores, maxima, sums and partial results are fp32, but a weight is
+ * rounded to bf16 for its product with V (the sum it is divided by is of the
+ * unrounded ones), and o once more: o is off by up to 2^-8 (sum_j p_j |V_j| +
+ * |o|), element by element, beside fp32 rounding; lse by fp32 rounding alone.
  * Limits: as dustin_sparse_verify_attn; kv strides below 2^39 elements; b <=
  * 2^20; n_prefix, n_own <= 2^27; 2^23 products of 128 rows with 128 positions
  * in all; a workspace of 2^35 bytes.  Beyond them: DUSTIN_ERR_SHAPE.

@@ -1545,8 +1545,9 @@ PrefixKArgs shape_args(const PrefixArgs& p, int sms, Layout* lay) {
 // The split of prefixes of one length (Walk::search for those on the device):
 // the M, from the even share on, whose longest CTA is the shortest, the own
 // parts taking equal shares of the CTAs left.  Own parts whose lengths are on
-// the device count as 5/8 of the longest: batches of continuations lie between
-// a third of that and all of it.
+// the device count as 5/8 of the longest they may have: a guess a little above
+// lengths spread evenly (the measured batches).  Where most are nearly empty, or
+// all full, some CTAs end early.
 void host_split(PrefixKArgs& a, bool lengths_given, bool own_given) {
   a.split = a.np = a.ns = a.range = 0;
   const long long tp = (a.n[0] + kTile - 1) / kTile;

@@ -13,22 +13,21 @@
 //    within a chunk a barrier stands between the last load and the first
 //    store.  Measured: 2048 of 32768 positions of 16 sequences, four layers of
 //    8 heads, 167 us (1.07 GB moved, 6.4 TB/s); 512 of 8192 in place on pages
-//    of 16, four layers of 4 sequences and heads, 10.3 us (64 CTAs, the
+//    of 16, four layers of 4 sequences and heads, 10.4 us (64 CTAs, the
 //    latency of four chunks).
 //  * kv_fork_kernel: one CTA per fork; table row copied, counts raised.
 //  * kv_resize_kernel: one cluster of 8 CTAs (for small pools and lists one CTA
 //    of 256 threads) does the whole update of the table, the lengths and the
 //    reference counts (a few microseconds of latency, far from any bandwidth):
-//    each CTA derives the same plan from
-//    the list, releases its share of the dropped entries, and reads its
-//    slice of the reference counts into a bitmap of free pages; ranks in
-//    page order come from population counts, so the pages given out do not
-//    depend on timing.
+//    each CTA derives the same plan from the list, releases its share of the
+//    dropped entries, and reads its slice of the reference counts into a bitmap
+//    of free pages; ranks in page order come from population counts, so the
+//    pages given out do not depend on timing.
 //  * kv_copy_pages_kernel: the copies that growth into a shared page asks
 //    for, one CTA per (list entry, layer, K or V).
 // Measured, a turn of a serving loop (release, fork, grow with its copies): 64
 // samples of four prompts of 32749 positions on pages of 16, four layers of 8
-// heads, 35.7 us; four samples of one prompt of 2051 14.2.  Every launch is
+// heads, 36.2 us; four samples of one prompt of 2051 13.5.  Every launch is
 // bound by its latency: the pages' rows copied take 0.6 us of bandwidth.
 #include <algorithm>
 #include <cooperative_groups.h>
@@ -465,7 +464,8 @@ cudaError_t launch_resize(const ResizeArgs& a, cudaStream_t st) {
   // A small update runs in one CTA, whose barriers cost less than a cluster's.
   // Measured, 8 entries grown by a page and released: of 1024 pages 8.4 us in
   // one CTA, 9.3 in the cluster, of 4096 10.9 and 9.3; 32 entries of 1024 pages
-  // 10.5 and 9.7.
+  // 10.5 and 9.7.  Nothing between was measured: the border is the last point
+  // at which one CTA is known to win.
   const bool small = a.num_pages <= 1024 && a.n_list <= 16 && (long long)a.n_list * a.pages_per_seq <= 8192;
   const int C = small ? 1 : kResizeCluster;
   const int threads = small ? 256 : kResizeThreads;

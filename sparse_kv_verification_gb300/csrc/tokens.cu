@@ -23,9 +23,9 @@
 //
 // Bound by latency: the chain launch, draft's probabilities, row, cluster
 // barrier, second walk.  Measured (one call after the other): 16 rows of
-// 152064 in fp32, drafts rejected at random, 12.9 us (its 19.4 MB alone take
-// 2.9), 64 rows of 50257 in bf16 at odd alignments 14.0, one row of 32000
-// 8.1.  (Read element by element, the odd rows took 20.9.)
+// 152064 in fp32, drafts rejected at random, 13.7 us (its 19.4 MB alone take
+// 2.9), 64 rows of 50257 in bf16 at odd alignments 13.8, one row of 32000
+// 7.9.  (Read element by element, the odd rows took 20.9.)
 #include <algorithm>
 #include <cooperative_groups.h>
 
