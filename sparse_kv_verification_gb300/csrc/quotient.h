@@ -29,8 +29,8 @@ DUSTIN_HD int quotient(int x, int d) { return quotient(x, d, reciprocal(d)); }
 DUSTIN_HD int quotient_up(int x, int d, float inv) { return quotient(x + d - 1, d, inv); }
 DUSTIN_HD int quotient_up(int x, int d) { return quotient(x + d - 1, d); }
 
-// The same for quotients of any size, x < 2^30: the first estimate is off by at
-// most 3 x 2^-24 / d + 1, a remainder that is divided once more.
+// The same for quotients of any size, x < 2^30: the estimate is off by at most 3 x
+// 2^-24 of the quotient and one, so the rest that it leaves is divided once more.
 DUSTIN_HD int quotient_wide(int x, int d, float inv) {
   const int q = (int)((float)x * inv);
   int r = x - q * d;

@@ -17,9 +17,8 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
 // against the driver library); null if unavailable.
 inline EncodeTiledFn encode_tiled() {
   static std::atomic<EncodeTiledFn> fn{nullptr};
-  static std::atomic<int> tried{0};
   EncodeTiledFn f = fn.load(std::memory_order_acquire);
-  if (f || tried.load()) return f;
+  if (f) return f;
   void* p = nullptr;
   cudaDriverEntryPointQueryResult q;
   if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
@@ -28,7 +27,6 @@ inline EncodeTiledFn encode_tiled() {
     f = reinterpret_cast<EncodeTiledFn>(p);
     fn.store(f, std::memory_order_release);
   }
-  tried.store(1);
   return f;
 }
 
