@@ -517,6 +517,151 @@ int dustin_kv_resize(int n_seqs, int pages_per_seq, int page_size, int num_pages
                      int32_t* copies, int n_layers, int h_kv, int d,
                      const dustin_kv* kv, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A KV cache held in 4 bits: rows quantised as they are written, read back, and
+ * attended to.  Not an API of the paper.
+ *
+ * One record per (position, kv head), dustin_kv4_record_size(d) bytes (144 for
+ * d = 128, 80 for d = 64; bf16 takes 512 and 256), 16-byte aligned:
+ *   d/2 bytes of codes of K (channel 2i in the low, 2i+1 in the high half of
+ *   byte i), d/2 bytes of codes of V, d/16 scales of K (one per 16 channels),
+ *   d/16 scales of V, zeros.
+ * A value is e2m1(code) * e4m3(scale) * 2^exp, with k_exp for K and v_exp for V;
+ * e2m1 has the values 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign (bit 3), e4m3 finite ones
+ * up to 448, NaN (0x7f) and a sign that writing never sets.  All of it is exact in
+ * bf16.
+ *
+ * Contiguous layout (page_table == NULL): the record of (b, kv head h, position
+ * j) is at data + b*stride_b + h*stride_h + j*stride_n.  Paged: position j of
+ * sequence b in page p = page_table[b*pages_per_seq + j/page_size] at
+ * data + p*stride_b + h*stride_h + (j % page_size)*stride_n.  Strides are in BYTES,
+ * multiples of 16; k_exp and v_exp in [-64, 64].
+ */
+typedef struct dustin_kv4 {
+  const void* data;
+  int64_t stride_b;
+  int64_t stride_h;
+  int64_t stride_n;
+  const int32_t* page_table;
+  int32_t page_size;
+  int32_t pages_per_seq;
+  int32_t num_pages;
+  int32_t k_exp;
+  int32_t v_exp;
+} dustin_kv4;
+
+/* Bytes of a record; 0 for an unsupported d. */
+size_t dustin_kv4_record_size(int d);
+
+/* Writes rows into 4-bit caches: for every layer l, sequence b, kv head and
+ * t < w_len[b], row t of src[l] becomes position start[b] + t of dst[l].  Of each
+ * 16 channels x, with y = x * 2^-exp,
+ *   scale = e4m3(min(max |y| / 6, 448)),   code = e2m1(y / scale),
+ * both rounded to nearest, ties to even, beyond 6 to 6 (zeros keep their signs; a
+ * scale of 0 makes all 16 zeros).  So a value is off by up to half a step of its
+ * scale, |y| in (4, 6] by up to scale * 1, beyond that by what max |y| / scale
+ * exceeds 6 (1/16 of the maximum; more past 2688).  16 channels that hold a NaN or
+ * an infinity get the scale NaN: they read back as NaN.
+ *
+ *   src    host array [n_layers]: bf16 rows [b][h_kv][w][d], contiguous or paged
+ *   dst    host array [n_layers]: caches of n positions
+ *   start  int32 [b], device, or NULL (0 each)
+ *   w_len  int32 [b], device, or NULL (w each); clamped to [0, w]
+ * Positions outside [0, n) are left out (DUSTIN_DEVFLAG_INDEX_RANGE), and so are
+ * pages outside the pool (DUSTIN_DEVFLAG_PAGE_RANGE).  Records are distinct: a
+ * stride of 0 in dst is refused, two sequences' rows on one page are the caller's
+ * to avoid.  Limits: d in {64, 128}; b * h_kv * w <= 2^30. */
+int dustin_kv4_write(int n_layers, int b, int h_kv, int d, int n, int w,
+                     const dustin_kv* src, const dustin_kv4* dst,
+                     const int32_t* start, const int32_t* w_len, void* stream);
+
+/* Reads rows back as bf16: for every layer l, sequence b, kv head and i < k_len[b],
+ * row i of dst[l] becomes what position idx[b][i] (idx NULL: i) of src[l] stands
+ * for.  Exact.  Rows from k_len[b] on are left as they were.
+ *
+ *   src    host array [n_layers]: caches of n positions
+ *   dst    host array [n_layers]: bf16 rows [b][h_kv][k][d], contiguous or paged
+ *   idx    int32 [b][k], device, or NULL; entries outside [0, n) raise
+ *          DUSTIN_DEVFLAG_INDEX_RANGE, pages outside a pool
+ *          DUSTIN_DEVFLAG_PAGE_RANGE, and leave their row as it was
+ *   k_len  int32 [b], device, or NULL (k each); clamped to [0, k]
+ * Limits: d in {64, 128}; k <= n without idx; b * h_kv * k <= 2^30. */
+int dustin_kv4_read(int n_layers, int b, int h_kv, int d, int n, int k,
+                    const dustin_kv4* src, const dustin_kv* dst, const int32_t* idx,
+                    const int32_t* k_len, void* stream);
+
+/* Verification attention over a 4-bit cache:
+ *   o[b][h][t] = softmax over [positions idx[b][0..k_len[b]), window 0..t]
+ *                of scale * q . K, times V;   lse = log sum exp (natural)
+ * idx NULL takes positions 0 .. k_len[b] - 1 (the whole cache, or w = 1 rows of a
+ * decoding step); the window part, where win is given, is as in the *_window calls:
+ * bf16 [b][h_kv][w][d] through win->stride_b/h/n, positions 0..t only.  (A serving
+ * loop keeps the window in bf16 and writes the accepted rows to the cache.)
+ *
+ *   q      bf16 [b][h_q][w][d], device (contiguous); o like q; lse fp32 [b][h_q][w]
+ *   kv     one dustin_kv4 of n positions; ignored (may be NULL) if k is 0
+ *   idx    int32 [b][k], device, or NULL; in any order.  Entries outside [0, n) are
+ *          left out (DUSTIN_DEVFLAG_INDEX_RANGE), and pages outside the pool
+ *          (DUSTIN_DEVFLAG_PAGE_RANGE); an entry that repeats counts each time
+ *   k_len  int32 [b], device, or NULL (k each); clamped to [0, k]
+ * Records behind the lengths are never used, whatever they hold.  A row that sees
+ * no position, or only scores of -inf, gives o = 0, lse = -inf.  A row with a
+ * score that is NaN or +inf gives NaN, o and lse (scores beyond fp32 count as
+ * infinite).  DUSTIN_ATTN_KV_READY is accepted, without effect.  Sums are taken in a
+ * fixed order: equal calls give equal bits.
+ * Precision: cached values enter exactly, q as well (entries 2^-37 below their row's
+ * largest are rounded); scores, maxima, sums and partial results are fp32.  A
+ * weight of a cached position is rounded to f16 for its product with V (by 2^-11,
+ * or by 2^-33 of the row's largest weight so far), and o to bf16 once.
+ * Limits: as dustin_sparse_verify_attn; k <= n without idx; k <= 2^27; b <= 2^20;
+ * (b * h_kv * blocks of 64 query rows) * (k / 128 + 1) <= 2^30; a workspace of 2^35
+ * bytes.
+ * Workspace: dustin_kv4_verify_attn_workspace_size (with or without win, idx);
+ * its content need not be kept, and calls that may run at the same time (two
+ * streams, two captured graphs) have one each. */
+size_t dustin_kv4_verify_attn_workspace_size(int b, int h_q, int h_kv, int d, int w,
+                                             int k);
+int dustin_kv4_verify_attn(int b, int h_q, int h_kv, int d, int w, int n, int k,
+                           const void* q, const dustin_kv4* kv, const int32_t* idx,
+                           const int32_t* k_len, const dustin_kv* win, float scale,
+                           void* o, float* lse, void* ws, size_t ws_bytes,
+                           unsigned flags, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Log probabilities of given tokens, with the entropy of each row and its most
+ * likely tokens, from logits: what a serving loop reports beside the tokens that
+ * dustin_verify_tokens accepts, and scores a prompt with.  Not an API of the paper.
+ *
+ * With z = scale * logits[b][t] (scale: an inverse temperature):
+ *   lse[b][t]          = log sum_j exp(z_j)
+ *   logprobs[b][t][i]  = z[tokens[b][t][i]] - lse
+ *   entropy[b][t]      = -sum_j p_j log p_j,  p = softmax(z), 0 log 0 = 0
+ *   top_ids[b][t][0..top), top_logprobs: the largest logits in descending order,
+ *                        equal ones (-0 equals +0) by ascending id
+ * Logits of -inf have no mass (logprob -inf); they are alternatives where the
+ * others do not suffice.  A row of -inf alone has lse and all logprobs -inf and
+ * entropy 0.  A row with a NaN or +inf has lse, logprobs and entropy NaN; NaN logits
+ * are no alternatives (places left over: id -1, NaN).  A token outside
+ * [0, vocab) has logprob -inf and raises DUSTIN_DEVFLAG_INDEX_RANGE, but -1 (no
+ * token) raises nothing.
+ *
+ *   logits  [b][w][vocab] of `dtype` (DUSTIN_DTYPE_*), device; row (i, t) at element
+ *           i*stride_b + t*stride_w, entries contiguous
+ *   n_rows  int32 [b], device, or NULL (w each): rows t >= n_rows[b] are not read
+ *           and their outputs left as they were
+ *   tokens  int32 [b][w][m];  logprobs fp32 [b][w][m]  (may be NULL if m is 0)
+ *   entropy, lse  fp32 [b][w], or NULL
+ *   top_ids int32 [b][w][top];  top_logprobs fp32 [b][w][top]  (NULL if top is 0)
+ * Rows may start at any element; they are read in aligned words of 16 bytes, so
+ * bytes beside a row may be read too (never used).  Equal calls give equal bits.
+ * b == 0 or w == 0 is a no-op.  Limits: 1 <= vocab <= 2^30, b * w <= 2^27; m <= 512;
+ * top <= min(vocab, 64); 0 < scale <= 2^100.  No workspace. */
+int dustin_token_logprobs(int b, int w, int vocab, int dtype, const void* logits,
+                          int64_t stride_b, int64_t stride_w, float scale,
+                          const int32_t* n_rows, int m, const int32_t* tokens,
+                          float* logprobs, float* entropy, float* lse, int top,
+                          int32_t* top_ids, float* top_logprobs, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -23,7 +23,8 @@ LIB = os.path.join(BUILD, "libdustin.so")
 
 SOURCES = ["api.cu", "score.cu", "select.cu", "attn_sparse.cu", "attn_dense.cu",
            "attn_ml.cu", "quest.cu", "tokens.cu", "kv_pages.cu",
-           "attn_prefix.cu"]
+           "attn_prefix.cu", "kv4_cache.cu", "attn_kv4.cu", "attn_kv4_d64.cu",
+           "attn_kv4_d128.cu", "logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
          "-I" + INCLUDE, "-I" + CSRC]

@@ -518,6 +518,9 @@ int dustin_device_status(uint32_t* flags) {
       (e = take_prefix_flags(&f)) != cudaSuccess ||
       (e = take_tokens_flags(&f)) != cudaSuccess ||
       (e = take_pages_flags(&f)) != cudaSuccess ||
+      (e = take_kv4_flags(&f)) != cudaSuccess ||
+      (e = take_attn_kv4_flags(&f)) != cudaSuccess ||
+      (e = take_logprobs_flags(&f)) != cudaSuccess ||
       (e = take_score_flags(&f)) != cudaSuccess)
     return cuda_fail(e, "dustin_device_status");
   if (flags) *flags = f;
@@ -1105,6 +1108,243 @@ int dustin_kv_resize(int n_seqs, int pages_per_seq, int page_size, int num_pages
     if ((e = launch_copy_pages(c, n_list, d, (cudaStream_t)stream)) != cudaSuccess)
       return cuda_fail(e, what);
   }
+  return DUSTIN_OK;
+}
+
+size_t dustin_kv4_record_size(int d) {
+  return d == 64 ? 80 : d == 128 ? 144 : 0;
+}
+
+static Kv4View to_view4(const dustin_kv4& kv) {
+  Kv4View v;
+  v.data = static_cast<const uint8_t*>(kv.data);
+  v.sb = kv.stride_b;
+  v.sh = kv.stride_h;
+  v.sn = kv.stride_n;
+  v.page_table = kv.page_table;
+  v.page_size = kv.page_size;
+  v.pages_per_seq = kv.pages_per_seq;
+  v.num_pages = kv.num_pages;
+  v.k_exp = kv.k_exp;
+  v.v_exp = kv.v_exp;
+  return v;
+}
+
+// Checks a 4-bit cache of n positions.
+static int check_kv4(const dustin_kv4* kv, int n, int d, const char* what) {
+  if (!kv || !kv->data) return fail(DUSTIN_ERR_INVALID_ARG, "%s: a 4-bit cache is NULL", what);
+  if (!aligned16(kv->data))
+    return fail(DUSTIN_ERR_ALIGNMENT, "%s: 4-bit cache not 16-byte aligned", what);
+  if (kv->stride_b < 0 || kv->stride_h < 0 ||
+      kv->stride_n < (int64_t)dustin_kv4_record_size(d))
+    return fail(DUSTIN_ERR_SHAPE, "%s: bad strides of a 4-bit cache (%lld, %lld, %lld)", what,
+                (long long)kv->stride_b, (long long)kv->stride_h, (long long)kv->stride_n);
+  if (kv->stride_b % 16 || kv->stride_h % 16 || kv->stride_n % 16)
+    return fail(DUSTIN_ERR_ALIGNMENT, "%s: strides of a 4-bit cache must be multiples of 16 bytes",
+                what);
+  if (kv->k_exp < -64 || kv->k_exp > 64 || kv->v_exp < -64 || kv->v_exp > 64)
+    return fail(DUSTIN_ERR_SHAPE, "%s: exponents %d, %d (-64 .. 64)", what, kv->k_exp, kv->v_exp);
+  // What a descriptor of bf16 rows has to have, this one's pages have to, too.
+  dustin_kv pages{};
+  pages.k = kv->data;
+  pages.stride_n = d;
+  pages.page_table = kv->page_table;
+  pages.page_size = kv->page_size;
+  pages.pages_per_seq = kv->pages_per_seq;
+  pages.num_pages = kv->num_pages;
+  return check_kv(&pages, 1, n, d, false, what);
+}
+
+// Records (or bf16 rows) that lie on one another have no one content.
+static bool shares_rows(int64_t stride_b, int64_t stride_h, bool paged, int num_pages, int b,
+                        int h_kv) {
+  return (stride_h == 0 && h_kv > 1) || (stride_b == 0 && (paged ? num_pages : b) > 1);
+}
+
+// Shared by the two calls that go between bf16 rows and 4-bit caches.
+static int run_kv4(bool write, int n_layers, int b, int h_kv, int d, int n, int rows,
+                   const dustin_kv* kv, const dustin_kv4* kv4, const int32_t* start,
+                   const int32_t* idx, const int32_t* lens, void* stream, const char* what) {
+  if (n_layers < 0 || b < 0 || h_kv < 1 || n < 0 || rows < 0)
+    return fail(DUSTIN_ERR_SHAPE, "%s: n_layers=%d b=%d h_kv=%d n=%d rows=%d", what, n_layers, b,
+                h_kv, n, rows);
+  if (d != 64 && d != 128)
+    return fail(DUSTIN_ERR_UNSUPPORTED, "%s: d=%d (64 or 128)", what, d);
+  if (n_layers == 0 || b == 0 || rows == 0) return DUSTIN_OK;
+  if (!kv || !kv4) return fail(DUSTIN_ERR_INVALID_ARG, "%s: src and dst are required", what);
+  if ((reinterpret_cast<uintptr_t>(start) | reinterpret_cast<uintptr_t>(idx) |
+       reinterpret_cast<uintptr_t>(lens)) & 3u)
+    return fail(DUSTIN_ERR_ALIGNMENT, "%s: an array is not 4-byte aligned", what);
+  // Records are counted in 32 bits.
+  if ((double)b * h_kv * rows > (double)(1 << 30))
+    return fail(DUSTIN_ERR_SHAPE, "%s: problem too large", what);
+  if (!write && !idx && rows > n)
+    return fail(DUSTIN_ERR_SHAPE, "%s: k=%d > n=%d", what, rows, n);
+  for (int l = 0; l < n_layers; ++l) {
+    int rc = check_kv(&kv[l], b, rows, d, true, what);
+    if (rc || (rc = check_kv4(&kv4[l], n, d, what))) return rc;
+    if (write ? shares_rows(kv4[l].stride_b, kv4[l].stride_h, kv4[l].page_table, kv4[l].num_pages, b, h_kv)
+              : shares_rows(kv[l].stride_b, kv[l].stride_h, kv[l].page_table, kv[l].num_pages, b, h_kv))
+      return fail(DUSTIN_ERR_SHAPE, "%s: layer %d: rows of dst share storage", what, l);
+  }
+  Kv4Args a;
+  a.start = start;
+  a.idx = idx;
+  a.lens = lens;
+  a.hkv = h_kv;
+  a.n = n;
+  a.rows = rows;
+  a.count = (unsigned)((long long)b * h_kv * rows);
+  for (int l0 = 0; l0 < n_layers; l0 += kKv4MaxLayers) {
+    a.layers = std::min(kKv4MaxLayers, n_layers - l0);
+    for (int l = 0; l < a.layers; ++l) {
+      a.layer[l].rows = to_view(kv[l0 + l]);
+      a.layer[l].cache = to_view4(kv4[l0 + l]);
+    }
+    cudaError_t e = write ? launch_kv4_write(a, d, (cudaStream_t)stream)
+                          : launch_kv4_read(a, d, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, what);
+  }
+  return DUSTIN_OK;
+}
+
+int dustin_kv4_write(int n_layers, int b, int h_kv, int d, int n, int w, const dustin_kv* src,
+                     const dustin_kv4* dst, const int32_t* start, const int32_t* w_len,
+                     void* stream) {
+  return run_kv4(true, n_layers, b, h_kv, d, n, w, src, dst, start, nullptr, w_len, stream,
+                 "dustin_kv4_write");
+}
+
+int dustin_kv4_read(int n_layers, int b, int h_kv, int d, int n, int k, const dustin_kv4* src,
+                    const dustin_kv* dst, const int32_t* idx, const int32_t* k_len,
+                    void* stream) {
+  return run_kv4(false, n_layers, b, h_kv, d, n, k, dst, src, nullptr, idx, k_len, stream,
+                 "dustin_kv4_read");
+}
+
+static constexpr size_t kKv4WorkspaceMost = size_t(1) << 35;
+
+static int check_kv4_shape(int b, int h_q, int h_kv, int d, int w, int k, const char* what) {
+  int rc = check_attn_shape(b, h_q, h_kv, d, w, k, what);
+  if (rc) return rc;
+  // The line of tiles is counted in 32 bits.
+  const double units = (double)b * h_kv * (((double)(h_q / h_kv) * w + 63) / 64 + 1);
+  if (b > (1 << 20) || k > (1 << 27) || units * (k / 128 + 1.0) > (double)(1 << 30))
+    return fail(DUSTIN_ERR_SHAPE, "%s: problem too large", what);
+  return DUSTIN_OK;
+}
+
+static Kv4AttnArgs kv4_attn_args(int b, int h_q, int h_kv, int d, int w, int k) {
+  Kv4AttnArgs a{};
+  a.b = b;
+  a.hq = h_q;
+  a.hkv = h_kv;
+  a.d = d;
+  a.w = w;
+  a.k = k;
+  return a;
+}
+
+size_t dustin_kv4_verify_attn_workspace_size(int b, int h_q, int h_kv, int d, int w, int k) {
+  if (b <= 0 || check_kv4_shape(b, h_q, h_kv, d, w, k, "dustin_kv4_verify_attn_workspace_size"))
+    return 0;
+  const size_t need = attn_kv4_workspace(kv4_attn_args(b, h_q, h_kv, d, w, k), sm_count());
+  return need > kKv4WorkspaceMost ? 0 : need;
+}
+
+int dustin_kv4_verify_attn(int b, int h_q, int h_kv, int d, int w, int n, int k, const void* q,
+                           const dustin_kv4* kv, const int32_t* idx, const int32_t* k_len,
+                           const dustin_kv* win, float scale, void* o, float* lse, void* ws,
+                           size_t ws_bytes, unsigned flags, void* stream) {
+  const char* what = "dustin_kv4_verify_attn";
+  int rc = check_kv4_shape(b, h_q, h_kv, d, w, k, what);
+  if (rc) return rc;
+  if (n < 0 || (!idx && k > n))
+    return fail(DUSTIN_ERR_SHAPE, "%s: k=%d of n=%d positions", what, k, n);
+  if (b == 0) return DUSTIN_OK;
+  if (!q || !o || !lse)
+    return fail(DUSTIN_ERR_INVALID_ARG, "%s: q, o and lse are required", what);
+  if (!aligned16(q) || !aligned16(o) ||
+      ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(idx) |
+        reinterpret_cast<uintptr_t>(k_len)) & 3u))
+    return fail(DUSTIN_ERR_ALIGNMENT, "%s: q/o need 16-byte, lse, idx and k_len 4-byte alignment",
+                what);
+  if (!std::isfinite(scale) || !(scale > 0.f))
+    return fail(DUSTIN_ERR_INVALID_ARG, "%s: scale must be finite and > 0", what);
+  if (flags & ~DUSTIN_ATTN_KV_READY)
+    return fail(DUSTIN_ERR_INVALID_ARG, "%s: unknown flags 0x%x", what, flags);
+  if (k > 0 && (rc = check_kv4(kv, n, d, what))) return rc;
+  if (win && (rc = check_win(win, d, what))) return rc;
+  Kv4AttnArgs a = kv4_attn_args(b, h_q, h_kv, d, w, k);
+  const size_t need = attn_kv4_workspace(a, sm_count());
+  if (need > kKv4WorkspaceMost) return fail(DUSTIN_ERR_SHAPE, "%s: problem too large", what);
+  if (!ws || ws_bytes < need || !aligned16(ws))
+    return fail(DUSTIN_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu (16-byte aligned)", what,
+                ws_bytes, need);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  if (k > 0) a.kv = to_view4(*kv);
+  if (win) a.win = to_view(*win);
+  a.has_win = win ? 1 : 0;
+  a.idx = idx;
+  a.k_len = k_len;
+  a.n = n;
+  a.scale_log2 = scale * kLog2e;
+  cudaError_t e = launch_attn_kv4(a, sm_count(), ws, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  return DUSTIN_OK;
+}
+
+int dustin_token_logprobs(int b, int w, int vocab, int dtype, const void* logits,
+                          int64_t stride_b, int64_t stride_w, float scale, const int32_t* n_rows,
+                          int m, const int32_t* tokens, float* logprobs, float* entropy,
+                          float* lse, int top, int32_t* top_ids, float* top_logprobs,
+                          void* stream) {
+  const char* what = "dustin_token_logprobs";
+  if (b < 0 || w < 0 || vocab < 1 || vocab > (1 << 30) || (double)b * w > (double)(1 << 27))
+    return fail(DUSTIN_ERR_SHAPE, "%s: b=%d w=%d vocab=%d", what, b, w, vocab);
+  if (m < 0 || top < 0 || top > vocab)
+    return fail(DUSTIN_ERR_SHAPE, "%s: m=%d top=%d of %d", what, m, top, vocab);
+  if (m > kLogprobsMaxTokens || top > kLogprobsMaxTop)
+    return fail(DUSTIN_ERR_UNSUPPORTED, "%s: m=%d > %d or top=%d > %d", what, m,
+                kLogprobsMaxTokens, top, kLogprobsMaxTop);
+  if (dtype != DUSTIN_DTYPE_F32 && dtype != DUSTIN_DTYPE_BF16)
+    return fail(DUSTIN_ERR_INVALID_ARG, "%s: dtype=%d", what, dtype);
+  if (!(scale > 0.f && scale <= 0x1p100f))
+    return fail(DUSTIN_ERR_INVALID_ARG, "%s: scale must be > 0 and <= 2^100", what);
+  if (b == 0 || w == 0) return DUSTIN_OK;
+  if (!logits || (m > 0 && (!tokens || !logprobs)) || (top > 0 && (!top_ids || !top_logprobs)))
+    return fail(DUSTIN_ERR_INVALID_ARG,
+                "%s: logits and, with m or top, their arrays are required", what);
+  if (stride_b < 0 || stride_w < 0)
+    return fail(DUSTIN_ERR_SHAPE, "%s: negative stride", what);
+  const uintptr_t at = dtype == DUSTIN_DTYPE_F32 ? 3u : 1u;
+  if ((reinterpret_cast<uintptr_t>(logits) & at) ||
+      ((reinterpret_cast<uintptr_t>(n_rows) | reinterpret_cast<uintptr_t>(tokens) |
+        reinterpret_cast<uintptr_t>(logprobs) | reinterpret_cast<uintptr_t>(entropy) |
+        reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(top_ids) |
+        reinterpret_cast<uintptr_t>(top_logprobs)) & 3u))
+    return fail(DUSTIN_ERR_ALIGNMENT, "%s: an array is not aligned to its elements", what);
+  LogprobArgs a;
+  a.x = logits;
+  a.stride_b = stride_b;
+  a.stride_w = stride_w;
+  a.n_rows = n_rows;
+  a.tokens = tokens;
+  a.logprobs = logprobs;
+  a.entropy = entropy;
+  a.lse = lse;
+  a.top_ids = top_ids;
+  a.top_logprobs = top_logprobs;
+  a.b = b;
+  a.w = w;
+  a.vocab = vocab;
+  a.m = m;
+  a.top = top;
+  a.scale = scale;
+  cudaError_t e = launch_logprobs(a, dtype == DUSTIN_DTYPE_BF16, sm_count(), (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, what);
   return DUSTIN_OK;
 }
 

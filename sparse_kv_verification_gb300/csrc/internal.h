@@ -12,6 +12,15 @@ struct dustin_kv;
 
 namespace dustin {
 
+// Everything the kernels need of dustin_kv4 (strides in bytes).
+struct Kv4View {
+  const uint8_t* data;
+  long long sb, sh, sn;
+  const int* page_table;
+  int page_size, pages_per_seq, num_pages;
+  int k_exp, v_exp;
+};
+
 // ---- scoring
 constexpr int kMaxPairs = 64;
 
@@ -148,6 +157,55 @@ cudaError_t launch_fork(const ForkArgs& a, cudaStream_t st);
 cudaError_t launch_resize(const ResizeArgs& a, cudaStream_t st);
 cudaError_t launch_copy_pages(const CopyArgs& a, int n_list, int d, cudaStream_t st);
 cudaError_t take_pages_flags(unsigned* flags);
+
+// ---- a cache held in 4 bits
+constexpr int kKv4MaxLayers = 128;       // per launch (kernel parameter space)
+struct Kv4Args {
+  const int* start;    // [b] or null: position of row 0 (writing)
+  const int* idx;      // [b][rows] or null: position of each row (reading)
+  const int* lens;     // [b] or null: rows of each sequence
+  int layers, hkv, n, rows;
+  unsigned count;      // records per layer: b * hkv * rows
+  struct { KvView rows; Kv4View cache; } layer[kKv4MaxLayers];
+};
+cudaError_t launch_kv4_write(const Kv4Args& a, int d, cudaStream_t st);
+cudaError_t launch_kv4_read(const Kv4Args& a, int d, cudaStream_t st);
+cudaError_t take_kv4_flags(unsigned* flags);
+
+// ---- attention over a 4-bit cache
+struct Kv4AttnArgs {
+  const __nv_bfloat16* q;   // [b][h_q][w][d]
+  __nv_bfloat16* o;
+  float* lse;
+  Kv4View kv;
+  KvView win;
+  const int* idx;           // [b][k] or null
+  const int* k_len;         // [b] or null
+  int b, hq, hkv, d, w, n, k, has_win;
+  float scale_log2;
+};
+size_t attn_kv4_workspace(const Kv4AttnArgs& a, int sms);
+cudaError_t launch_attn_kv4(const Kv4AttnArgs& a, int sms, void* ws, cudaStream_t st);
+cudaError_t take_attn_kv4_flags(unsigned* flags);
+
+// ---- log probabilities
+constexpr int kLogprobsMaxTop = 64;
+constexpr int kLogprobsMaxTokens = 512;
+struct LogprobArgs {
+  const void* x;       // [b][w][vocab], fp32 or bf16
+  long long stride_b, stride_w;
+  const int* n_rows;   // [b] or null
+  const int* tokens;   // [b][w][m]
+  float* logprobs;     // [b][w][m]
+  float* entropy;      // [b][w] or null
+  float* lse;          // [b][w] or null
+  int* top_ids;        // [b][w][top]
+  float* top_logprobs;
+  int b, w, vocab, m, top;
+  float scale;
+};
+cudaError_t launch_logprobs(const LogprobArgs& a, bool bf16, int sms, cudaStream_t st);
+cudaError_t take_logprobs_flags(unsigned* flags);
 
 // ---- bookkeeping (api.cu)
 void note_launches(int count);

@@ -1,0 +1,370 @@
+// Log probabilities of given tokens, entropy and the most likely alternatives of
+// rows of logits.
+//
+// With M = max x_j, t_j = c (x_j - M), c = scale log2 e, and l = sum_j 2^t_j:
+//   lse = scale M + ln l,      logprob(j) = scale (x_j - M) - ln l,
+//   entropy = ln l - ln 2 / l sum_j 2^t_j t_j.
+// One pass: each thread keeps (m, l, s = sum 2^t t) over its entries; two parts
+// join at the larger m with
+//   l = l_1 + f l_2,  s = s_1 + f (s_2 + l_2 t),  t = c (m_2 - m_1), f = 2^t.
+// Differences x_j - m are formed before they are scaled, so that their rounding
+// goes by their own size and not by the logits', and halved, so that those of the
+// largest numbers stay finite.
+//
+// The alternatives are found in the same pass.  Of the first 16 words of each
+// warp's lanes the `top` largest lane maxima give a bound that `top` entries reach;
+// entries that reach it go to a list in shared memory, and where the list grows
+// past kRefine it is cut to its `top` best, the last of which is the next bound.
+// An entry that equals the bound counts if its index is lower, so ties go to the
+// lowest index and equal entries (a row of banned tokens at -inf) do not fill the
+// list.  Places come from counting better entries: no order of atomics shows.
+//
+// One cluster of C CTAs per row (C by the number of rows); rank 0 joins the parts
+// through distributed shared memory.  No workspace.  Bound by HBM for many
+// rows, by the latency of one load batch, three barriers and the cluster's for few.
+#include <algorithm>
+#include <climits>
+#include <cooperative_groups.h>
+
+#include "device_common.cuh"
+#include "dustin.h"
+#include "internal.h"
+
+namespace cg = cooperative_groups;
+
+namespace dustin {
+
+namespace {
+
+__device__ unsigned int g_logprobs_dev_flags;
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kWords = 4;                   // 16-byte words of a thread per batch
+constexpr int kTop = kLogprobsMaxTop;
+constexpr int kLists = (kTop + kWarps - 1) / kWarps;   // lane maxima a warp gives
+constexpr int kList = 1024;
+constexpr int kRefine = 192;                // entries that a list may keep between batches
+static_assert(kRefine + kThreads <= kList && kMaxCluster * kTop <= kList, "list");
+
+using Key = unsigned long long;             // larger: better
+
+// Order of values as unsigned numbers; -0 counts as +0.
+__device__ __forceinline__ unsigned order_of(float x) {
+  const unsigned u = __float_as_uint(x + 0.f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(unsigned o) {
+  return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ Key key_of(float x, int j) {
+  return (Key)order_of(x) << 32 | (unsigned)~j;
+}
+__device__ __forceinline__ int index_of(Key k) { return (int)~(unsigned)k; }
+
+struct Sums {
+  float m, l, s;
+};
+// c (x - m) from half, -m / 2, and c2, 2 c.
+__device__ __forceinline__ float exponent(float x, float half, float c2) {
+  return fmaf(x, 0.5f, half) * c2;
+}
+// 2^t times t where 2^t is 0: 0, though t be -inf.
+constexpr float kLeast = -1e30f;
+
+// l of a part without entries above -inf is 0, or NaN where it met one.
+__device__ __forceinline__ Sums join(const Sums& a, const Sums& b, float c2) {
+  Sums r;
+  r.m = fmaxf(a.m, b.m);
+  r.l = a.l + b.l;
+  r.s = 0.f;
+  if (r.m == -INFINITY) return r;
+  r.l = 0.f;
+  const Sums* part[2] = {&a, &b};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const Sums& p = *part[i];
+    if (p.m == -INFINITY) {
+      r.l += p.l;
+    } else {
+      const float t = fmaxf(exponent(p.m, -0.5f * r.m, c2), kLeast), f = ex2(t);
+      r.l = fmaf(f, p.l, r.l);
+      r.s = fmaf(f, fmaf(p.l, t, p.s), r.s);
+    }
+  }
+  return r;
+}
+
+struct Shared {
+  Key list[kList], best[kTop];
+  unsigned maxima[kWarps * kLists];
+  Sums part[kWarps], all;
+  Key bound;
+  int count, over, kept;
+};
+
+// The list's `top` best to sh.best in order, and back to the list's start.  All
+// threads; the list is complete and stays so.
+__device__ void refine(Shared& sh, int top) {
+  __syncthreads();
+  const int n = min(sh.count, kList);
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const Key mine = sh.list[i];
+    int better = 0;
+    for (int j = 0; j < n; ++j) better += sh.list[j] > mine;
+    if (better < top) sh.best[better] = mine;
+  }
+  __syncthreads();
+  const int kept = min(n, top);
+  if (threadIdx.x < kept) sh.list[threadIdx.x] = sh.best[threadIdx.x];
+  if (threadIdx.x == 0) {
+    sh.count = sh.kept = kept;
+    if (kept == top) sh.bound = sh.best[top - 1];
+  }
+  __syncthreads();
+}
+
+template <typename T>
+__device__ __forceinline__ float element(const uint4& w, int i) {
+  const uint32_t* u = &w.x;
+  if constexpr (sizeof(T) == 4) return __uint_as_float(u[i]);
+  return __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2)
+    logprobs_kernel(const __grid_constant__ LogprobArgs a) {
+  constexpr int V = 16 / sizeof(T);
+  __shared__ Shared sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
+  const int row = blockIdx.x / ranks, bb = row / a.w, t = row - bb * a.w;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float c2 = 2.f * a.scale * kLog2e;
+  const int top = a.top;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (a.n_rows && t >= __ldg(a.n_rows + bb)) return;   // the whole cluster
+  const T* x = static_cast<const T*>(a.x) + bb * a.stride_b + t * a.stride_w;
+  // The logit of a given token, fetched ahead.
+  int token = 0;
+  float given = -INFINITY;
+  if (rank == 0 && tid < a.m) {
+    token = __ldg(a.tokens + (long long)row * a.m + tid);
+    if (token >= 0 && token < a.vocab)
+      given = (float)x[token];
+    else if (token != -1)
+      atomicOr(&g_logprobs_dev_flags, DUSTIN_DEVFLAG_INDEX_RANGE);
+  }
+  if (tid == 0) {
+    sh.count = sh.over = sh.kept = 0;
+    sh.bound = 0;                                      // every entry but NaN is better
+  }
+  // Words of 16 bytes; entry i of word k is entry k V + i - lead of the row.
+  const int lead = (int)(reinterpret_cast<uintptr_t>(x) & 15u) / (int)sizeof(T);
+  const uint4* words = reinterpret_cast<const uint4*>(x - lead);
+  const long long all = ((long long)lead + a.vocab + V - 1) / V;
+  const int w0 = (int)(all * rank / ranks), w1 = (int)(all * (rank + 1) / ranks);
+  const int last = (int)all - 1;
+
+  Sums sum{-INFINITY, 0.f, 0.f};
+  uint4 next[kWords];
+  auto load = [&](int base) {
+#pragma unroll
+    for (int u = 0; u < kWords; ++u) {
+      const int k = base + u * kThreads + tid;
+      if (k < w1) next[u] = __ldg(words + k);
+    }
+  };
+  load(w0);
+  __syncthreads();
+  for (int base = w0; base < w1; base += kThreads * kWords) {
+    float v[kWords][V];
+    float most = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kWords; ++u) {
+      const int k = base + u * kThreads + tid;
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[u][i] = k < w1 ? element<T>(next[u], i) : -INFINITY;
+      if (k == 0 || k == last) {                       // entries beside the row
+        const long long j0 = (long long)k * V - lead;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (j0 + i < 0 || j0 + i >= a.vocab) v[u][i] = -INFINITY;
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) most = fmaxf(most, v[u][i]);
+    }
+    load(base + kThreads * kWords);
+    if (most > sum.m) {
+      const float t = fmaxf(exponent(sum.m, -0.5f * most, c2), kLeast), f = ex2(t);
+      sum.s = f * fmaf(sum.l, t, sum.s);
+      sum.l *= f;
+      sum.m = most;
+    }
+    const float half = sum.m == -INFINITY ? 0.f : -0.5f * sum.m;
+#pragma unroll
+    for (int u = 0; u < kWords; ++u)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float t = exponent(v[u][i], half, c2), e = ex2(t);
+        sum.l += e;
+        sum.s = fmaf(e, fmaxf(t, kLeast), sum.s);
+      }
+    if (top == 0) continue;
+
+    if (base == w0) {
+      // A first bound: the `top`-th of the warps' best lane maxima.
+      unsigned mine = order_of(most);
+      const int lists = (top + kWarps - 1) / kWarps;
+      for (int i = 0; i < lists; ++i) {
+        const unsigned best = __reduce_max_sync(0xffffffffu, mine);
+        if (lane == 0) sh.maxima[warp * lists + i] = best;
+        const unsigned has = __ballot_sync(0xffffffffu, mine == best);
+        if (lane == __ffs(has) - 1) mine = 0;
+      }
+      __syncthreads();
+      const int n = kWarps * lists;
+      if (tid < n) {
+        const unsigned x0 = sh.maxima[tid];
+        int better = 0;
+        for (int i = 0; i < n; ++i) better += sh.maxima[i] > x0 || (sh.maxima[i] == x0 && i < tid);
+        // Entries equal to it count, whatever their index; -inf bounds nothing
+        // (lanes without an entry have it, too).
+        if (better == top - 1 && value_of(x0) > -INFINITY) sh.bound = (Key)x0 << 32;
+      }
+      __syncthreads();
+    }
+    // Entries that reach the bound.  Those that do not fit are taken one word and
+    // entry at a time, the list cut in between.
+    Key bound = sh.bound;
+    float least = bound ? value_of((unsigned)(bound >> 32)) : -INFINITY;
+    const int before = sh.count;
+    auto entry = [&](int u, int i) -> Key {            // 0: none
+      const int k = base + u * kThreads + tid;
+      const long long j = (long long)k * V + i - lead;
+      const float xv = v[u][i];
+      if (!(xv >= least) || k >= w1 || j < 0 || j >= a.vocab) return 0;
+      const Key key = key_of(xv, (int)j);
+      return key > bound ? key : 0;
+    };
+    __syncthreads();                                   // all have read the count
+    if (most >= least) {
+#pragma unroll
+      for (int u = 0; u < kWords; ++u)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const Key key = entry(u, i);
+          if (key) {
+            const int at = atomicAdd(&sh.count, 1);
+            if (at < kList) sh.list[at] = key;
+          }
+        }
+    }
+    __syncthreads();
+    if (sh.count > kList) {
+      __syncthreads();
+      if (tid == 0) sh.count = before;                 // at most kRefine
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kWords; ++u)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const Key key = entry(u, i);
+          if (__syncthreads_or(key != 0)) {
+            if (key) sh.list[atomicAdd(&sh.count, 1)] = key;
+            refine(sh, top);
+            bound = sh.bound;
+            least = bound ? value_of((unsigned)(bound >> 32)) : -INFINITY;
+          }
+        }
+    } else if (sh.count > kRefine) {
+      refine(sh, top);
+    }
+  }
+  if (top > 0) refine(sh, top);
+
+  // Sums: lanes, warps, CTAs.
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    const Sums o{__shfl_xor_sync(0xffffffffu, sum.m, d), __shfl_xor_sync(0xffffffffu, sum.l, d),
+                 __shfl_xor_sync(0xffffffffu, sum.s, d)};
+    sum = lane & d ? join(o, sum, c2) : join(sum, o, c2);
+  }
+  if (lane == 0) sh.part[warp] = sum;
+  __syncthreads();
+  if (tid == 0) {
+    Sums r = sh.part[0];
+    for (int i = 1; i < kWarps; ++i) r = join(r, sh.part[i], c2);
+    sh.all = r;
+  }
+  if (ranks > 1) {
+    cluster.sync();
+    if (rank == 0) {
+      if (tid == 0) {
+        Sums r = sh.all;
+        for (int i = 1; i < ranks; ++i) r = join(r, *cluster.map_shared_rank(&sh.all, i), c2);
+        sh.all = r;
+      }
+      for (int i = tid; i < (ranks - 1) * top; i += kThreads) {
+        const Shared* of = cluster.map_shared_rank(&sh, 1 + i / top);
+        if (i % top < of->kept) sh.list[atomicAdd(&sh.count, 1)] = of->best[i % top];
+      }
+    }
+    cluster.sync();                                    // the others' parts are read
+    if (rank) return;
+    if (top > 0) refine(sh, top);
+  }
+  __syncthreads();
+  const Sums r = sh.all;
+  const bool none = r.m == -INFINITY && r.l == 0.f;    // only -inf
+  const float ln_l = none ? 0.f : logf(r.l);           // NaN where an entry is NaN or +inf
+  auto logprob = [&](float xv) {
+    return none ? -INFINITY : isnan(ln_l) ? ln_l : fmaf(xv, 0.5f, -0.5f * r.m) * (2.f * a.scale) - ln_l;
+  };
+  if (tid < a.m) a.logprobs[(long long)row * a.m + tid] = logprob(given);
+  if (tid < top) {
+    const bool have = tid < sh.kept;                   // NaN entries are no alternatives
+    const Key key = have ? sh.best[tid] : 0;
+    a.top_ids[(long long)row * top + tid] = have ? index_of(key) : -1;
+    a.top_logprobs[(long long)row * top + tid] =
+        have ? logprob(value_of((unsigned)(key >> 32))) : NAN;
+  }
+  if (tid == 0) {
+    if (a.entropy) a.entropy[row] = none ? 0.f : ln_l - kLn2 * r.s / r.l;
+    if (a.lse) a.lse[row] = none ? -INFINITY : isnan(ln_l) ? ln_l : fmaf(r.m, a.scale, ln_l);
+  }
+}
+
+template <typename T>
+cudaError_t run(const LogprobArgs& a, int sms, cudaStream_t st) {
+  // CTAs per row: twice the SMs in all, and a load batch of each CTA's at least
+  // one word per thread.
+  const long long rows = (long long)a.b * a.w;
+  const long long words = (a.vocab + 16 / sizeof(T) - 1) / (16 / sizeof(T));
+  int c = 1;
+  while (c < kMaxCluster && rows * c < 2 * sms && words > (long long)c * kThreads) c *= 2;
+  const dim3 grid((unsigned)(rows * c)), block(kThreads);
+  cudaError_t e = c == 1 ? launch_pdl(logprobs_kernel<T>, grid, block, 0, st, a)
+                         : launch_pdl_cluster(logprobs_kernel<T>, grid, block, 0, st, c, a);
+  if (e == cudaSuccess) note_launches(1);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_logprobs(const LogprobArgs& a, bool bf16, int sms, cudaStream_t st) {
+  return bf16 ? run<__nv_bfloat16>(a, sms, st) : run<float>(a, sms, st);
+}
+
+cudaError_t take_logprobs_flags(unsigned* flags) {
+  unsigned v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_logprobs_dev_flags, sizeof(v));
+  if (e != cudaSuccess) return e;
+  e = cudaMemcpyToSymbol(g_logprobs_dev_flags, &zero, sizeof(zero));
+  *flags |= v;
+  return e;
+}
+
+}  // namespace dustin

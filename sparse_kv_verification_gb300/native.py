@@ -38,6 +38,9 @@ EXPORTS = (
     "dustin_prefix_verify_attn_workspace_size", "dustin_prefix_verify_attn",
     "dustin_verify_tokens", "dustin_kv_compact", "dustin_kv_fork",
     "dustin_kv_resize",
+    "dustin_kv4_record_size", "dustin_kv4_write", "dustin_kv4_read",
+    "dustin_kv4_verify_attn_workspace_size", "dustin_kv4_verify_attn",
+    "dustin_token_logprobs",
 )
 
 
@@ -60,6 +63,23 @@ class DustinKV(ctypes.Structure):
         ("pages_per_seq", ctypes.c_int32),
         ("num_pages", ctypes.c_int32),
     ]
+
+
+class DustinKV4(ctypes.Structure):
+    """Mirror of ``dustin_kv4``; ``index`` is the device its cache lives on."""
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("stride_b", ctypes.c_int64),
+        ("stride_h", ctypes.c_int64),
+        ("stride_n", ctypes.c_int64),
+        ("page_table", ctypes.c_void_p),
+        ("page_size", ctypes.c_int32),
+        ("pages_per_seq", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("k_exp", ctypes.c_int32),
+        ("v_exp", ctypes.c_int32),
+    ]
+    index = -1
 
 
 _LIB: Optional[ctypes.CDLL] = None
@@ -122,6 +142,14 @@ def load(build_if_missing: bool = False, path: Optional[str] = None
         "dustin_kv_compact": (I, [I, I, I, I, I, I, P, P, P, P, P]),
         "dustin_kv_fork": (I, [I, I, I, I, I, P, P, P, P, P, P]),
         "dustin_kv_resize": (I, [I, I, I, I, I, P, P, P, P, P, P, I, I, I, P, P]),
+        "dustin_kv4_record_size": (S, [I]),
+        "dustin_kv4_write": (I, [I, I, I, I, I, I, P, P, P, P, P]),
+        "dustin_kv4_read": (I, [I, I, I, I, I, I, P, P, P, P, P]),
+        "dustin_kv4_verify_attn_workspace_size": (S, [I, I, I, I, I, I]),
+        "dustin_kv4_verify_attn": (I, [I, I, I, I, I, I, I, P, P, P, P, P, F, P, P, P, S,
+                                       U, P]),
+        "dustin_token_logprobs": (I, [I, I, I, I, P, L, L, F, P, I, P, P, P, P, I, P, P,
+                                      P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -742,3 +770,163 @@ def dustin_kv_resize(page_table: torch.Tensor, seq_len: torch.Tensor,
          seqs.data_ptr(), _ptr(new_len), page_table.data_ptr(), seq_len.data_ptr(),
          refcount.data_ptr(), copies.data_ptr(), len(kvs), h_kv, d,
          ctypes.addressof(arr) if kvs else None)
+
+
+# ------------------------------------------------------ a cache held in 4 bits
+
+def kv4_record_size(d: int) -> int:
+    """Bytes of one record: K and V of one position and kv head."""
+    return int(load().dustin_kv4_record_size(d))
+
+
+def kv4_desc(cache: torch.Tensor, page_table: Optional[torch.Tensor] = None,
+             k_exp: int = 0, v_exp: int = 0) -> DustinKV4:
+    """Describes a 4-bit cache.  Contiguous: cache uint8 [b][h_kv][n][record].
+    Paged: cache is a pool [pages][h_kv][page_size][record] and page_table is
+    int32 [b][pages_per_seq].  Values are code * scale * 2^k_exp (2^v_exp)."""
+    strides = cache.stride()
+    if cache.dtype != torch.uint8 or len(strides) != 4 or strides[3] != 1:
+        raise ValueError("a 4-bit cache must be a uint8 4-D tensor with a contiguous last dim")
+    table, page_size, pages_per_seq, num_pages = None, 0, 0, 0
+    index = _one_device(cache, page_table)
+    if page_table is not None:
+        rows = page_table.stride()
+        if page_table.dtype != torch.int32 or len(rows) != 2:
+            raise ValueError("page_table must be int32 [b][pages_per_seq]")
+        if rows[1] != 1:
+            raise ValueError("page_table rows must be contiguous")
+        num_pages, _, page_size, _ = cache.shape
+        table, pages_per_seq = page_table.data_ptr(), rows[0]
+    sb, sh, sn, _ = strides
+    kv = DustinKV4(cache.data_ptr(), sb, sh, sn, table, page_size, pages_per_seq, num_pages,
+                   k_exp, v_exp)
+    kv.index = index
+    return kv
+
+
+def _kv4_index(caches, *ts) -> int:
+    """The device of 4-bit caches and tensors that are used together."""
+    index = _one_device(*ts)
+    for kv in caches:
+        if index >= 0 and kv.index >= 0 and kv.index != index:
+            raise ValueError("tensors must live on one device")
+        index = max(index, kv.index)
+    return index
+
+
+def _kv4_arrays(kvs, caches):
+    if len(kvs) != len(caches):
+        raise ValueError("one src and one dst cache per layer")
+    return (DustinKV * len(kvs))(*kvs), (DustinKV4 * len(caches))(*caches)
+
+
+def dustin_kv4_write(src: Sequence[DustinKV], dst: Sequence[DustinKV4], b: int, h_kv: int,
+                     d: int, n: int, w: int, start: Optional[torch.Tensor] = None,
+                     w_len: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Rows t < w_len[b] of each layer's src (bf16 [b][h_kv][w][d]) become
+    positions start[b] + t of its 4-bit cache of n positions (start, w_len int32
+    [b]; None: 0 and w)."""
+    index = _kv4_index(dst, start, w_len)
+    for what, t in (("start", start), ("w_len", w_len)):
+        if t is not None:
+            _int32(what, t, b)
+    rows, caches = _kv4_arrays(src, dst)
+    if index < 0:
+        return                                           # no layers
+    _run(load().dustin_kv4_write, index, stream, len(src), b, h_kv, d, n, w,
+         ctypes.addressof(rows), ctypes.addressof(caches), _ptr(start), _ptr(w_len))
+
+
+def dustin_kv4_read(src: Sequence[DustinKV4], dst: Sequence[DustinKV], b: int, h_kv: int,
+                    d: int, n: int, k: int, idx: Optional[torch.Tensor] = None,
+                    k_len: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Row i < k_len[b] of each layer's dst (bf16 [b][h_kv][k][d]) becomes what
+    position idx[b][i] (idx int32 [b][k]; None: i) of its 4-bit cache of n
+    positions stands for."""
+    index = _kv4_index(src, idx, k_len)
+    if idx is not None:
+        _int32("idx", idx, b, k)
+    if k_len is not None:
+        _int32("k_len", k_len, b)
+    rows, caches = _kv4_arrays(dst, src)
+    if index < 0:
+        return                                           # no layers
+    _run(load().dustin_kv4_read, index, stream, len(src), b, h_kv, d, n, k,
+         ctypes.addressof(caches), ctypes.addressof(rows), _ptr(idx), _ptr(k_len))
+
+
+def dustin_kv4_verify_attn_workspace_size(b, h_q, h_kv, d, w, k) -> int:
+    return int(load().dustin_kv4_verify_attn_workspace_size(b, h_q, h_kv, d, w, k))
+
+
+def dustin_kv4_verify_attn(q: torch.Tensor, kv: Optional[DustinKV4], h_kv: int, n: int,
+                           k: int, scale: float, o: torch.Tensor, lse: torch.Tensor,
+                           ws: Optional[torch.Tensor], idx: Optional[torch.Tensor] = None,
+                           k_len: Optional[torch.Tensor] = None,
+                           win: Optional[DustinKV] = None, stream=None,
+                           flags: int = 0) -> None:
+    """Attention of q (bf16 [b][h_q][w][d]) over positions idx[b][:k_len[b]] (idx
+    int32 [b][k]; None: positions 0 .. k_len[b] - 1) of a 4-bit cache of n
+    positions and, with win, the window's bf16 causal block."""
+    index = _kv4_index(() if kv is None else (kv,), q, o, lse, ws, idx, k_len)
+    if q.dim() != 4 or q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("q must be contiguous bf16 [b][h_q][w][d]")
+    b, h_q, w, d = q.shape
+    if o.shape != q.shape or o.dtype != torch.bfloat16 or not o.is_contiguous():
+        raise ValueError("o must be contiguous bf16 shaped like q")
+    _float32("lse", lse, b, h_q, w)
+    if idx is not None:
+        _int32("idx", idx, b, k)
+    if k_len is not None:
+        _int32("k_len", k_len, b)
+    ref = lambda x: None if x is None else ctypes.byref(x)
+    _run(load().dustin_kv4_verify_attn, index, stream, b, h_q, h_kv, d, w, n, k,
+         q.data_ptr(), ref(kv), _ptr(idx), _ptr(k_len), ref(win), scale, o.data_ptr(),
+         lse.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+         flags)
+
+
+# ----------------------------------------------------------- log probabilities
+
+def dustin_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor],
+                          logprobs: Optional[torch.Tensor],
+                          entropy: Optional[torch.Tensor] = None,
+                          lse: Optional[torch.Tensor] = None,
+                          top_ids: Optional[torch.Tensor] = None,
+                          top_logprobs: Optional[torch.Tensor] = None, scale: float = 1.0,
+                          n_rows: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Of logits fp32 or bf16 [b][w][vocab] times scale: the log probabilities of
+    tokens (int32 [b][w][m], to logprobs fp32 alike; None: no tokens), the rows'
+    entropy and log-sum-exp (fp32 [b][w] or None), and the most likely tokens
+    (top_ids int32, top_logprobs fp32 [b][w][top], or None).  n_rows int32 [b]:
+    rows of each sequence (None: w); the others' outputs stay as they were."""
+    index = _one_device(logits, tokens, logprobs, entropy, lse, top_ids, top_logprobs, n_rows)
+    if logits.dim() != 3:
+        raise ValueError("logits must be [b][w][vocab]")
+    b, w, vocab = logits.shape
+    dtype = logits.dtype
+    if dtype != torch.float32 and dtype != torch.bfloat16:
+        raise ValueError("logits are fp32 or bf16")
+    sb, sw, row = logits.stride()
+    if row != 1 and vocab > 1:
+        raise ValueError("the vocabulary rows must be contiguous")
+    if (tokens is None) != (logprobs is None) or (top_ids is None) != (top_logprobs is None):
+        raise ValueError("tokens come with logprobs, top_ids with top_logprobs")
+    m = top = 0
+    if tokens is not None:
+        m = tokens.shape[-1]
+        _int32("tokens", tokens, b, w, m)
+        _float32("logprobs", logprobs, b, w, m)
+    if top_ids is not None:
+        top = top_ids.shape[-1]
+        _int32("top_ids", top_ids, b, w, top)
+        _float32("top_logprobs", top_logprobs, b, w, top)
+    for what, t in (("entropy", entropy), ("lse", lse)):
+        if t is not None:
+            _float32(what, t, b, w)
+    if n_rows is not None:
+        _int32("n_rows", n_rows, b)
+    _run(load().dustin_token_logprobs, index, stream, b, w, vocab,
+         DUSTIN_DTYPE_F32 if dtype == torch.float32 else DUSTIN_DTYPE_BF16, logits.data_ptr(),
+         sb, sw, scale, _ptr(n_rows), m, _ptr(tokens), _ptr(logprobs), _ptr(entropy),
+         _ptr(lse), top, _ptr(top_ids), _ptr(top_logprobs))
