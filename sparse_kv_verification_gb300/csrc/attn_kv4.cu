@@ -82,15 +82,16 @@ __global__ void __launch_bounds__(kJoinThreads) attn_kv4_join_kernel(const __gri
       const int g = min(a.grid, total);
       const int c0 = kv4_cta(first, total, g), c1 = kv4_cta(first + tiles - 1, total, g);
       const int slot0 = bb * hr + unit;
-      for (int i0 = c0 + turn; i0 <= c1; i0 += W * kInFlight) {
+      const int parts = 2 * (c1 - c0 + 1);       // two streams each
+      for (int i0 = turn; i0 < parts; i0 += W * kInFlight) {
         float2 ml[kInFlight];
         float v[kInFlight][E];
 #pragma unroll
         for (int i = 0; i < kInFlight; ++i) {
           const int at = i0 + i * W;
           ml[i] = make_float2(-INFINITY, 0.f);
-          if (at <= c1) {
-            const long long place = (long long)(slot0 + at) * a.rows + in;
+          if (at < parts) {
+            const long long place = ((long long)(slot0 + c0) * 2 + at) * a.rows + in;
             ml[i] = __ldcg(a.ws_ml + place);
             const float* from = a.ws_o + place * D + lane * E;
             if constexpr (E == 4) {
@@ -193,7 +194,7 @@ Kv4KArgs plan(const Kv4AttnArgs& p, int sms, Layout* lay) {
   a.rows = (a.gw + a.blocks - 1) / a.blocks;
   a.grid = sms;
   const size_t units = (size_t)p.b * p.hkv * a.blocks;
-  const size_t slots = p.k > 0 ? units + a.grid : 0;
+  const size_t slots = p.k > 0 ? 2 * (units + a.grid) : 0;
   lay->o = 0;
   lay->ml = align256(slots * a.rows * p.d * sizeof(float));
   lay->plan = lay->ml + align256(slots * a.rows * sizeof(float2));

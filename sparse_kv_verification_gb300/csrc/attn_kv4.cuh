@@ -23,12 +23,13 @@
 //
 // One persistent CTA per SM.  The tiles of all units (sequence, kv head, block of
 // rows) lie on a line that the CTAs share in equal ranges; a CTA's part of a unit
-// is a segment, whose O, m and l go to the workspace.  Roles of the 20 warps: 0
+// is a segment.  Its even and odd tiles are two streams, each with an m, l and O of
+// its own, so that one's chain (scores, softmax, weights, product) hides the
+// other's; the streams' O, m and l go to the workspace.  Roles of the 20 warps: 0
 // issues the products, 1 (and 3, where rows are gathered) loads records, 2 walks the
-// CTA's range and prepares Q, 4-7 take K to tensor memory (a thread has a
-// position), 8-11 V (a warp has 32 channels: bytes transposed by ldmatrix), 12-15
-// and 16-19 are the softmax of the first and the second half of the rows (a thread
-// has a position).
+// CTA's range and prepares Q; 4-7 and 8-11 take a stream's K and V to tensor memory
+// (K: a thread has a position; V: a warp has 32 channels, bytes transposed by
+// ldmatrix); 12-15 and 16-19 are a stream's softmax.
 #pragma once
 
 #include <cstddef>
@@ -48,8 +49,8 @@ struct Kv4KArgs {
   Kv4View kv;
   const int* idx;
   const int* k_len;
-  float* ws_o;         // [slot][rows][D], unnormalised, without 2^v_exp
-  float2* ws_ml;       // [slot][rows]: reference (log2 units), sum
+  float* ws_o;         // [slot][stream][rows][D], unnormalised, without 2^v_exp
+  float2* ws_ml;       // [slot][stream][rows]: reference (log2 units), sum
   int* plan;           // [b + 1]: where a sequence's tiles start on the line
   int b, hkv, gw, n, k;
   int blocks, rows;    // blocks of rows per kv head, rows of a block
@@ -73,6 +74,9 @@ __device__ __forceinline__ int kv4_cta(int tile, int total, int g) {
 }
 
 #ifdef DUSTIN_KV4_KERNEL
+#ifndef HINT
+#define HINT 0
+#endif
 
 namespace {
 
@@ -80,15 +84,33 @@ __device__ unsigned int g_kv4_attn_flags;
 
 constexpr int kTile = kKv4Tile;
 constexpr int kWarps = 20, kThreads = kWarps * 32;
-constexpr int kMmaWarp = 0, kLoadWarp = 1, kWalkWarp = 2, kLoadWarp2 = 3, kKWarp = 4, kVWarp = 8,
+constexpr int kMmaWarp = 0, kLoadWarp = 1, kWalkWarp = 2, kMmaWarp2 = 3, kCodeWarp = 4,
               kSoftmaxWarp = 12;
 constexpr int kSegRing = 4, kDeadRing = 32;
-// Tensor memory columns, two buffers of 64 each but O.
+// Tensor memory columns: each stream's S, K, V and O.
 constexpr int kColS = 0, kColK = 128, kColV = 256, kColO = 384;
+
+// Registers: a softmax thread holds a tile's scores; the other warps give up what
+// it needs beyond the launch's 96.
+struct Split {
+  static constexpr int OTHER = 56, CODE = 72, SOFTMAX = 136;
+  // In check_register_split's terms: all that give registers up as one warp.
+  static constexpr int NT = kThreads, NPW = 1, PRODUCER_REGS = 4 * OTHER + 8 * CODE;
+  static constexpr int NCW = 8, CONSUMER_REGS = SOFTMAX;
+  static_assert(PRODUCER_REGS + NCW * CONSUMER_REGS <= kWarps * 96, "the launch's registers");
+};
+template <int R>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(R) : "memory");
+}
+template <int R>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(R) : "memory");
+}
 
 // A reference is set this far below the largest score; weights stay below 2^15.
 constexpr float kBelow = 8.f;
-constexpr uint32_t kMostWeight = 0x7800;
+constexpr float kMostWeight = 15.f;   // log2
 
 template <int D>
 struct Cfg {
@@ -106,23 +128,22 @@ struct Seg {
 
 struct Control {
   unsigned long long full[12], empty[12];
-  unsigned long long k_full[2], v_full[2], s_full[2], s_empty[2], p_full[2], pv_done[2];
+  // Of a stream: K there and S free; V and P there; each product done.
+  unsigned long long qk_ready[2], pv_ready[2], s_full[2], pv_done[2];
   unsigned long long q_full[2], q_empty[2], seg_full[kSegRing], seg_empty[kSegRing];
-  unsigned long long dead_full[kDeadRing], meet[2], drain;
+  unsigned long long drain[2];
   Seg seg[kSegRing];
   alignas(16) unsigned dead[kDeadRing][4]; // positions of a tile that do not count
   float qs[2][kKv4Rows];                   // what S of a row is times, to log2 units
-  alignas(16) float4 row_of[8][16];        // per softmax warp: {qs, qs, -m, -m} of two rows
-  float exchange[2][2][4][32];            // used in turn: a meeting lies between
-  alignas(16) __half vscale[4][2][kTile];  // per V warp: scales of its two groups
-  int over[2][4];
-  int abort;
+  alignas(16) float exchange[2][2][4][kKv4Rows];   // used in turn: a vote lies between
+  float minus[2][kKv4Rows];                // -m of a stream's rows, at a segment's end
+  alignas(16) __half vscale[8][2][kTile];  // per code warp: V scales of its two groups
   uint32_t tmem;
 };
 
 // Read in pieces of 16 and 8 bytes.
-static_assert(offsetof(Control, dead) % 16 == 0 && offsetof(Control, row_of) % 16 == 0 &&
-                  offsetof(Control, vscale) % 16 == 0,
+static_assert(offsetof(Control, dead) % 16 == 0 && offsetof(Control, exchange) % 16 == 0 &&
+                  offsetof(Control, vscale) % 16 == 0 && offsetof(Control, qs) % 8 == 0,
               "alignment");
 static_assert(Cfg<64>::STAGE % 1024 == 0 && Cfg<128>::STAGE % 1024 == 0 && Rec<64>::SK % 8 == 0 &&
                   Rec<128>::SK % 8 == 0 && Rec<64>::V % 16 == 0 && Rec<128>::V % 16 == 0,
@@ -134,34 +155,38 @@ static_assert(kSmem<128> <= 232448 && kSmem<64> <= 232448, "shared memory of one
 
 __device__ __forceinline__ void raise_flag(unsigned f) { atomicOr(&g_kv4_attn_flags, f); }
 
-// try_wait that may keep the thread suspended for up to 100 us.
-__device__ __forceinline__ bool try_wait_long(uint32_t bar, uint32_t parity) {
+// Waits (a whole warp) for about a second at most: 2^25 tries of 50 cycles.  In as
+// few instructions as can be: a wait that is over takes 76 cycles so (with the clock
+// and other roles' troubles looked at between tries 115), and the warp that issues
+// the products takes every tile through its waits.
+__device__ __forceinline__ bool pwait(unsigned long long* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n"
-      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
+      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 0;\n"
+#if HINT
+      "L_%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n @p bra D_%=;\n"
+#else
+      "L_%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra D_%=;\n"
+#endif
+      " add.u32 n, n, 1;\n setp.lt.u32 q, n, 33554432;\n @q bra L_%=;\n"
+      "D_%=:\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(100000u)
+      : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
-  return ok != 0;
+  if (__all_sync(0xffffffffu, ok)) return true;
+  raise_flag(DUSTIN_DEVFLAG_WAIT_TIMEOUT);
+  return false;
 }
-// Waits with the library's limit; gives up when another role has.
-__device__ __forceinline__ bool pwait(unsigned long long* bar, uint32_t parity, int* abort) {
-  const uint32_t b = smem_u32(bar);
-  if (mbar_try_wait(b, parity)) return true;
-  const long long t0 = clock64();
-  while (!try_wait_long(b, parity)) {
-    if (*(volatile int*)abort || clock64() - t0 > kWaitLimitCycles) {
-      *(volatile int*)abort = 1;
-      raise_flag(DUSTIN_DEVFLAG_WAIT_TIMEOUT);
-      return false;
-    }
-  }
-  return true;
-}
-__device__ __forceinline__ bool pwait_warp(unsigned long long* bar, uint32_t parity, int* abort) {
-  return __all_sync(0xffffffffu, pwait(bar, parity, abort));
+// Whether any thread of a warpgroup says so (named barrier `id`).
+__device__ __forceinline__ bool vote(int id, bool says) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, %2, 128, q;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)says), "r"(id)
+      : "memory");
+  return r != 0;
 }
 
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
@@ -181,14 +206,14 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ float lo_of(uint64_t x) { return __uint_as_float((uint32_t)x); }
 __device__ __forceinline__ float hi_of(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float warp_max(float x) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -203,6 +228,13 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+// Four 8 x 8 matrices of f16: lane i has two entries of row i / 4 of each, and the
+// address of row i % 8 of matrix i / 8.
+__device__ __forceinline__ void stmatrix_x4(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(addr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
 }
 // Two 16 x 16 byte matrices, transposed: of the first (addresses of lanes 0-15)
 // lane i gets bytes (rows 4 (i % 4) ..+3, column i / 4) in r[0], column i / 4 + 8
@@ -289,12 +321,76 @@ struct Walk {
   }
 };
 
+// Segment `at` of the ring, once published; null: given up.
+__device__ __forceinline__ const Seg* segment(Control& sh, int at) {
+  if (!pwait(&sh.seg_full[at % kSegRing], (at / kSegRing) & 1)) return nullptr;
+  return &sh.seg[at % kSegRing];
+}
+// One arrival of a warp, after what all its lanes did.
+__device__ __forceinline__ void arrive(unsigned long long* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(bar));
+}
+
+// All of tensor memory is the CTA's: it starts at 0.
+constexpr uint32_t kTmem = 0;
+
+// The products of stream BUF: a tile's weights times V just before the next tile's
+// scores, or at the segment's end.  Everything asked for before scores that are there
+// is done.
+template <int D, int NC, int BUF>
+__device__ __forceinline__ void products(Control& sh, uint32_t p_buf, uint32_t q_buf) {
+  using C = Cfg<D>;
+  constexpr uint32_t kQk = mma_idesc_f16(128, NC, false), kPv = mma_idesc_f16(128, NC, true);
+  constexpr uint32_t tS = kTmem + kColS + BUF * 64, tK = kTmem + kColK + BUF * 64;
+  constexpr uint32_t tV = kTmem + kColV + BUF * 64, tO = kTmem + kColO + BUF * 64;
+  const uint32_t on = elect_one();
+  const uint64_t qd0 = smem_desc(q_buf, 16, 1024), pd = smem_desc(p_buf + BUF * C::P, 16, 1024);
+  bool ok = true;
+  int i = 0, done = 0;                     // tiles of the CTA; of the stream, scored
+  auto pv = [&](bool fresh) {
+    if (!pwait(&sh.pv_ready[BUF], (done - 1) & 1)) return false;
+    tc_fence_after();
+#pragma unroll
+    for (int k = 0; k < kTile / 16; ++k)
+      mma_ts(on, tO, tV + k * 8, pd + (k * 2048 >> 4), kPv, !fresh || k > 0);
+    mma_commit(on, smem_u32(&sh.pv_done[BUF]));
+    return true;
+  };
+  for (int at = 0; ok; ++at) {
+    const Seg* sp = segment(sh, at);
+    ok = sp != nullptr;
+    if (!ok || sp->slot < 0) break;
+    const int first = i + ((i ^ BUF) & 1), end = i + sp->n;   // the stream's tiles: first, + 2, ..
+    arrive(&sh.seg_empty[at % kSegRing]);
+    ok = pwait(&sh.q_full[at & 1], at >> 1 & 1);
+    const uint64_t qd = qd0 + ((at & 1) * C::Q >> 4);
+    for (int x = first; ok && x < end; x += 2) {
+      if (x > first && !(ok = pv(x == first + 2))) break;
+      ok = pwait(&sh.qk_ready[BUF], done & 1);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        mma_ts(on, tS, tK + k * 8, qd + (((k / 4) * (kKv4Rows * 128) + (k % 4) * 32) >> 4), kQk, k > 0);
+      mma_commit(on, smem_u32(&sh.s_full[BUF]));
+      ++done;
+    }
+    mma_commit(on, smem_u32(&sh.q_empty[at & 1]));     // also where the stream has none
+    if (ok && first < end) ok = pv(first + 2 >= end);
+    i = end;
+  }
+  // The products in flight end before tensor memory is freed.
+  mma_commit(on, smem_u32(&sh.drain[BUF]));
+  mbar_wait(smem_u32(&sh.drain[BUF]), 0, kWaitLimitCycles);
+  __syncwarp();
+}
+
 template <int D, int NC, bool GATHER>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_kv4_kernel(const __grid_constant__ Kv4KArgs a) {
   using C = Cfg<D>;
   using R = Rec<D>;
-  constexpr int N = NC / 2;                // rows of a softmax warp
   constexpr int STAGES = C::STAGES;
   extern __shared__ __align__(1024) unsigned char raw[];
   Control& sh = *reinterpret_cast<Control*>(raw + 2 * C::P + 2 * C::Q + STAGES * C::STAGE);
@@ -305,25 +401,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto init = [](unsigned long long* bar, int count, int n) {
       for (int i = 0; i < n; ++i) mbar_init(smem_u32(bar + i), count);
     };
-    constexpr int kLoaders = GATHER ? 2 : 1;
-    init(sh.full, GATHER ? 64 + 2 : 1, STAGES);
-    init(sh.empty, 8, STAGES);
-    init(sh.k_full, 4, 2);
-    init(sh.v_full, 4, 2);
+    init(sh.full, GATHER ? 32 + 1 : 1, STAGES);
+    init(sh.empty, 4, STAGES);
+    init(sh.qk_ready, 4 + 4, 2);
+    init(sh.pv_ready, 4 + 4, 2);
     init(sh.s_full, 1, 2);
-    init(sh.s_empty, 8, 2);
-    init(sh.p_full, 8, 2);
     init(sh.pv_done, 1, 2);
     init(sh.q_full, 1, 2);
-    init(sh.q_empty, 1 + 8, 2);
+    init(sh.q_empty, 2 + 8, 2);
     init(sh.seg_full, 1, kSegRing);
-    init(sh.seg_empty, kLoaders + 1 + 4 + 4 + 8, kSegRing);
-    init(sh.dead_full, kLoaders, kDeadRing);
-    init(sh.meet, 4, 2);
-    init(&sh.drain, 1, 1);
+    init(sh.seg_empty, 1 + 2 + 8 + 8, kSegRing);
+    init(sh.drain, 1, 2);
     mbar_fence_init();
-    sh.abort = 0;
-    for (int i = 0; i < 8; ++i) sh.over[i >> 2][i & 3] = 0;
   }
   if (warp == kMmaWarp) tmem_alloc<512>(smem_u32(&sh.tmem));
   tc_fence_before();
@@ -331,22 +420,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   griddep_wait();
   griddep_launch_dependents();
-  const uint32_t tmem = sh.tmem;
+  constexpr uint32_t tmem = kTmem;
   const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // tensor memory lane of the warp's first
 
-  // Segment `at` of the ring, once published; null: given up.
-  auto segment = [&](int at) -> const Seg* {
-    if (!pwait_warp(&sh.seg_full[at % kSegRing], (at / kSegRing) & 1, &sh.abort)) return nullptr;
-    return &sh.seg[at % kSegRing];
-  };
-  auto done_with = [&](int at) {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&sh.seg_empty[at % kSegRing]));
-  };
-  auto arrive = [&](unsigned long long* bar) {         // once per warp
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(bar));
-  };
+  auto done_with = [&](int at) { arrive(&sh.seg_empty[at % kSegRing]); };
+
+
+  // One instruction for a whole warpgroup; the others' stand in their roles, so
+  // that the compiler sees what each has.
+  if (warp < kCodeWarp) give_registers<Split::OTHER>();
 
   if (warp == kWalkWarp) {
     // ------------------------------------------------- the range, and its Q
@@ -354,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Seg s{};
     for (int at = 0;; ++at) {
       const bool more = walk.next(s);
-      if (!pwait_warp(&sh.seg_empty[at % kSegRing], (at / kSegRing & 1) ^ 1, &sh.abort)) break;
+      if (!pwait(&sh.seg_empty[at % kSegRing], (at / kSegRing & 1) ^ 1)) break;
       if (!more) s.slot = -1;
       if (lane == 0) {
         sh.seg[at % kSegRing] = s;
@@ -362,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!more) break;
       const int buf = at & 1;
-      if (!pwait_warp(&sh.q_empty[buf], (at >> 1 & 1) ^ 1, &sh.abort)) break;
+      if (!pwait(&sh.q_empty[buf], (at >> 1 & 1) ^ 1)) break;
       // A row's lanes scale it by the power of two that takes its largest finite
       // entry to [2^13, 2^14): f16 then has all 8 bits of entries down to 2^-30 of
       // that, and fewer to 2^-37.
@@ -413,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     const int runs = kTile / a.run;
     for (int at = 0; ok; ++at) {
-      const Seg* sp = segment(at);
+      const Seg* sp = segment(sh, at);
       ok = sp != nullptr;
       if (!ok || sp->slot < 0) break;
       const Seg s = *sp;
@@ -450,8 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (gone >> ((lane * 32 + k) / a.run) & 1) dead |= 1u << k;
           sh.dead[i % kDeadRing][lane] = dead;
         }
-        arrive(&sh.dead_full[i % kDeadRing]);
-        ok = pwait_warp(&sh.empty[st], (i / STAGES & 1) ^ 1, &sh.abort);
+        __syncwarp();
+        ok = pwait(&sh.empty[st], (i / STAGES & 1) ^ 1);
         if (!ok) break;
         const uint32_t bar = smem_u32(&sh.full[st]);
         if (lane == 0) {
@@ -470,131 +552,149 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok)
       for (int k = max(0, filled - STAGES); k < filled; ++k)
         mbar_wait(smem_u32(&sh.full[k % STAGES]), k / STAGES & 1, kWaitLimitCycles);
-  } else if ((warp == kLoadWarp || warp == kLoadWarp2) && GATHER) {
-    // ------------------------------------- records one by one, 64 of a tile
-    const int half = warp == kLoadWarp2;
+  } else if (warp == kLoadWarp && GATHER) {
+    // ------------------------------------------------- records one by one
     int i = 0;
     bool ok = true;
     for (int at = 0; ok; ++at) {
-      const Seg* sp = segment(at);
+      const Seg* sp = segment(sh, at);
       ok = sp != nullptr;
       if (!ok || sp->slot < 0) break;
       const Seg s = *sp;
       done_with(at);
       const int* idx = a.idx ? a.idx + (long long)s.bb * a.k : nullptr;
-      auto position = [&](int t, int u) -> int {       // -1: behind the end
-        const int j = t * kTile + half * 64 + u * 32 + lane;
-        if (j >= s.len || t >= s.t0 + s.n) return -1;
-        return idx ? __ldg(idx + j) : j;
+      // Lane's four positions of a tile, fetched a tile ahead; -1: behind the end.
+      int next[4];
+      auto fetch = [&](int t) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int j = t * kTile + u * 32 + lane;
+          next[u] = j >= s.len || t >= s.t0 + s.n ? -1 : idx ? __ldg(idx + j) : j;
+        }
       };
-      int at0 = position(s.t0, 0), at1 = position(s.t0, 1);
+      fetch(s.t0);
       for (int t = s.t0; t < s.t0 + s.n; ++t, ++i) {
         const int st = i % STAGES;
-        long long off[2];
+        long long off[4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int j = u ? at1 : at0;
-          const bool in = t * kTile + half * 64 + u * 32 + lane < s.len;
+        for (int u = 0; u < 4; ++u) {
+          const bool in = t * kTile + u * 32 + lane < s.len;
           off[u] = -1;
-          if (in && (j < 0 || j >= a.n)) {
+          if (in && (next[u] < 0 || next[u] >= a.n)) {
             raise_flag(DUSTIN_DEVFLAG_INDEX_RANGE);
           } else if (in) {
-            off[u] = place_of(a.kv, s.bb, s.h, j);
+            off[u] = place_of(a.kv, s.bb, s.h, next[u]);
             if (off[u] < 0) raise_flag(DUSTIN_DEVFLAG_PAGE_RANGE);
           }
           const unsigned dead = __ballot_sync(0xffffffffu, off[u] < 0);
-          if (lane == 0) sh.dead[i % kDeadRing][half * 2 + u] = dead;
+          if (lane == 0) sh.dead[i % kDeadRing][u] = dead;
         }
-        at0 = position(t + 1, 0);
-        at1 = position(t + 1, 1);
-        arrive(&sh.dead_full[i % kDeadRing]);
-        ok = pwait_warp(&sh.empty[st], (i / STAGES & 1) ^ 1, &sh.abort);
+        fetch(t + 1);
+        __syncwarp();
+        ok = pwait(&sh.empty[st], (i / STAGES & 1) ^ 1);
         if (!ok) break;
-        const uint32_t dst = ring + st * C::STAGE + half * 64 * R::BYTES;
+        const uint32_t dst = ring + st * C::STAGE;
         constexpr int P = R::PIECES;
 #pragma unroll
-        for (int x0 = 0; x0 < 64 * P; x0 += 32) {
-          const int x = x0 + lane, r = x / P, c = x - r * P;
-          const long long o0 = __shfl_sync(0xffffffffu, off[0], r & 31);
-          const long long o1 = __shfl_sync(0xffffffffu, off[1], r & 31);
-          const long long o = r < 32 ? o0 : o1;
-          cp_async_16(dst + x * 16, a.kv.data + max(o, 0LL) + c * 16, o < 0 ? 0 : 16);
-        }
-        const uint32_t bar = smem_u32(&sh.full[st]);
-        cp_async_mbar_arrive(bar);
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int x0 = 0; x0 < P; ++x0) {             // 32 records, a piece per lane
+            const int x = x0 * 32 + lane, r = x / P, c = x - r * P;
+            const long long o = __shfl_sync(0xffffffffu, off[u], r);
+            cp_async_16(dst + u * 32 * R::BYTES + x * 16, a.kv.data + max(o, 0LL) + c * 16, o < 0 ? 0 : 16);
+          }
+        cp_async_mbar_arrive(smem_u32(&sh.full[st]));
         arrive(&sh.full[st]);
       }
     }
     cp_async_wait<0>();
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------- products
-    // The whole warp walks, one lane issues.  A tile's scores are asked for
-    // before the product of the tile before, so that they are there when the
-    // softmax is done with that one.
-    constexpr uint32_t kQk = mma_idesc_f16(128, NC, false), kPv = mma_idesc_f16(128, NC, true);
-    const uint32_t on = elect_one();
-    const uint64_t qd = smem_desc(q_buf, 16, 1024), pd = smem_desc(p_buf, 16, 1024);
-    bool ok = true, first = false;         // of the tile whose product is still to come
+  } else if (warp == kMmaWarp || warp == kMmaWarp2) {
+    // ------------------------------------------------ a stream's products
+    // The whole warp walks, one lane issues.  A warp per stream: a tile takes it
+    // through two waits and 16 products, and one warp for both streams was what
+    // bounded all others.
+    if (warp == kMmaWarp)
+      products<D, NC, 0>(sh, p_buf, q_buf);
+    else
+      products<D, NC, 1>(sh, p_buf, q_buf);
+  } else if (warp >= kCodeWarp && warp < kSoftmaxWarp) {
+    // -------------------------------- a stream's K and V to tensor memory
+    give_registers<Split::CODE>();
+    const int buf = (warp - kCodeWarp) >> 2, q = warp & 3;
     int i = 0;
-    auto pv = [&](int x, bool fresh) {
-      const int buf = x & 1, phase = x >> 1 & 1;
-      if (!pwait_warp(&sh.v_full[buf], phase, &sh.abort) ||
-          !pwait_warp(&sh.p_full[buf], phase, &sh.abort))
-        return false;
-      tc_fence_after();
+    bool ok = true;
+    const uint32_t to_k = tmem + lanes + kColK + buf * 64, to_v = tmem + lanes + kColV + buf * 64;
+    const bool live = q * 32 < D;                      // the warp has channels
+    __half (&vscale)[2][kTile] = sh.vscale[warp - kCodeWarp];
+    const uint32_t scales = smem_u32(&vscale[0][0]) + (lane & 3) * 8;
+    // V of a tile comes before K of the stream's next: it is what the product in
+    // flight waits for.
+    auto value = [&](int x) {
+      const int st = x % STAGES;
+      const uint32_t from = ring + st * C::STAGE;
+      // The warp has 32 channels, two groups g.  A byte holds two channels, and a
+      // column of bytes has its lower halves in the first eight of 16 tensor memory
+      // lanes: channel c of a group goes to lane (c % 2) * 8 + c / 2.
+      if (live) {
+        // Scales in f16 by position; positions that do not count have 0, so that
+        // no NaN of memory never written meets their weight of 0.
 #pragma unroll
-      for (int k = 0; k < kTile / 16; ++k)
-        mma_ts(on, tmem + kColO, tmem + kColV + buf * 64 + k * 8,
-               pd + ((buf * C::P + k * 2048) >> 4), kPv, !fresh || k > 0);
-      mma_commit(on, smem_u32(&sh.pv_done[buf]));
+        for (int k = 0; k < 4; ++k) {
+          const int p = k * 32 + lane;
+          unsigned short two;
+          asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(two) : "r"(from + p * R::BYTES + R::SV + q * 2));
+          uint32_t s = e4m3x2_to_f16x2(two);
+          if (sh.dead[x % kDeadRing][k] >> lane & 1) s = 0;
+          vscale[0][p] = __ushort_as_half((unsigned short)s);
+          vscale[1][p] = __ushort_as_half((unsigned short)(s >> 16));
+        }
+      }
+      if (!pwait(&sh.pv_done[buf], (x >> 1 & 1) ^ 1)) return false;
+      tc_fence_after();
+      if (live) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {                  // 32 positions
+          uint32_t w[4];
+          ldmatrix_bytes_trans(from + (y * 32 + lane) * R::BYTES + R::V + q * 16, w);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            uint32_t o[8];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {              // 16 positions: lane's four
+              const uint32_t u = w[2 * z + g];
+              const uint2 s = lds64(scales + g * (kTile * 2) + (y * 32 + z * 16) * 2);
+              const uint32_t h0 = e2m1_to_f16x2<0>(u), h1 = e2m1_to_f16x2<1>(u);
+              const uint32_t h2 = e2m1_to_f16x2<2>(u), h3 = e2m1_to_f16x2<3>(u);
+              o[4 * z] = mul_f16x2(__byte_perm(h0, h1, 0x5410), s.x);
+              o[4 * z + 1] = mul_f16x2(__byte_perm(h2, h3, 0x5410), s.y);
+              o[4 * z + 2] = mul_f16x2(__byte_perm(h0, h1, 0x7632), s.x);
+              o[4 * z + 3] = mul_f16x2(__byte_perm(h2, h3, 0x7632), s.y);
+            }
+            tmem_st_16x16(to_v + ((uint32_t)g << 20) + y * 16, o);
+          }
+        }
+        tc_wait_st();
+      }
+      arrive(&sh.empty[st]);
+      tc_fence_before();
+      arrive(&sh.pv_ready[buf]);
       return true;
     };
     for (int at = 0; ok; ++at) {
-      const Seg* sp = segment(at);
-      ok = sp != nullptr;
-      if (!ok || sp->slot < 0) break;
-      const int n = sp->n, qbuf = at & 1;
-      done_with(at);
-      ok = pwait_warp(&sh.q_full[qbuf], at >> 1 & 1, &sh.abort);
-      for (int j = 0; ok && j < n; ++j, ++i) {
-        const int buf = i & 1, phase = i >> 1 & 1;
-        ok = pwait_warp(&sh.k_full[buf], phase, &sh.abort) &&
-             pwait_warp(&sh.s_empty[buf], phase ^ 1, &sh.abort);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ts(on, tmem + kColS + buf * 64, tmem + kColK + buf * 64 + k * 8,
-                 qd + ((qbuf * C::Q + (k / 4) * (kKv4Rows * 128) + (k % 4) * 32) >> 4), kQk, k > 0);
-        mma_commit(on, smem_u32(&sh.s_full[buf]));
-        if (j == n - 1) mma_commit(on, smem_u32(&sh.q_empty[qbuf]));
-        if (i > 0) ok = pv(i - 1, first);
-        first = j == 0;
-      }
-    }
-    if (ok && i > 0) ok = pv(i - 1, first);
-    // The products in flight end before tensor memory is freed.
-    mma_commit(on, smem_u32(&sh.drain));
-    mbar_wait(smem_u32(&sh.drain), 0, kWaitLimitCycles);
-    __syncwarp();
-  } else if (warp >= kKWarp && warp < kKWarp + 4) {
-    // ------------------------------------------------- K to tensor memory
-    int i = 0;
-    bool ok = true;
-    const uint32_t row = ring + ((warp & 3) * 32 + lane) * R::BYTES;
-    for (int at = 0; ok; ++at) {
-      const Seg* sp = segment(at);
+      const Seg* sp = segment(sh, at);
       if (!sp || sp->slot < 0) break;
-      const int n = sp->n;
+      const int first = i + ((i ^ buf) & 1), end = i + sp->n;
       done_with(at);
-      for (int j = 0; j < n; ++j, ++i) {
-        const int st = i % STAGES, buf = i & 1;
-        ok = pwait_warp(&sh.full[st], i / STAGES & 1, &sh.abort) &&
-             pwait_warp(&sh.s_full[buf], (i >> 1 & 1) ^ 1, &sh.abort);
+      for (int x = first; ok; x += 2) {
+        if (x > first && !(ok = value(x - 2))) break;
+        if (x >= end) break;
+        const int st = x % STAGES;
+        ok = pwait(&sh.full[st], x / STAGES & 1) && pwait(&sh.s_full[buf], (x >> 1 & 1) ^ 1);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t from = row + st * C::STAGE, to = tmem + lanes + kColK + buf * 64;
-        const uint2 sc = lds64(from + R::SK);          // D 64: the first word
+        // K: the thread has a position.
+        const uint32_t row = ring + st * C::STAGE + (q * 32 + lane) * R::BYTES;
+        const uint2 sc = lds64(row + R::SK);           // D 64: the first word
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {             // 64 channels, four scales
           const uint32_t four = c ? sc.y : sc.x;
@@ -603,306 +703,264 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  __byte_perm(s23, 0, 0x1010), __byte_perm(s23, 0, 0x3232)};
           uint32_t h[32];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint4 v = lds128(from + R::K + c * 32 + x * 16);
+          for (int y = 0; y < 2; ++y) {
+            const uint4 v = lds128(row + R::K + c * 32 + y * 16);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              uint32_t* o = h + x * 16 + y * 4;
-              const uint32_t by = s[x * 2 + y / 2];
-              o[0] = mul_f16x2(e2m1_to_f16x2<0>(w[y]), by);
-              o[1] = mul_f16x2(e2m1_to_f16x2<1>(w[y]), by);
-              o[2] = mul_f16x2(e2m1_to_f16x2<2>(w[y]), by);
-              o[3] = mul_f16x2(e2m1_to_f16x2<3>(w[y]), by);
+            for (int z = 0; z < 4; ++z) {
+              uint32_t* o = h + y * 16 + z * 4;
+              const uint32_t by = s[y * 2 + z / 2];
+              o[0] = mul_f16x2(e2m1_to_f16x2<0>(w[z]), by);
+              o[1] = mul_f16x2(e2m1_to_f16x2<1>(w[z]), by);
+              o[2] = mul_f16x2(e2m1_to_f16x2<2>(w[z]), by);
+              o[3] = mul_f16x2(e2m1_to_f16x2<3>(w[z]), by);
             }
           }
-          tmem_st32(to + c * 32, h);
+          tmem_st32(to_k + c * 32, h);
         }
-        arrive(&sh.empty[st]);
         tc_wait_st();
         tc_fence_before();
-        arrive(&sh.k_full[buf]);
+        arrive(&sh.qk_ready[buf]);
       }
-    }
-  } else if (warp >= kVWarp && warp < kVWarp + 4) {
-    // ------------------------------------------------- V to tensor memory
-    // Channel c of the warp's groups g = 0, 1 goes to its tensor memory lane
-    // 16 g + (c % 2) * 8 + c / 2: a byte holds two channels, and a column of bytes
-    // has its lower halves in the first eight lanes.
-    const int q = warp & 3;
-    const bool live = q * 32 < D;
-    int i = 0;
-    bool ok = true;
-    for (int at = 0; ok; ++at) {
-      const Seg* sp = segment(at);
-      if (!sp || sp->slot < 0) break;
-      const int n = sp->n;
-      done_with(at);
-      for (int j = 0; j < n; ++j, ++i) {
-        const int st = i % STAGES, buf = i & 1;
-        ok = pwait_warp(&sh.full[st], i / STAGES & 1, &sh.abort);
-        if (!ok) break;
-        const uint32_t from = ring + st * C::STAGE;
-        if (live) {
-          // Scales in f16 by position; positions that do not count have 0, so
-          // that no NaN of memory never written meets their weight of 0.
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int p = k * 32 + lane;
-            unsigned short two;
-            asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(two) : "r"(from + p * R::BYTES + R::SV + q * 2));
-            uint32_t s = e4m3x2_to_f16x2(two);
-            if (sh.dead[i % kDeadRing][k] >> lane & 1) s = 0;
-            sh.vscale[q][0][p] = __ushort_as_half((unsigned short)s);
-            sh.vscale[q][1][p] = __ushort_as_half((unsigned short)(s >> 16));
-          }
-        }
-        ok = pwait_warp(&sh.pv_done[buf], (i >> 1 & 1) ^ 1, &sh.abort);
-        if (!ok) break;
-        tc_fence_after();
-        __syncwarp();
-        if (live) {
-          const uint32_t to = tmem + lanes + kColV + buf * 64;
-          const uint32_t scales = smem_u32(&sh.vscale[q][0][0]) + (lane & 3) * 8;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {                // 32 positions
-            uint32_t w[4];
-            ldmatrix_bytes_trans(from + (x * 32 + lane) * R::BYTES + R::V + q * 16, w);
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              uint32_t o[8];
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {            // 16 positions: lane's four
-                const uint32_t u = w[2 * y + g];
-                const uint2 s = lds64(scales + g * (kTile * 2) + (x * 32 + y * 16) * 2);
-                const uint32_t h0 = e2m1_to_f16x2<0>(u), h1 = e2m1_to_f16x2<1>(u);
-                const uint32_t h2 = e2m1_to_f16x2<2>(u), h3 = e2m1_to_f16x2<3>(u);
-                o[4 * y] = mul_f16x2(__byte_perm(h0, h1, 0x5410), s.x);
-                o[4 * y + 1] = mul_f16x2(__byte_perm(h2, h3, 0x5410), s.y);
-                o[4 * y + 2] = mul_f16x2(__byte_perm(h0, h1, 0x7632), s.x);
-                o[4 * y + 3] = mul_f16x2(__byte_perm(h2, h3, 0x7632), s.y);
-              }
-              tmem_st_16x16(to + ((uint32_t)g << 20) + x * 16, o);
-            }
-          }
-          tc_wait_st();
-        }
-        arrive(&sh.empty[st]);
-        tc_fence_before();
-        arrive(&sh.v_full[buf]);
-      }
+      i = end;
     }
   } else if (warp >= kSoftmaxWarp) {
-    // -------------------------------------------------------------- softmax
-    const int wg = (warp - kSoftmaxWarp) >> 2, q = warp & 3, pos = q * 32 + lane;
-    const int col0 = wg * N;
-    float4* mine = sh.row_of[warp - kSoftmaxWarp];
-    const uint32_t row_of = smem_u32(mine);
-    const uint32_t tO = tmem + lanes + kColO + col0;
-    // The thread's place in P: rows col0 .. col0 + N - 1 of position pos.
-    const uint32_t p_row = p_buf + pos * 128;
-    int i = 0, votes = 0, turn = 0;
-    uint32_t meet_phase = 0;
-    bool ok = true;
-    auto meet = [&]() {                                // of the warpgroup
-      arrive(&sh.meet[wg]);
-      const bool r = pwait_warp(&sh.meet[wg], meet_phase, &sh.abort);
-      meet_phase ^= 1;
-      return r;
-    };
-    for (int at = 0; ok; ++at) {
-      const Seg* sp = segment(at);
-      if (!sp || sp->slot < 0) break;
+    // ------------------------------------------------ a stream's softmax
+    take_registers<Split::SOFTMAX>();
+    // A thread has 4 positions (8 k + lane / 4 of the warp's 32, k = 0 .. 3) and two
+    // rows of each 8 (2 (lane % 4), + 1): the rows' factors, references and sums are
+    // a quarter of what a position's whole line of rows would take, so that they
+    // stay in registers (read from shared memory for every tile they took 384 of its
+    // cycles), and the weights leave by stmatrix.
+    constexpr int G = NC / 8;                          // groups of 8 rows
+    const int buf = (warp - kSoftmaxWarp) >> 2, q = warp & 3;
+    const int bar = 1 + buf;                           // named barrier of the warpgroup
+    const uint32_t tS = tmem + lanes + kColS + buf * 64, tO = tmem + lanes + kColO + buf * 64;
+    const int pos = q * 32 + lane;                     // whose line of P the lane addresses
+    const uint32_t p_row = p_buf + buf * C::P + pos * 128;
+    const int col = 2 * (lane & 3);
+    int i = 0, turn = 0;
+    arrive(&sh.qk_ready[buf]);                         // S is free
+    for (int at = 0;; ++at) {
+      const Seg* sp = segment(sh, at);
+      bool ok = sp && (sp->slot < 0 || pwait(&sh.q_full[at & 1], at >> 1 & 1));
+      // A warp leaves where all of its warpgroup do: after a vote.  Every wait in
+      // between has its limit, so every warp gets there.
+      if (vote(bar, !ok) || sp->slot < 0) break;
       const int n = sp->n, rows = sp->rows, slot = sp->slot;
       done_with(at);
-      ok = pwait_warp(&sh.q_full[at & 1], at >> 1 & 1, &sh.abort);
-      if (!ok) break;
-      if (lane < N / 2) {
-        const float* qs = sh.qs[at & 1] + col0 + 2 * lane;
-        mine[lane] = make_float4(qs[0], qs[1], 0.f, 0.f);
+      uint64_t qs[G], minus[G], l[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const float2 f = *reinterpret_cast<const float2*>(&sh.qs[at & 1][8 * g + col]);
+        qs[g] = pack2(f.x, f.y);
+        minus[g] = l[g] = 0;
       }
       arrive(&sh.q_empty[at & 1]);
       bool fresh = true;                               // no reference yet
-      uint64_t l[N / 2];
-#pragma unroll
-      for (int c = 0; c < N / 2; ++c) l[c] = 0;
+      int last = -1;                                   // the stream's latest tile
       for (int j = 0; j < n; ++j, ++i) {
-        const int buf = i & 1, dr = i % kDeadRing;
-        ok = pwait_warp(&sh.dead_full[dr], i / kDeadRing & 1, &sh.abort) &&
-             pwait_warp(&sh.s_full[buf], i >> 1 & 1, &sh.abort);
-        if (!ok) break;
+        if ((i & 1) != buf) continue;
+        const int phase = i >> 1 & 1;
+        ok = ok && pwait(&sh.s_full[buf], phase);
         tc_fence_after();
-        const uint4 dead = lds128(smem_u32(sh.dead[dr]));
+        const uint4 dead = lds128(smem_u32(sh.dead[i % kDeadRing]));
+        uint64_t x[G][4];                              // two rows of position k
+        auto load = [&]() {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int g = 0; g < G; g += 2) {
+              uint32_t r[8];
+              tmem_ld_16x16(tS + ((uint32_t)h << 20) + g * 8, r);
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                x[g + y / 2][2 * h + y % 2] = pack2(__uint_as_float(r[2 * y]), __uint_as_float(r[2 * y + 1]));
+            }
+          tc_wait_ld();
+        };
+        load();
+        // x becomes the weights' exponents.
+        float most = -INFINITY;
         bool slow = fresh || (dead.x | dead.y | dead.z | dead.w);
-        const uint32_t tS = tmem + lanes + kColS + buf * 64 + col0;
-        uint32_t x[N], pk[N / 2];
-#pragma unroll
-        for (int c = 0; c < N; c += 8) tmem_ld8(tS + c, x + c);
-        tc_wait_ld();
         if (!slow) {
-          uint32_t most = 0;
 #pragma unroll
-          for (int c = 0; c < N / 2; ++c) {
-            const uint4 r = lds128(row_of + c * 16);
-            const uint64_t y = fma2(pack2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])),
-                                    pack2(__uint_as_float(r.x), __uint_as_float(r.y)),
-                                    pack2(__uint_as_float(r.z), __uint_as_float(r.w)));
-            const float e0 = ex2(lo_of(y)), e1 = ex2(hi_of(y));
-            x[2 * c] = __float_as_uint(e0);
-            x[2 * c + 1] = __float_as_uint(e1);
-            pk[c] = pack_f16(e0, e1);
-            most = __vmaxu2(most, pk[c]);
-          }
-          const bool over = (most & 0xffffu) >= kMostWeight || most >> 16 >= kMostWeight;
-          const int v = votes++ & 3;
-          if (__any_sync(0xffffffffu, over) && lane == 0) *(volatile int*)&sh.over[wg][v] = 1;
-          if (q == 0 && lane == 0) *(volatile int*)&sh.over[wg][(v + 2) & 3] = 0;
-          ok = meet();
-          if (!ok) break;
-          slow = *(volatile int*)&sh.over[wg][v] != 0;
+          for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              x[g][k] = fma2(x[g][k], qs[g], minus[g]);
+              most = max3(most, lo_of(x[g][k]), hi_of(x[g][k]));
+            }
         }
+        slow = vote(bar, slow || most > kMostWeight || !ok);
         if (slow) {
           // Masks, first tiles and references that move.
-          const unsigned word = q == 0 ? dead.x : q == 1 ? dead.y : q == 2 ? dead.z : dead.w;
-          const bool gone = word >> lane & 1;
-#pragma unroll
-          for (int c = 0; c < N; c += 8) tmem_ld8(tS + c, x + c);
-          tc_wait_ld();
-#pragma unroll
-          for (int c = 0; c < N; ++c) {
-            const float s = __fmul_rn(__uint_as_float(x[c]), (&mine[c / 2].x)[c & 1]);
-            x[c] = __float_as_uint(gone ? -INFINITY : s);
-            const float top = warp_max(__uint_as_float(x[c]));
-            if (lane == 0) sh.exchange[wg][turn][q][c] = top;
-          }
-          const float (&from)[4][32] = sh.exchange[wg][turn];
+          const unsigned word = (q == 0 ? dead.x : q == 1 ? dead.y : q == 2 ? dead.z : dead.w) >> (lane >> 2);
+          float (&to)[4][kKv4Rows] = sh.exchange[buf][turn];
           turn ^= 1;
-          ok = meet();
-          if (!ok) break;
-          // One lane per row: its reference.
-          float f = 1.f, minus = 0.f;
-          if (lane < N) {
-            const float top = fmaxf(fmaxf(from[0][lane], from[1][lane]),
-                                    fmaxf(from[2][lane], from[3][lane]));
-            const float old = (&mine[lane / 2].z)[lane & 1];
-            minus = old;
-            if (fresh) {
-              minus = top == -INFINITY ? 0.f : kBelow - top;
-            } else if (top + old > kBelow) {
-              minus = kBelow - top;
-              f = ex2(minus - old);
+          load();
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const bool gone = word >> (8 * k) & 1;
+              const float s0 = gone ? -INFINITY : __fmul_rn(lo_of(x[g][k]), lo_of(qs[g]));
+              const float s1 = gone ? -INFINITY : __fmul_rn(hi_of(x[g][k]), hi_of(qs[g]));
+              x[g][k] = pack2(s0, s1);
+              t0 = fmaxf(t0, s0);
+              t1 = fmaxf(t1, s1);
             }
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+              t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, d));
+              t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, d));
+            }
+            if (lane < 4) *reinterpret_cast<float2*>(&to[q][8 * g + col]) = make_float2(t0, t1);
           }
-          __syncwarp();
-          if (lane < N) (&mine[lane / 2].z)[lane & 1] = minus;
-          __syncwarp();
-          if (__any_sync(0xffffffffu, minus != minus || f != 1.f)) {
-            // O of the tiles before is scaled once their products are complete.
-            ok = pwait_warp(&sh.pv_done[(i - 1) & 1], (i - 1) >> 1 & 1, &sh.abort);
-            if (!ok) break;
-            tc_fence_after();
+          if (vote(bar, !ok)) {
+            ok = false;
+            break;
+          }
+          uint64_t f[G];
+          bool moves = false;
 #pragma unroll
-            for (int c = 0; c < N; c += 8) {
-              uint32_t o[8];
-              tmem_ld8(tO + c, o);
-              tc_wait_ld();
+          for (int g = 0; g < G; ++g) {
+            float top[2] = {-INFINITY, -INFINITY}, old[2] = {lo_of(minus[g]), hi_of(minus[g])};
 #pragma unroll
-              for (int y = 0; y < 8; y += 2) {
-                const float f0 = __shfl_sync(0xffffffffu, f, c + y);
-                const float f1 = __shfl_sync(0xffffffffu, f, c + y + 1);
-                o[y] = __float_as_uint(__uint_as_float(o[y]) * f0);
-                o[y + 1] = __float_as_uint(__uint_as_float(o[y + 1]) * f1);
-                l[(c + y) / 2] = pack2(lo_of(l[(c + y) / 2]) * f0, hi_of(l[(c + y) / 2]) * f1);
+            for (int w = 0; w < 4; ++w) {
+              const float2 t = *reinterpret_cast<const float2*>(&to[w][8 * g + col]);
+              top[0] = fmaxf(top[0], t.x);
+              top[1] = fmaxf(top[1], t.y);
+            }
+            float by[2] = {1.f, 1.f};
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              if (fresh) {
+                old[y] = top[y] == -INFINITY ? 0.f : kBelow - top[y];
+              } else if (top[y] + old[y] > kBelow) {
+                by[y] = ex2(kBelow - top[y] - old[y]);
+                old[y] = kBelow - top[y];
+                moves = true;
               }
-              tmem_st8(tO + c, o);
+            }
+            minus[g] = pack2(old[0], old[1]);
+            f[g] = pack2(by[0], by[1]);
+          }
+          if (__any_sync(0xffffffffu, moves)) {
+            // The products before these scores are complete.
+#pragma unroll
+            for (int g = 0; g < G; g += 2) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t o[8];
+                tmem_ld_16x16(tO + ((uint32_t)h << 20) + g * 8, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int y = 0; y < 8; ++y)
+                  o[y] = __float_as_uint(__uint_as_float(o[y]) * (y & 1 ? hi_of(f[g + y / 4]) : lo_of(f[g + y / 4])));
+                tmem_st_16x16(tO + ((uint32_t)h << 20) + g * 8, o);
+              }
+              l[g] = fma2(l[g], f[g], 0);
+              l[g + 1] = fma2(l[g + 1], f[g + 1], 0);
             }
             tc_wait_st();
           }
           // The scaled score rounded as the maximum was: a weight is at most
           // 2^8 here, whatever the size of the scores.
 #pragma unroll
-          for (int c = 0; c < N / 2; ++c) {
-            const float e0 = ex2(__uint_as_float(x[2 * c]) + mine[c].z);
-            const float e1 = ex2(__uint_as_float(x[2 * c + 1]) + mine[c].w);
-            x[2 * c] = __float_as_uint(e0);
-            x[2 * c + 1] = __float_as_uint(e1);
-            pk[c] = pack_f16(e0, e1);
-          }
+          for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[g][k] = add2(x[g][k], minus[g]);
           if ((dead.x & dead.y & dead.z & dead.w) != ~0u) fresh = false;
         }
         tc_fence_before();
-        arrive(&sh.s_empty[buf]);
+        arrive(&sh.qk_ready[buf]);
+        // P is free: the product with it was asked for before these scores.
 #pragma unroll
-        for (int c = 0; c < N / 2; ++c)
-          l[c] = add2(l[c], pack2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])));
-        ok = pwait_warp(&sh.pv_done[buf], (i >> 1 & 1) ^ 1, &sh.abort);
-        if (!ok) break;
+        for (int g = 0; g < G; ++g) {
+          uint32_t pk[4];
 #pragma unroll
-        for (int c = 0; c < N / 8; ++c)
-          sts128(p_row + buf * C::P + (((col0 / 8 + c) ^ (pos & 7)) << 4), pk[4 * c], pk[4 * c + 1],
-                 pk[4 * c + 2], pk[4 * c + 3]);
+          for (int k = 0; k < 4; ++k) {
+            const float e0 = ex2(lo_of(x[g][k])), e1 = ex2(hi_of(x[g][k]));
+            l[g] = add2(l[g], pack2(e0, e1));
+            pk[k] = pack_f16(e0, e1);
+          }
+          stmatrix_x4(p_row + ((g ^ (pos & 7)) << 4), pk);
+        }
         fence_proxy_async_smem();
         tc_fence_before();
-        arrive(&sh.p_full[buf]);
+        arrive(&sh.pv_ready[buf]);
+        last = i;
       }
-      if (!ok) break;
-      // The segment's sums over positions: lane c ends with row c's.
-      float v[32];
-#pragma unroll
-      for (int c = 0; c < 32; ++c) v[c] = c < N ? (c & 1 ? hi_of(l[(c % N) / 2]) : lo_of(l[(c % N) / 2])) : 0.f;
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1)
-#pragma unroll
-        for (int c = 0; c < d; ++c) {
-          const float give = lane & d ? v[c] : v[c + d], keep = lane & d ? v[c + d] : v[c];
-          v[c] = keep + __shfl_xor_sync(0xffffffffu, give, d);
-        }
-      const float (&from)[4][32] = sh.exchange[wg][turn];
-      sh.exchange[wg][turn][q][lane] = v[0];
+      // The rows' sums over positions.
+      float (&to)[4][kKv4Rows] = sh.exchange[buf][turn];
       turn ^= 1;
-      ok = meet();
-      if (!ok) break;
-      if (q == 0 && lane < N && col0 + lane < rows) {
-        a.ws_ml[(long long)slot * a.rows + col0 + lane] =
-            make_float2(-(&mine[lane / 2].z)[lane & 1],
-                        from[0][lane] + from[1][lane] + from[2][lane] + from[3][lane]);
-      }
-      ok = pwait_warp(&sh.pv_done[(i - 1) & 1], (i - 1) >> 1 & 1, &sh.abort);
-      if (!ok) break;
-      tc_fence_after();
-      const int channel = q * 32 + (lane >> 4) * 16 + (lane & 7) * 2 + (lane >> 3 & 1);
-      if (q * 32 < D) {
-        float* out = a.ws_o + ((long long)slot * a.rows + col0) * D + channel;
 #pragma unroll
-        for (int c = 0; c < N; c += 8) {
-          uint32_t o[8];
-          tmem_ld8(tO + c, o);
-          tc_wait_ld();
+      for (int g = 0; g < G; ++g) {
+        float s0 = lo_of(l[g]), s1 = hi_of(l[g]);
 #pragma unroll
-          for (int y = 0; y < 8; ++y)
-            if (col0 + c + y < rows) out[(c + y) * D] = __uint_as_float(o[y]);
+        for (int d = 4; d < 32; d <<= 1) {
+          s0 += __shfl_xor_sync(0xffffffffu, s0, d);
+          s1 += __shfl_xor_sync(0xffffffffu, s1, d);
         }
+        if (lane < 4) {
+          *reinterpret_cast<float2*>(&to[q][8 * g + col]) = make_float2(s0, s1);
+          if (q == 0) *reinterpret_cast<uint64_t*>(&sh.minus[buf][8 * g + col]) = minus[g];
+        }
+      }
+      if (ok && last >= 0) ok = pwait(&sh.pv_done[buf], last >> 1 & 1);
+      tc_fence_after();
+      if (vote(bar, !ok)) break;
+      const long long place = ((long long)slot * 2 + buf) * a.rows;
+      if (q < 2) {
+        const int c = q * 32 + lane;
+        if (c < rows)
+          a.ws_ml[place + c] = make_float2(-sh.minus[buf][c], to[0][c] + to[1][c] + to[2][c] + to[3][c]);
+      }
+      if (q * 32 < D && last >= 0) {
+        // Tensor memory lanes l and l + 8 have neighbouring channels.
+        float* out = a.ws_o + (place + col) * D + q * 32 + (lane >> 2) * 2;
+#pragma unroll
+        for (int g = 0; g < G; g += 2)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t o[8];
+            tmem_ld_16x16(tO + ((uint32_t)h << 20) + g * 8, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const int c = (g + y) * 8 + z;
+                if (c + col < rows)
+                  *reinterpret_cast<float2*>(out + c * D + h * 16) =
+                      make_float2(__uint_as_float(o[4 * y + z]), __uint_as_float(o[4 * y + 2 + z]));
+              }
+          }
       }
       tc_fence_before();
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) tmem_dealloc<512>(tmem);
+  if (warp == kMmaWarp) tmem_dealloc<512>(sh.tmem);
 }
 
 template <int D, int NC>
 cudaError_t run_kv4(const Kv4KArgs& k, bool gather, cudaStream_t st) {
-  auto go = [&](auto kern, std::atomic<uint64_t>& done) {
+  auto go = [&](auto kern, std::atomic<uint64_t>& done, std::atomic<int>& split_ok) {
     cudaError_t e = ensure_smem_attr(kern, kSmem<D>, done);
+    if (e == cudaSuccess) e = check_register_split<Split>(kern, split_ok);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3((unsigned)k.grid), dim3(kThreads), kSmem<D>, st, k);
     if (e == cudaSuccess) note_launches(1);
     return e;
   };
   static std::atomic<uint64_t> done[2];
-  return gather ? go(attn_kv4_kernel<D, NC, true>, done[1])
-                : go(attn_kv4_kernel<D, NC, false>, done[0]);
+  static std::atomic<int> split_ok[2];
+  return gather ? go(attn_kv4_kernel<D, NC, true>, done[1], split_ok[1])
+                : go(attn_kv4_kernel<D, NC, false>, done[0], split_ok[0]);
 }
 
 template <int D>
