@@ -74,30 +74,31 @@ __device__ __forceinline__ int kv4_cta(int tile, int total, int g) {
 }
 
 #ifdef DUSTIN_KV4_KERNEL
-#ifndef HINT
-#define HINT 0
-#endif
 
 namespace {
 
 __device__ unsigned int g_kv4_attn_flags;
 
 constexpr int kTile = kKv4Tile;
-constexpr int kWarps = 20, kThreads = kWarps * 32;
+constexpr int kWarps = 28, kThreads = kWarps * 32;
 constexpr int kMmaWarp = 0, kLoadWarp = 1, kWalkWarp = 2, kMmaWarp2 = 3, kCodeWarp = 4,
-              kSoftmaxWarp = 12;
+              kSoftmaxWarp = 20;
+// Where records are gathered, half of the warps that convert load them instead.
+constexpr int kGatherWarp = 4, kGatherWarps = 8;
 constexpr int kSegRing = 4, kDeadRing = 32;
 // Tensor memory columns: each stream's S, K, V and O.
 constexpr int kColS = 0, kColK = 128, kColV = 256, kColO = 384;
 
 // Registers: a softmax thread holds a tile's scores; the other warps give up what
-// it needs beyond the launch's 96.
+// it needs beyond the launch's 72.
+template <bool GATHER>
 struct Split {
-  static constexpr int OTHER = 56, CODE = 72, SOFTMAX = 136;
+  static constexpr int OTHER = 40, LOAD = 40, CODE = GATHER ? 56 : 48, SOFTMAX = 136;
   // In check_register_split's terms: all that give registers up as one warp.
-  static constexpr int NT = kThreads, NPW = 1, PRODUCER_REGS = 4 * OTHER + 8 * CODE;
+  static constexpr int NT = kThreads, NPW = 1;
+  static constexpr int PRODUCER_REGS = 4 * OTHER + (GATHER ? 8 * (LOAD + CODE) : 16 * CODE);
   static constexpr int NCW = 8, CONSUMER_REGS = SOFTMAX;
-  static_assert(PRODUCER_REGS + NCW * CONSUMER_REGS <= kWarps * 96, "the launch's registers");
+  static_assert(PRODUCER_REGS + NCW * CONSUMER_REGS <= kWarps * 72, "the launch's registers");
 };
 template <int R>
 __device__ __forceinline__ void give_registers() {
@@ -115,7 +116,7 @@ constexpr float kMostWeight = 15.f;   // log2
 template <int D>
 struct Cfg {
   static constexpr int STAGE = kTile * Rec<D>::BYTES;
-  static constexpr int STAGES = D == 128 ? 8 : 12;
+  static constexpr int PN = 2, STAGES = D == 128 ? 6 : 12;   // buffers of P per stream; tiles in flight
   static constexpr int P = kTile * 128;             // bytes: 64 rows of f16 per position
   static constexpr int Q = D / 64 * kKv4Rows * 128; // 64-channel halves behind one another
 };
@@ -150,12 +151,12 @@ static_assert(Cfg<64>::STAGE % 1024 == 0 && Cfg<128>::STAGE % 1024 == 0 && Rec<6
               "alignment");
 
 template <int D>
-constexpr int kSmem = 2 * Cfg<D>::P + 2 * Cfg<D>::Q + Cfg<D>::STAGES * Cfg<D>::STAGE + (int)sizeof(Control);
+constexpr int kSmem = 2 * Cfg<D>::PN * Cfg<D>::P + 2 * Cfg<D>::Q + Cfg<D>::STAGES * Cfg<D>::STAGE + (int)sizeof(Control);
 static_assert(kSmem<128> <= 232448 && kSmem<64> <= 232448, "shared memory of one CTA");
 
 __device__ __forceinline__ void raise_flag(unsigned f) { atomicOr(&g_kv4_attn_flags, f); }
 
-// Waits (a whole warp) for about a second at most: 2^25 tries of 50 cycles.  In as
+// Waits (a whole warp) for about a second at most: 2^23 times four tries of 50 cycles.  In as
 // few instructions as can be: a wait that is over takes 76 cycles so (with the clock
 // and other roles' troubles looked at between tries 115), and the warp that issues
 // the products takes every tile through its waits.
@@ -163,12 +164,11 @@ __device__ __forceinline__ bool pwait(unsigned long long* bar, uint32_t parity) 
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 0;\n"
-#if HINT
-      "L_%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n @p bra D_%=;\n"
-#else
       "L_%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra D_%=;\n"
-#endif
-      " add.u32 n, n, 1;\n setp.lt.u32 q, n, 33554432;\n @q bra L_%=;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra D_%=;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra D_%=;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra D_%=;\n"
+      " add.u32 n, n, 1;\n setp.lt.u32 q, n, 8388608;\n @q bra L_%=;\n"
       "D_%=:\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
@@ -335,9 +335,8 @@ __device__ __forceinline__ void arrive(unsigned long long* bar) {
 // All of tensor memory is the CTA's: it starts at 0.
 constexpr uint32_t kTmem = 0;
 
-// The products of stream BUF: a tile's weights times V just before the next tile's
-// scores, or at the segment's end.  Everything asked for before scores that are there
-// is done.
+// The products of stream BUF.  A tile's scores are asked for before the product of
+// the tile before, as soon as the softmax has read that one's.
 template <int D, int NC, int BUF>
 __device__ __forceinline__ void products(Control& sh, uint32_t p_buf, uint32_t q_buf) {
   using C = Cfg<D>;
@@ -345,11 +344,12 @@ __device__ __forceinline__ void products(Control& sh, uint32_t p_buf, uint32_t q
   constexpr uint32_t tS = kTmem + kColS + BUF * 64, tK = kTmem + kColK + BUF * 64;
   constexpr uint32_t tV = kTmem + kColV + BUF * 64, tO = kTmem + kColO + BUF * 64;
   const uint32_t on = elect_one();
-  const uint64_t qd0 = smem_desc(q_buf, 16, 1024), pd = smem_desc(p_buf + BUF * C::P, 16, 1024);
+  const uint64_t qd0 = smem_desc(q_buf, 16, 1024), pd0 = smem_desc(p_buf + BUF * C::PN * C::P, 16, 1024);
   bool ok = true;
-  int i = 0, done = 0;                     // tiles of the CTA; of the stream, scored
+  int i = 0, scored = 0, done = 0;         // tiles of the CTA, of the stream
   auto pv = [&](bool fresh) {
-    if (!pwait(&sh.pv_ready[BUF], (done - 1) & 1)) return false;
+    const uint64_t pd = pd0 + (done & (C::PN - 1)) * (C::P >> 4);
+    if (!pwait(&sh.pv_ready[BUF], done++ & 1)) return false;
     tc_fence_after();
 #pragma unroll
     for (int k = 0; k < kTile / 16; ++k)
@@ -366,15 +366,14 @@ __device__ __forceinline__ void products(Control& sh, uint32_t p_buf, uint32_t q
     ok = pwait(&sh.q_full[at & 1], at >> 1 & 1);
     const uint64_t qd = qd0 + ((at & 1) * C::Q >> 4);
     for (int x = first; ok && x < end; x += 2) {
-      if (x > first && !(ok = pv(x == first + 2))) break;
-      ok = pwait(&sh.qk_ready[BUF], done & 1);
+      ok = pwait(&sh.qk_ready[BUF], scored++ & 1);
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
         mma_ts(on, tS, tK + k * 8, qd + (((k / 4) * (kKv4Rows * 128) + (k % 4) * 32) >> 4), kQk, k > 0);
       mma_commit(on, smem_u32(&sh.s_full[BUF]));
-      ++done;
+      if (x > first) ok = pv(x == first + 2);
     }
     mma_commit(on, smem_u32(&sh.q_empty[at & 1]));     // also where the stream has none
     if (ok && first < end) ok = pv(first + 2 >= end);
@@ -393,24 +392,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   using R = Rec<D>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ __align__(1024) unsigned char raw[];
-  Control& sh = *reinterpret_cast<Control*>(raw + 2 * C::P + 2 * C::Q + STAGES * C::STAGE);
+  Control& sh = *reinterpret_cast<Control*>(raw + 2 * C::PN * C::P + 2 * C::Q + STAGES * C::STAGE);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t p_buf = smem_u32(raw), q_buf = p_buf + 2 * C::P, ring = q_buf + 2 * C::Q;
+  const uint32_t p_buf = smem_u32(raw), q_buf = p_buf + 2 * C::PN * C::P, ring = q_buf + 2 * C::Q;
 
   if (tid == 0) {
     auto init = [](unsigned long long* bar, int count, int n) {
       for (int i = 0; i < n; ++i) mbar_init(smem_u32(bar + i), count);
     };
-    init(sh.full, GATHER ? 32 + 1 : 1, STAGES);
-    init(sh.empty, 4, STAGES);
-    init(sh.qk_ready, 4 + 4, 2);
+    init(sh.full, GATHER ? 4 * (32 + 1) : 1, STAGES);
+    init(sh.empty, GATHER ? 4 : 8, STAGES);
+    init(sh.qk_ready, 4 + 1, 2);
     init(sh.pv_ready, 4 + 4, 2);
     init(sh.s_full, 1, 2);
     init(sh.pv_done, 1, 2);
     init(sh.q_full, 1, 2);
     init(sh.q_empty, 2 + 8, 2);
     init(sh.seg_full, 1, kSegRing);
-    init(sh.seg_empty, 1 + 2 + 8 + 8, kSegRing);
+    init(sh.seg_empty, GATHER ? kGatherWarps + 2 + 8 + 8 : 1 + 2 + 16 + 8, kSegRing);
     init(sh.drain, 1, 2);
     mbar_fence_init();
   }
@@ -428,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // One instruction for a whole warpgroup; the others' stand in their roles, so
   // that the compiler sees what each has.
-  if (warp < kCodeWarp) give_registers<Split::OTHER>();
+  if (warp < kCodeWarp) give_registers<Split<GATHER>::OTHER>();
 
   if (warp == kWalkWarp) {
     // ------------------------------------------------- the range, and its Q
@@ -552,60 +551,56 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok)
       for (int k = max(0, filled - STAGES); k < filled; ++k)
         mbar_wait(smem_u32(&sh.full[k % STAGES]), k / STAGES & 1, kWaitLimitCycles);
-  } else if (warp == kLoadWarp && GATHER) {
-    // ------------------------------------------------- records one by one
+  } else if (GATHER && warp >= kGatherWarp && warp < kGatherWarp + kGatherWarps) {
+    // ------------- records one by one: four warps a tile, 32 each, in turns
+    give_registers<Split<GATHER>::LOAD>();
+    const int turn = (warp - kGatherWarp) >> 2, quarter = (warp & 3) * 32;
     int i = 0;
     bool ok = true;
     for (int at = 0; ok; ++at) {
       const Seg* sp = segment(sh, at);
       ok = sp != nullptr;
       if (!ok || sp->slot < 0) break;
-      const Seg s = *sp;
+      const int bb = sp->bb, h = sp->h, len = sp->len, end = i + sp->n;
+      const int from = sp->t0 - i;                     // tile x of the CTA is tile x + from
       done_with(at);
-      const int* idx = a.idx ? a.idx + (long long)s.bb * a.k : nullptr;
-      // Lane's four positions of a tile, fetched a tile ahead; -1: behind the end.
-      int next[4];
-      auto fetch = [&](int t) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int j = t * kTile + u * 32 + lane;
-          next[u] = j >= s.len || t >= s.t0 + s.n ? -1 : idx ? __ldg(idx + j) : j;
-        }
+      const int* idx = a.idx ? a.idx + (long long)bb * a.k : nullptr;
+      // The lane's position of a tile, fetched one of its tiles ahead.
+      auto fetch = [&](int x) -> int {
+        const int j = (x + from) * kTile + quarter + lane;
+        return x >= end || j >= len ? 0 : idx ? __ldg(idx + j) : j;
       };
-      fetch(s.t0);
-      for (int t = s.t0; t < s.t0 + s.n; ++t, ++i) {
-        const int st = i % STAGES;
-        long long off[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const bool in = t * kTile + u * 32 + lane < s.len;
-          off[u] = -1;
-          if (in && (next[u] < 0 || next[u] >= a.n)) {
+      int x = i + ((i ^ turn) & 1);
+      int next = fetch(x);
+      for (; x < end; x += 2) {
+        const int st = x % STAGES, j = next;
+        long long off = -1;
+        if ((x + from) * kTile + quarter + lane < len) {
+          if (j < 0 || j >= a.n) {
             raise_flag(DUSTIN_DEVFLAG_INDEX_RANGE);
-          } else if (in) {
-            off[u] = place_of(a.kv, s.bb, s.h, next[u]);
-            if (off[u] < 0) raise_flag(DUSTIN_DEVFLAG_PAGE_RANGE);
+          } else {
+            off = place_of(a.kv, bb, h, j);
+            if (off < 0) raise_flag(DUSTIN_DEVFLAG_PAGE_RANGE);
           }
-          const unsigned dead = __ballot_sync(0xffffffffu, off[u] < 0);
-          if (lane == 0) sh.dead[i % kDeadRing][u] = dead;
         }
-        fetch(t + 1);
+        const unsigned dead = __ballot_sync(0xffffffffu, off < 0);
+        if (lane == 0) sh.dead[x % kDeadRing][warp & 3] = dead;
+        next = fetch(x + 2);
         __syncwarp();
-        ok = pwait(&sh.empty[st], (i / STAGES & 1) ^ 1);
+        ok = pwait(&sh.empty[st], (x / STAGES & 1) ^ 1);
         if (!ok) break;
-        const uint32_t dst = ring + st * C::STAGE;
+        const uint32_t dst = ring + st * C::STAGE + quarter * R::BYTES;
         constexpr int P = R::PIECES;
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int x0 = 0; x0 < P; ++x0) {             // 32 records, a piece per lane
-            const int x = x0 * 32 + lane, r = x / P, c = x - r * P;
-            const long long o = __shfl_sync(0xffffffffu, off[u], r);
-            cp_async_16(dst + u * 32 * R::BYTES + x * 16, a.kv.data + max(o, 0LL) + c * 16, o < 0 ? 0 : 16);
-          }
+        for (int y = 0; y < P; ++y) {                  // 32 records, a piece per lane
+          const int piece = y * 32 + lane, r = piece / P, c = piece - r * P;
+          const long long o = __shfl_sync(0xffffffffu, off, r);
+          cp_async_16(dst + piece * 16, a.kv.data + max(o, 0LL) + c * 16, o < 0 ? 0 : 16);
+        }
         cp_async_mbar_arrive(smem_u32(&sh.full[st]));
         arrive(&sh.full[st]);
       }
+      i = end;
     }
     cp_async_wait<0>();
   } else if (warp == kMmaWarp || warp == kMmaWarp2) {
@@ -618,115 +613,113 @@ __global__ void __launch_bounds__(kThreads, 1)
     else
       products<D, NC, 1>(sh, p_buf, q_buf);
   } else if (warp >= kCodeWarp && warp < kSoftmaxWarp) {
-    // -------------------------------- a stream's K and V to tensor memory
-    give_registers<Split::CODE>();
-    const int buf = (warp - kCodeWarp) >> 2, q = warp & 3;
+    // --------------------------- a stream's K, or its V, to tensor memory
+    give_registers<Split<GATHER>::CODE>();
+    // Two warpgroups per stream, one for K and one for V; where records are gathered
+    // one for both.
+    const int buf = GATHER ? (warp - kGatherWarp - kGatherWarps) >> 2 : (warp - kCodeWarp) >> 3;
+    const int q = warp & 3;
+    const bool key = GATHER || !(warp - kCodeWarp & 4), value = GATHER || !key;
     int i = 0;
     bool ok = true;
     const uint32_t to_k = tmem + lanes + kColK + buf * 64, to_v = tmem + lanes + kColV + buf * 64;
     const bool live = q * 32 < D;                      // the warp has channels
-    __half (&vscale)[2][kTile] = sh.vscale[warp - kCodeWarp];
+    __half (&vscale)[2][kTile] = sh.vscale[buf * 4 + q];
     const uint32_t scales = smem_u32(&vscale[0][0]) + (lane & 3) * 8;
-    // V of a tile comes before K of the stream's next: it is what the product in
-    // flight waits for.
-    auto value = [&](int x) {
-      const int st = x % STAGES;
-      const uint32_t from = ring + st * C::STAGE;
-      // The warp has 32 channels, two groups g.  A byte holds two channels, and a
-      // column of bytes has its lower halves in the first eight of 16 tensor memory
-      // lanes: channel c of a group goes to lane (c % 2) * 8 + c / 2.
-      if (live) {
-        // Scales in f16 by position; positions that do not count have 0, so that
-        // no NaN of memory never written meets their weight of 0.
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int p = k * 32 + lane;
-          unsigned short two;
-          asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(two) : "r"(from + p * R::BYTES + R::SV + q * 2));
-          uint32_t s = e4m3x2_to_f16x2(two);
-          if (sh.dead[x % kDeadRing][k] >> lane & 1) s = 0;
-          vscale[0][p] = __ushort_as_half((unsigned short)s);
-          vscale[1][p] = __ushort_as_half((unsigned short)(s >> 16));
-        }
-      }
-      if (!pwait(&sh.pv_done[buf], (x >> 1 & 1) ^ 1)) return false;
-      tc_fence_after();
-      if (live) {
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {                  // 32 positions
-          uint32_t w[4];
-          ldmatrix_bytes_trans(from + (y * 32 + lane) * R::BYTES + R::V + q * 16, w);
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            uint32_t o[8];
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {              // 16 positions: lane's four
-              const uint32_t u = w[2 * z + g];
-              const uint2 s = lds64(scales + g * (kTile * 2) + (y * 32 + z * 16) * 2);
-              const uint32_t h0 = e2m1_to_f16x2<0>(u), h1 = e2m1_to_f16x2<1>(u);
-              const uint32_t h2 = e2m1_to_f16x2<2>(u), h3 = e2m1_to_f16x2<3>(u);
-              o[4 * z] = mul_f16x2(__byte_perm(h0, h1, 0x5410), s.x);
-              o[4 * z + 1] = mul_f16x2(__byte_perm(h2, h3, 0x5410), s.y);
-              o[4 * z + 2] = mul_f16x2(__byte_perm(h0, h1, 0x7632), s.x);
-              o[4 * z + 3] = mul_f16x2(__byte_perm(h2, h3, 0x7632), s.y);
-            }
-            tmem_st_16x16(to_v + ((uint32_t)g << 20) + y * 16, o);
-          }
-        }
-        tc_wait_st();
-      }
-      arrive(&sh.empty[st]);
-      tc_fence_before();
-      arrive(&sh.pv_ready[buf]);
-      return true;
-    };
     for (int at = 0; ok; ++at) {
       const Seg* sp = segment(sh, at);
       if (!sp || sp->slot < 0) break;
-      const int first = i + ((i ^ buf) & 1), end = i + sp->n;
+      const int end = i + sp->n;
       done_with(at);
-      for (int x = first; ok; x += 2) {
-        if (x > first && !(ok = value(x - 2))) break;
-        if (x >= end) break;
-        const int st = x % STAGES;
-        ok = pwait(&sh.full[st], x / STAGES & 1) && pwait(&sh.s_full[buf], (x >> 1 & 1) ^ 1);
+      for (int x = i + ((i ^ buf) & 1); x < end; x += 2) {
+        const int st = x % STAGES, phase = (x >> 1 & 1) ^ 1;
+        const uint32_t from = ring + st * C::STAGE;
+        ok = pwait(&sh.full[st], x / STAGES & 1);
         if (!ok) break;
-        tc_fence_after();
-        // K: the thread has a position.
-        const uint32_t row = ring + st * C::STAGE + (q * 32 + lane) * R::BYTES;
-        const uint2 sc = lds64(row + R::SK);           // D 64: the first word
+        if (key) {
+          // K: the thread has a position.
+          ok = pwait(&sh.s_full[buf], phase);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t row = from + (q * 32 + lane) * R::BYTES;
+          const uint2 sc = lds64(row + R::SK);         // D 64: the first word
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {             // 64 channels, four scales
-          const uint32_t four = c ? sc.y : sc.x;
-          const uint32_t s01 = e4m3x2_to_f16x2(four), s23 = e4m3x2_to_f16x2(four >> 16);
-          const uint32_t s[4] = {__byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232),
-                                 __byte_perm(s23, 0, 0x1010), __byte_perm(s23, 0, 0x3232)};
-          uint32_t h[32];
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const uint4 v = lds128(row + R::K + c * 32 + y * 16);
+          for (int c = 0; c < D / 32; ++c) {           // 32 channels, two scales
+            const uint32_t s01 = e4m3x2_to_f16x2((c < 2 ? sc.x : sc.y) >> (c & 1) * 16);
+            const uint32_t s[2] = {__byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232)};
+            const uint4 v = lds128(row + R::K + c * 16);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t h[16];
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
-              uint32_t* o = h + y * 16 + z * 4;
-              const uint32_t by = s[y * 2 + z / 2];
-              o[0] = mul_f16x2(e2m1_to_f16x2<0>(w[z]), by);
-              o[1] = mul_f16x2(e2m1_to_f16x2<1>(w[z]), by);
-              o[2] = mul_f16x2(e2m1_to_f16x2<2>(w[z]), by);
-              o[3] = mul_f16x2(e2m1_to_f16x2<3>(w[z]), by);
+              h[4 * z] = mul_f16x2(e2m1_to_f16x2<0>(w[z]), s[z / 2]);
+              h[4 * z + 1] = mul_f16x2(e2m1_to_f16x2<1>(w[z]), s[z / 2]);
+              h[4 * z + 2] = mul_f16x2(e2m1_to_f16x2<2>(w[z]), s[z / 2]);
+              h[4 * z + 3] = mul_f16x2(e2m1_to_f16x2<3>(w[z]), s[z / 2]);
+            }
+            tmem_st16(to_k + c * 16, h);
+          }
+          if (!GATHER) arrive(&sh.empty[st]);
+          tc_wait_st();
+          tc_fence_before();
+          arrive(&sh.qk_ready[buf]);
+        }
+        if (value) {
+          // V: the warp has 32 channels, two groups g.  A byte holds two channels,
+          // and a column of bytes has its lower halves in the first eight of 16
+          // tensor memory lanes: channel c of a group goes to lane (c % 2) * 8 +
+          // c / 2.
+          if (live) {
+            // Scales in f16 by position; positions that do not count have 0, so
+            // that no NaN of memory never written meets their weight of 0.
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int p = k * 32 + lane;
+              unsigned short two;
+              asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(two) : "r"(from + p * R::BYTES + R::SV + q * 2));
+              uint32_t s = e4m3x2_to_f16x2(two);
+              if (sh.dead[x % kDeadRing][k] >> lane & 1) s = 0;
+              vscale[0][p] = __ushort_as_half((unsigned short)s);
+              vscale[1][p] = __ushort_as_half((unsigned short)(s >> 16));
             }
           }
-          tmem_st32(to_k + c * 32, h);
+          ok = pwait(&sh.pv_done[buf], phase);
+          if (!ok) break;
+          tc_fence_after();
+          if (live) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {              // 32 positions
+              uint32_t w[4];
+              ldmatrix_bytes_trans(from + (y * 32 + lane) * R::BYTES + R::V + q * 16, w);
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                uint32_t o[8];
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {          // 16 positions: lane's four
+                  const uint32_t u = w[2 * z + g];
+                  const uint2 s = lds64(scales + g * (kTile * 2) + (y * 32 + z * 16) * 2);
+                  const uint32_t h0 = e2m1_to_f16x2<0>(u), h1 = e2m1_to_f16x2<1>(u);
+                  const uint32_t h2 = e2m1_to_f16x2<2>(u), h3 = e2m1_to_f16x2<3>(u);
+                  o[4 * z] = mul_f16x2(__byte_perm(h0, h1, 0x5410), s.x);
+                  o[4 * z + 1] = mul_f16x2(__byte_perm(h2, h3, 0x5410), s.y);
+                  o[4 * z + 2] = mul_f16x2(__byte_perm(h0, h1, 0x7632), s.x);
+                  o[4 * z + 3] = mul_f16x2(__byte_perm(h2, h3, 0x7632), s.y);
+                }
+                tmem_st_16x16(to_v + ((uint32_t)g << 20) + y * 16, o);
+              }
+            }
+          }
+          arrive(&sh.empty[st]);
+          tc_wait_st();
+          tc_fence_before();
+          arrive(&sh.pv_ready[buf]);
         }
-        tc_wait_st();
-        tc_fence_before();
-        arrive(&sh.qk_ready[buf]);
       }
       i = end;
     }
   } else if (warp >= kSoftmaxWarp) {
     // ------------------------------------------------ a stream's softmax
-    take_registers<Split::SOFTMAX>();
+    take_registers<Split<GATHER>::SOFTMAX>();
     // A thread has 4 positions (8 k + lane / 4 of the warp's 32, k = 0 .. 3) and two
     // rows of each 8 (2 (lane % 4), + 1): the rows' factors, references and sums are
     // a quarter of what a position's whole line of rows would take, so that they
@@ -737,10 +730,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int bar = 1 + buf;                           // named barrier of the warpgroup
     const uint32_t tS = tmem + lanes + kColS + buf * 64, tO = tmem + lanes + kColO + buf * 64;
     const int pos = q * 32 + lane;                     // whose line of P the lane addresses
-    const uint32_t p_row = p_buf + buf * C::P + pos * 128;
+    const uint32_t p_row0 = p_buf + buf * C::PN * C::P + pos * 128;
     const int col = 2 * (lane & 3);
     int i = 0, turn = 0;
-    arrive(&sh.qk_ready[buf]);                         // S is free
+    if (q == 0) arrive(&sh.qk_ready[buf]);             // S is free
     for (int at = 0;; ++at) {
       const Seg* sp = segment(sh, at);
       bool ok = sp && (sp->slot < 0 || pwait(&sh.q_full[at & 1], at >> 1 & 1));
@@ -792,7 +785,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               most = max3(most, lo_of(x[g][k]), hi_of(x[g][k]));
             }
         }
+        tc_fence_before();
         slow = vote(bar, slow || most > kMostWeight || !ok);
+        tc_fence_after();
         if (slow) {
           // Masks, first tiles and references that move.
           const unsigned word = (q == 0 ? dead.x : q == 1 ? dead.y : q == 2 ? dead.z : dead.w) >> (lane >> 2);
@@ -818,10 +813,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (lane < 4) *reinterpret_cast<float2*>(&to[q][8 * g + col]) = make_float2(t0, t1);
           }
+          tc_fence_before();
           if (vote(bar, !ok)) {
             ok = false;
             break;
           }
+          tc_fence_after();
           uint64_t f[G];
           bool moves = false;
 #pragma unroll
@@ -848,7 +845,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             f[g] = pack2(by[0], by[1]);
           }
           if (__any_sync(0xffffffffu, moves)) {
-            // The products before these scores are complete.
+            // O of the tiles before is scaled once their products are complete.
+            ok = pwait(&sh.pv_done[buf], phase ^ 1);
+            tc_fence_after();
 #pragma unroll
             for (int g = 0; g < G; g += 2) {
 #pragma unroll
@@ -874,9 +873,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 4; ++k) x[g][k] = add2(x[g][k], minus[g]);
           if ((dead.x & dead.y & dead.z & dead.w) != ~0u) fresh = false;
         }
-        tc_fence_before();
-        arrive(&sh.qk_ready[buf]);
-        // P is free: the product with it was asked for before these scores.
+        // All have read S: they have voted since.
+        if (q == 0) {
+          tc_fence_before();
+          arrive(&sh.qk_ready[buf]);
+        }
+        // This P is free: the product two tiles back in the stream was asked for
+        // before these scores, and is done since they are.
+        const uint32_t p_row = p_row0 + (phase & (C::PN - 1)) * C::P;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           uint32_t pk[4];
@@ -949,9 +953,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D, int NC>
 cudaError_t run_kv4(const Kv4KArgs& k, bool gather, cudaStream_t st) {
-  auto go = [&](auto kern, std::atomic<uint64_t>& done, std::atomic<int>& split_ok) {
+  auto go = [&](auto kern, auto split, std::atomic<uint64_t>& done, std::atomic<int>& split_ok) {
+    using S = decltype(split);
     cudaError_t e = ensure_smem_attr(kern, kSmem<D>, done);
-    if (e == cudaSuccess) e = check_register_split<Split>(kern, split_ok);
+    if (e == cudaSuccess) e = check_register_split<S>(kern, split_ok);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3((unsigned)k.grid), dim3(kThreads), kSmem<D>, st, k);
     if (e == cudaSuccess) note_launches(1);
@@ -959,8 +964,8 @@ cudaError_t run_kv4(const Kv4KArgs& k, bool gather, cudaStream_t st) {
   };
   static std::atomic<uint64_t> done[2];
   static std::atomic<int> split_ok[2];
-  return gather ? go(attn_kv4_kernel<D, NC, true>, done[1], split_ok[1])
-                : go(attn_kv4_kernel<D, NC, false>, done[0], split_ok[0]);
+  return gather ? go(attn_kv4_kernel<D, NC, true>, Split<true>(), done[1], split_ok[1])
+                : go(attn_kv4_kernel<D, NC, false>, Split<false>(), done[0], split_ok[0]);
 }
 
 template <int D>
