@@ -17,7 +17,7 @@ namespace dustin {
 namespace {
 
 constexpr int kJoinThreads = 128;
-constexpr int kInFlight = 8;
+constexpr int kInFlight = 4;
 
 struct JoinArgs {
   Kv4KArgs k;
@@ -32,15 +32,20 @@ struct JoinArgs {
 template <int E>
 struct Part {
   float m = -INFINITY, l = 0.f, o[E] = {};
-  // Adds weight 2^by times (sum, v); by == -inf adds nothing, NaN makes it NaN.
+  // Before anything of weight 2^to is added.
   __device__ __forceinline__ void raise(float to) {
     if (to > m) {
       const float f = m == -INFINITY ? 0.f : ex2(m - to);
       m = to;
-      l = l == 0.f ? 0.f : l * f;
+      l = l == 0.f ? 0.f : l * f;            // NaN stays
 #pragma unroll
       for (int i = 0; i < E; ++i) o[i] = l == 0.f ? 0.f : o[i] * f;
     }
+  }
+  __device__ __forceinline__ void add(float weight, float sum, float by, const float (&v)[E]) {
+    l = fmaf(weight, sum, l);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = fmaf(weight * by, v[e], o[e]);
   }
 };
 
@@ -59,9 +64,12 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16* p, float (&x)[E]) 
     x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
 }
 
-// W warps to a row.
+// W warps to a row, the loads of kInFlight parts or window positions at a time.
+// Measured (72B-shaped, 5120 rows, cold): 22 us with eight parts in flight (126
+// registers, two waves) and the window's positions one after another.
 template <int D, int W>
-__global__ void __launch_bounds__(kJoinThreads) attn_kv4_join_kernel(const __grid_constant__ JoinArgs c) {
+__global__ void __launch_bounds__(kJoinThreads, 8)
+    attn_kv4_join_kernel(const __grid_constant__ JoinArgs c) {
   constexpr int E = D / 32;      // channels of a lane
   const Kv4KArgs& a = c.k;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, turn = warp % W;
@@ -74,6 +82,40 @@ __global__ void __launch_bounds__(kJoinThreads) attn_kv4_join_kernel(const __gri
   griddep_wait();
   griddep_launch_dependents();
   Part<E> part;
+  if (have && c.has_win) {
+    const int last = r % c.w;                    // window positions 0 .. last
+    float q[E];
+    load_row<E>(a.q + (long long)row * D + lane * E, q);
+    const long long at = (long long)bb * c.win.sb + (long long)h * c.win.sh + lane * E;
+    for (int t0 = turn; t0 <= last; t0 += W * kInFlight) {
+      float k[kInFlight][E], v[kInFlight][E], s[kInFlight];
+#pragma unroll
+      for (int i = 0; i < kInFlight; ++i) {
+        const int t = min(t0 + i * W, last);     // those past the end are not added
+        load_row<E>(c.win.k + at + t * c.win.sn, k[i]);
+        load_row<E>(c.win.v + at + t * c.win.sn, v[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kInFlight; ++i) {
+        s[i] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) s[i] = fmaf(q[e], k[i][e], s[i]);
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < kInFlight; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
+#pragma unroll
+      for (int i = 0; i < kInFlight; ++i) {
+        if (t0 + i * W > last) s[i] = -INFINITY;
+        s[i] *= c.scale_log2;
+        part.raise(s[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kInFlight; ++i)
+        if (s[i] != -INFINITY) part.add(ex2(s[i] - part.m), 1.f, 1.f, v[i]);
+    }
+  }
   if (have && a.k > 0) {
     const int tiles = kv4_tiles(kv4_length(a, bb));
     const int total = a.k_len ? a.plan[a.b] : a.b * hr * tiles;
@@ -81,61 +123,34 @@ __global__ void __launch_bounds__(kJoinThreads) attn_kv4_join_kernel(const __gri
     if (tiles > 0) {
       const int g = min(a.grid, total);
       const int c0 = kv4_cta(first, total, g), c1 = kv4_cta(first + tiles - 1, total, g);
-      const int slot0 = bb * hr + unit;
+      const long long place0 = (long long)(bb * hr + unit + c0) * 2 * a.rows + in;
       const int parts = 2 * (c1 - c0 + 1);       // two streams each
       for (int i0 = turn; i0 < parts; i0 += W * kInFlight) {
         float2 ml[kInFlight];
         float v[kInFlight][E];
 #pragma unroll
         for (int i = 0; i < kInFlight; ++i) {
-          const int at = i0 + i * W;
-          ml[i] = make_float2(-INFINITY, 0.f);
-          if (at < parts) {
-            const long long place = ((long long)(slot0 + c0) * 2 + at) * a.rows + in;
-            ml[i] = __ldcg(a.ws_ml + place);
-            const float* from = a.ws_o + place * D + lane * E;
-            if constexpr (E == 4) {
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(from));
-              v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
-            } else {
-              const float2 x = __ldcg(reinterpret_cast<const float2*>(from));
-              v[i][0] = x.x, v[i][1] = x.y;
-            }
+          const int at = min(i0 + i * W, parts - 1);   // those past the end are not added
+          const long long place = place0 + (long long)at * a.rows;
+          ml[i] = __ldcg(a.ws_ml + place);
+          const float* from = a.ws_o + place * D + lane * E;
+          if constexpr (E == 4) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(from));
+            v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+          } else {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(from));
+            v[i][0] = x.x, v[i][1] = x.y;
           }
         }
 #pragma unroll
         for (int i = 0; i < kInFlight; ++i) {
-          if (ml[i].y == 0.f) continue;          // nothing seen
-          part.raise(ml[i].x);
-          const float f = ex2(ml[i].x - part.m);
-          part.l = fmaf(f, ml[i].y, part.l);
-#pragma unroll
-          for (int e = 0; e < E; ++e) part.o[e] = fmaf(f * c.v_unit, v[i][e], part.o[e]);
+          if (i0 + i * W >= parts) ml[i].y = 0.f;
+          if (ml[i].y != 0.f) part.raise(ml[i].x);
         }
+#pragma unroll
+        for (int i = 0; i < kInFlight; ++i)      // a sum of 0: nothing seen, O may be unwritten
+          if (ml[i].y != 0.f) part.add(ex2(ml[i].x - part.m), ml[i].y, c.v_unit, v[i]);
       }
-    }
-  }
-  if (have && c.has_win) {
-    const int last = r % c.w;                    // window positions 0 .. last
-    float q[E];
-    load_row<E>(a.q + (long long)row * D + lane * E, q);
-    const long long at = (long long)bb * c.win.sb + (long long)h * c.win.sh + lane * E;
-    for (int t = turn; t <= last; t += W) {
-      float k[E], v[E];
-      load_row<E>(c.win.k + at + t * c.win.sn, k);
-      load_row<E>(c.win.v + at + t * c.win.sn, v);
-      float s = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) s = fmaf(q[e], k[e], s);
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      s *= c.scale_log2;
-      if (s == -INFINITY) continue;
-      part.raise(s);
-      const float f = ex2(s - part.m);
-      part.l += f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) part.o[e] = fmaf(f, v[e], part.o[e]);
     }
   }
   if constexpr (W > 1) {
@@ -149,10 +164,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_kv4_join_kernel(const __gri
     for (int i = 1; i < W; ++i) {
       if (ml[i].y == 0.f) continue;
       part.raise(ml[i].x);
-      const float f = ex2(ml[i].x - part.m);
-      part.l = fmaf(f, ml[i].y, part.l);
+      float v[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) part.o[e] = fmaf(f, os[i][lane * E + e], part.o[e]);
+      for (int e = 0; e < E; ++e) v[e] = os[i][lane * E + e];
+      part.add(ex2(ml[i].x - part.m), ml[i].y, 1.f, v);
     }
   }
   if (!have) return;

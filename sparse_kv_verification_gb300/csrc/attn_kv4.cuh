@@ -65,15 +65,26 @@ __device__ __forceinline__ int kv4_length(const Kv4KArgs& a, int bb) {
   return a.k_len ? min(max(__ldg(a.k_len + bb), 0), a.k) : a.k;
 }
 __device__ __forceinline__ int kv4_tiles(int len) { return (len + kKv4Tile - 1) / kKv4Tile; }
-// CTA c of g has the tiles [c total / g, (c + 1) total / g), g <= total.
+// CTA c of g has the tiles [floor(c total / g), floor((c + 1) total / g)), g <= total:
+// with total = q g + r, floor(c total / g) = c q + floor(c r / g), all in 32 bits.
 __device__ __forceinline__ int kv4_start(int c, int total, int g) {
-  return (int)((long long)c * total / g);
+  const unsigned q = (unsigned)total / (unsigned)g, r = (unsigned)total - q * g;
+  return (int)(c * q + c * r / (unsigned)g);
 }
+// The last c whose range starts at `tile` or before: the largest with c total < (tile
+// + 1) g.  The quotient in fp32 is off by one at most (c < 2^12).
 __device__ __forceinline__ int kv4_cta(int tile, int total, int g) {
-  return (int)((((long long)tile + 1) * g - 1) / total);
+  const long long x = ((long long)tile + 1) * g;
+  int c = (int)__fdividef((float)x, (float)total);
+  if ((long long)c * total >= x) --c;
+  if ((long long)(c + 1) * total < x) ++c;
+  return c;
 }
 
 #ifdef DUSTIN_KV4_KERNEL
+#ifndef GAVE_UP
+#define GAVE_UP(b)
+#endif
 
 namespace {
 
@@ -156,25 +167,26 @@ static_assert(kSmem<128> <= 232448 && kSmem<64> <= 232448, "shared memory of one
 
 __device__ __forceinline__ void raise_flag(unsigned f) { atomicOr(&g_kv4_attn_flags, f); }
 
-// Waits (a whole warp) for about a second at most: 2^23 times four tries of 50 cycles.  In as
-// few instructions as can be: a wait that is over takes 76 cycles so (with the clock
-// and other roles' troubles looked at between tries 115), and the warp that issues
-// the products takes every tile through its waits.
+// Waits (a whole warp) with the library's limit; the clock is read every 1024 tries
+// only, and the code is short: how soon a warp sees that its wait is over sets the
+// pace here.
 __device__ __forceinline__ bool pwait(unsigned long long* bar, uint32_t parity) {
+  static_assert(kWaitLimitCycles == 2000000000LL, "the constant below");
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 0;\n"
+      "{\n .reg .pred p, q;\n .reg .u32 n;\n .reg .u64 t, u;\n mov.u64 t, 0;\n"
+      "A_%=:\n mov.u32 n, 0;\n"
       "L_%=:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra D_%=;\n"
-      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra D_%=;\n"
-      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra D_%=;\n"
-      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra D_%=;\n"
-      " add.u32 n, n, 1;\n setp.lt.u32 q, n, 8388608;\n @q bra L_%=;\n"
+      " add.u32 n, n, 1;\n setp.lt.u32 q, n, 1024;\n @q bra L_%=;\n"
+      " mov.u64 u, %%clock64;\n setp.eq.u64 q, t, 0;\n @q mov.u64 t, u;\n"
+      " sub.u64 u, u, t;\n setp.lt.u64 q, u, 2000000000;\n @q bra A_%=;\n"
       "D_%=:\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   if (__all_sync(0xffffffffu, ok)) return true;
   raise_flag(DUSTIN_DEVFLAG_WAIT_TIMEOUT);
+  GAVE_UP(smem_u32(bar));
   return false;
 }
 // Whether any thread of a warpgroup says so (named barrier `id`).
@@ -202,6 +214,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ float lo_of(uint64_t x) { return __uint_as_float((uint32_t)x); }
@@ -406,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     init(sh.pv_ready, 4 + 4, 2);
     init(sh.s_full, 1, 2);
     init(sh.pv_done, 1, 2);
-    init(sh.q_full, 1, 2);
+    init(sh.q_full, 8, 2);
     init(sh.q_empty, 2 + 8, 2);
     init(sh.seg_full, 1, kSegRing);
     init(sh.seg_empty, GATHER ? kGatherWarps + 2 + 8 + 8 : 1 + 2 + 16 + 8, kSegRing);
@@ -430,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kCodeWarp) give_registers<Split<GATHER>::OTHER>();
 
   if (warp == kWalkWarp) {
-    // ------------------------------------------------- the range, and its Q
+    // ------------------------------------------------------------ the range
     Walk walk(a);
     Seg s{};
     for (int at = 0;; ++at) {
@@ -442,50 +459,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(smem_u32(&sh.seg_full[at % kSegRing]));
       }
       if (!more) break;
-      const int buf = at & 1;
-      if (!pwait(&sh.q_empty[buf], (at >> 1 & 1) ^ 1)) break;
-      // A row's lanes scale it by the power of two that takes its largest finite
-      // entry to [2^13, 2^14): f16 then has all 8 bits of entries down to 2^-30 of
-      // that, and fewer to 2^-37.
-      constexpr int L = D / 8, STEP = 32 / L, U = 4;
-      const int c = lane % L;
-      const __nv_bfloat16* q =
-          a.q + (((long long)s.bb * a.hkv + s.h) * a.gw + s.row0) * D + c * 8;
-      const uint32_t to = q_buf + buf * C::Q + (c / 8) * (kKv4Rows * 128);
-      for (int r0 = lane / L; r0 < NC; r0 += STEP * U) {
-        uint4 v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int r = r0 + u * STEP;
-          v[u] = r < s.rows ? __ldg(reinterpret_cast<const uint4*>(q + (long long)r * D))
-                            : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int r = r0 + u * STEP;
-          const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-          uint32_t top = 0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t m = (i & 1 ? w[i / 2] >> 16 : w[i / 2]) & 0x7fffu;
-            if (m < 0x7f80u) top = max(top, m);
-          }
-#pragma unroll
-          for (int d = 1; d < L; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-          const int e = top ? min(126, 140 - (int)(top >> 7)) : 0;
-          const float up = __int_as_float((e + 127) << 23), down = __int_as_float((127 - e) << 23);
-          uint32_t h[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            h[i] = pack_f16(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
-          if (r < NC) {
-            sts128(to + r * 128 + ((c % 8 ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-            if (c == 0) sh.qs[buf][r] = a.scale_log2 * down;
-          }
-        }
-      }
-      fence_proxy_async_smem();
-      arrive(&sh.q_full[buf]);
     }
     if (blockIdx.x == 0 && a.k_len) walk.table();
   } else if (warp == kLoadWarp && !GATHER) {
@@ -732,16 +705,64 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pos = q * 32 + lane;                     // whose line of P the lane addresses
     const uint32_t p_row0 = p_buf + buf * C::PN * C::P + pos * 128;
     const int col = 2 * (lane & 3);
+    // Both streams' warps bring a segment's Q, a segment ahead.  A row's lanes scale it
+    // by the power of two that takes its largest finite entry to [2^13, 2^14): f16
+    // then has all 8 bits of entries down to 2^-30 of that, and fewer to 2^-37.
+    auto bring = [&](int at) -> bool {
+      const Seg* sp = segment(sh, at);
+      if (!sp) return false;
+      if (sp->slot < 0) return true;
+      const int have = sp->rows;
+      constexpr int L = D / 8, STEP = 8 * 32 / L;      // lanes of a row, rows at a time
+      const int c = lane % L, r0 = (warp - kSoftmaxWarp) * (32 / L) + lane / L;
+      const __nv_bfloat16* from =
+          a.q + (((long long)sp->bb * a.hkv + sp->h) * a.gw + sp->row0) * D + c * 8;
+      if (!pwait(&sh.q_empty[at & 1], (at >> 1 & 1) ^ 1)) return false;
+      const uint32_t to = q_buf + (at & 1) * C::Q + (c / 8) * (kKv4Rows * 128);
+      uint4 v[(NC + STEP - 1) / STEP];
+#pragma unroll
+      for (int u = 0; u < (NC + STEP - 1) / STEP; ++u) {
+        const int r = r0 + u * STEP;
+        v[u] = r < have ? __ldg(reinterpret_cast<const uint4*>(from + (long long)r * D)) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int u = 0; u < (NC + STEP - 1) / STEP; ++u) {
+        const int r = r0 + u * STEP;
+        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        uint32_t top = 0;
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          const uint32_t m = (y & 1 ? w[y / 2] >> 16 : w[y / 2]) & 0x7fffu;
+          if (m < 0x7f80u) top = max(top, m);
+        }
+#pragma unroll
+        for (int d = 1; d < L; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const int e = top ? min(126, 140 - (int)(top >> 7)) : 0;
+        const float up = __int_as_float((e + 127) << 23), down = __int_as_float((127 - e) << 23);
+        uint32_t f[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          f[y] = pack_f16(__uint_as_float(w[y] << 16) * up, __uint_as_float(w[y] & 0xffff0000u) * up);
+        if (r < NC) {
+          sts128(to + r * 128 + ((c % 8 ^ (r & 7)) << 4), f[0], f[1], f[2], f[3]);
+          // Within fp32: 0 times a masked -inf, and infinity times 0, would be NaN.
+          if (c == 0) sh.qs[at & 1][r] = fminf(fmaxf(a.scale_log2 * down, 0x1p-126f), 3.4e38f);
+        }
+      }
+      fence_proxy_async_smem();
+      arrive(&sh.q_full[at & 1]);
+      return true;
+    };
     int i = 0, turn = 0;
     if (q == 0) arrive(&sh.qk_ready[buf]);             // S is free
+    bool ok = bring(0);
     for (int at = 0;; ++at) {
       const Seg* sp = segment(sh, at);
-      bool ok = sp && (sp->slot < 0 || pwait(&sh.q_full[at & 1], at >> 1 & 1));
+      ok = ok && sp && (sp->slot < 0 || pwait(&sh.q_full[at & 1], at >> 1 & 1));
       // A warp leaves where all of its warpgroup do: after a vote.  Every wait in
       // between has its limit, so every warp gets there.
       if (vote(bar, !ok) || sp->slot < 0) break;
       const int n = sp->n, rows = sp->rows, slot = sp->slot;
-      done_with(at);
       uint64_t qs[G], minus[G], l[G];
 #pragma unroll
       for (int g = 0; g < G; ++g) {
@@ -750,12 +771,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         minus[g] = l[g] = 0;
       }
       arrive(&sh.q_empty[at & 1]);
+      ok = bring(at + 1);
+      done_with(at);
       bool fresh = true;                               // no reference yet
       int last = -1;                                   // the stream's latest tile
       for (int j = 0; j < n; ++j, ++i) {
         if ((i & 1) != buf) continue;
         const int phase = i >> 1 & 1;
-        ok = ok && pwait(&sh.s_full[buf], phase);
+        ok = pwait(&sh.s_full[buf], phase) && ok;
         tc_fence_after();
         const uint4 dead = lds128(smem_u32(sh.dead[i % kDeadRing]));
         uint64_t x[G][4];                              // two rows of position k
@@ -794,24 +817,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           float (&to)[4][kKv4Rows] = sh.exchange[buf][turn];
           turn ^= 1;
           load();
+          if (dead.x | dead.y | dead.z | dead.w) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (word >> (8 * k) & 1) {
+#pragma unroll
+                for (int g = 0; g < G; ++g) x[g][k] = pack2(-INFINITY, -INFINITY);
+              }
+          }
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const bool gone = word >> (8 * k) & 1;
-              const float s0 = gone ? -INFINITY : __fmul_rn(lo_of(x[g][k]), lo_of(qs[g]));
-              const float s1 = gone ? -INFINITY : __fmul_rn(hi_of(x[g][k]), hi_of(qs[g]));
-              x[g][k] = pack2(s0, s1);
-              t0 = fmaxf(t0, s0);
-              t1 = fmaxf(t1, s1);
-            }
+            float t0 = max3(lo_of(x[g][0]), lo_of(x[g][1]), fmaxf(lo_of(x[g][2]), lo_of(x[g][3])));
+            float t1 = max3(hi_of(x[g][0]), hi_of(x[g][1]), fmaxf(hi_of(x[g][2]), hi_of(x[g][3])));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) {
               t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, d));
               t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, d));
             }
-            if (lane < 4) *reinterpret_cast<float2*>(&to[q][8 * g + col]) = make_float2(t0, t1);
+            if (lane < 4)
+              *reinterpret_cast<float2*>(&to[q][8 * g + col]) =
+                  make_float2(__fmul_rn(t0, lo_of(qs[g])), __fmul_rn(t1, hi_of(qs[g])));
           }
           tc_fence_before();
           if (vote(bar, !ok)) {
@@ -870,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int g = 0; g < G; ++g)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[g][k] = add2(x[g][k], minus[g]);
+            for (int k = 0; k < 4; ++k) x[g][k] = add2(mul2(x[g][k], qs[g]), minus[g]);
           if ((dead.x & dead.y & dead.z & dead.w) != ~0u) fresh = false;
         }
         // All have read S: they have voted since.
