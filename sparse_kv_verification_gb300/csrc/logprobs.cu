@@ -11,13 +11,16 @@
 // goes by their own size and not by the logits', and halved, so that those of the
 // largest numbers stay finite.
 //
-// The alternatives are found in the same pass.  Of the first 16 words of each
-// warp's lanes the `top` largest lane maxima give a bound that `top` entries reach;
-// entries that reach it go to a list in shared memory, and where the list grows
-// past kRefine it is cut to its `top` best, the last of which is the next bound.
-// An entry that equals the bound counts if its index is lower, so ties go to the
-// lowest index and equal entries (a row of banned tokens at -inf) do not fill the
-// list.  Places come from counting better entries: no order of atomics shows.
+// The alternatives are found in the same pass.  Of the first batch the `top` largest
+// lane maxima give a bound that `top` entries reach; entries that reach it go to a
+// list in shared memory, which after the first batch is cut to its `top` best, the
+// last of which is the next bound: some top * ln(row / batch) entries follow, taken
+// without a barrier.  (A barrier per batch cost a prompt's rows 90 of 290 us.)  Should
+// they not fit (rows that rise, or have few values above many equal ones), the list's
+// own `top`-th is a bound for a second pass, which cuts the list as it fills.  An
+// entry that equals a bound counts if its index is lower, so ties go to the lowest
+// index and equal entries (banned tokens at -inf) do not fill the list.  Places come
+// from counting better entries: no order of atomics shows.
 //
 // One cluster of C CTAs per row (C by the number of rows); rank 0 joins the parts
 // through distributed shared memory.  No workspace.  Bound by HBM for many
@@ -41,12 +44,41 @@ __device__ unsigned int g_logprobs_dev_flags;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kWords = 4;                   // 16-byte words of a thread per batch
+constexpr int kEntries = 16;                // of a thread per batch
 constexpr int kTop = kLogprobsMaxTop;
 constexpr int kLists = (kTop + kWarps - 1) / kWarps;   // lane maxima a warp gives
 constexpr int kList = 1024;
 constexpr int kRefine = 192;                // entries that a list may keep between batches
 static_assert(kRefine + kThreads <= kList && kMaxCluster * kTop <= kList, "list");
+
+// Two fp32 numbers at a time.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float lo_of(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float hi_of(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 using Key = unsigned long long;             // larger: better
 
@@ -135,7 +167,7 @@ __device__ __forceinline__ float element(const uint4& w, int i) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2)
     logprobs_kernel(const __grid_constant__ LogprobArgs a) {
-  constexpr int V = 16 / sizeof(T);
+  constexpr int V = 16 / sizeof(T), kWords = kEntries / V;   // of 16 bytes: their entries, a batch's
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
@@ -177,113 +209,154 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (k < w1) next[u] = __ldg(words + k);
     }
   };
-  load(w0);
-  __syncthreads();
-  for (int base = w0; base < w1; base += kThreads * kWords) {
-    float v[kWords][V];
-    float most = -INFINITY;
+  constexpr int kStep = kThreads * kWords;
+  for (int pass = 0; pass < 2; ++pass) {
+    load(w0);
+    __syncthreads();
+    for (int base = w0, batch = 0; base < w1; base += kStep, ++batch) {
+      float v[kWords][V];
+      float most = -INFINITY;
 #pragma unroll
-    for (int u = 0; u < kWords; ++u) {
-      const int k = base + u * kThreads + tid;
+      for (int u = 0; u < kWords; ++u) {
+        const int k = base + u * kThreads + tid;
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[u][i] = k < w1 ? element<T>(next[u], i) : -INFINITY;
-      if (k == 0 || k == last) {                       // entries beside the row
-        const long long j0 = (long long)k * V - lead;
+        for (int i = 0; i < V; ++i) v[u][i] = element<T>(next[u], i);
+        if (k == 0 || k >= last || k >= w1) {            // entries beside the row, or none
+          const long long j0 = (long long)k * V - lead;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (j0 + i < 0 || j0 + i >= a.vocab) v[u][i] = -INFINITY;
+          for (int i = 0; i < V; ++i)
+            if (k >= w1 || j0 + i < 0 || j0 + i >= a.vocab) v[u][i] = -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < V; i += 2) most = max3(most, v[u][i], v[u][i + 1]);
       }
-#pragma unroll
-      for (int i = 0; i < V; ++i) most = fmaxf(most, v[u][i]);
-    }
-    load(base + kThreads * kWords);
-    if (most > sum.m) {
-      const float t = fmaxf(exponent(sum.m, -0.5f * most, c2), kLeast), f = ex2(t);
-      sum.s = f * fmaf(sum.l, t, sum.s);
-      sum.l *= f;
-      sum.m = most;
-    }
-    const float half = sum.m == -INFINITY ? 0.f : -0.5f * sum.m;
-#pragma unroll
-    for (int u = 0; u < kWords; ++u)
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float t = exponent(v[u][i], half, c2), e = ex2(t);
-        sum.l += e;
-        sum.s = fmaf(e, fmaxf(t, kLeast), sum.s);
+      load(base + kStep);
+      if (pass == 0) {
+        if (most > sum.m) {
+        const float t = fmaxf(exponent(sum.m, -0.5f * most, c2), kLeast), f = ex2(t);
+        sum.s = f * fmaf(sum.l, t, sum.s);
+        sum.l *= f;
+        sum.m = most;
       }
-    if (top == 0) continue;
-
-    if (base == w0) {
-      // A first bound: the `top`-th of the warps' best lane maxima.
-      unsigned mine = order_of(most);
-      const int lists = (top + kWarps - 1) / kWarps;
-      for (int i = 0; i < lists; ++i) {
-        const unsigned best = __reduce_max_sync(0xffffffffu, mine);
-        if (lane == 0) sh.maxima[warp * lists + i] = best;
-        const unsigned has = __ballot_sync(0xffffffffu, mine == best);
-        if (lane == __ffs(has) - 1) mine = 0;
-      }
-      __syncthreads();
-      const int n = kWarps * lists;
-      if (tid < n) {
-        const unsigned x0 = sh.maxima[tid];
-        int better = 0;
-        for (int i = 0; i < n; ++i) better += sh.maxima[i] > x0 || (sh.maxima[i] == x0 && i < tid);
-        // Entries equal to it count, whatever their index; -inf bounds nothing
-        // (lanes without an entry have it, too).
-        if (better == top - 1 && value_of(x0) > -INFINITY) sh.bound = (Key)x0 << 32;
-      }
-      __syncthreads();
-    }
-    // Entries that reach the bound.  Those that do not fit are taken one word and
-    // entry at a time, the list cut in between.
-    Key bound = sh.bound;
-    float least = bound ? value_of((unsigned)(bound >> 32)) : -INFINITY;
-    const int before = sh.count;
-    auto entry = [&](int u, int i) -> Key {            // 0: none
-      const int k = base + u * kThreads + tid;
-      const long long j = (long long)k * V + i - lead;
-      const float xv = v[u][i];
-      if (!(xv >= least) || k >= w1 || j < 0 || j >= a.vocab) return 0;
-      const Key key = key_of(xv, (int)j);
-      return key > bound ? key : 0;
-    };
-    __syncthreads();                                   // all have read the count
-    if (most >= least) {
+      const float half = sum.m == -INFINITY ? 0.f : -0.5f * sum.m;
+      const uint64_t half2 = pack2(half, half), scale2 = pack2(c2, c2), point5 = pack2(0.5f, 0.5f);
+      uint64_t l2 = pack2(sum.l, 0.f), s2 = pack2(sum.s, 0.f);
 #pragma unroll
       for (int u = 0; u < kWords; ++u)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const Key key = entry(u, i);
-          if (key) {
-            const int at = atomicAdd(&sh.count, 1);
-            if (at < kList) sh.list[at] = key;
-          }
+        for (int i = 0; i < V; i += 2) {
+          // exponent(), two entries at a time
+          const uint64_t t = mul2(fma2(pack2(v[u][i], v[u][i + 1]), point5, half2), scale2);
+          const uint64_t e = pack2(ex2(lo_of(t)), ex2(hi_of(t)));
+          l2 = add2(l2, e);
+          s2 = fma2(e, pack2(fmaxf(lo_of(t), kLeast), fmaxf(hi_of(t), kLeast)), s2);
         }
+      sum.l = lo_of(l2) + hi_of(l2);
+      sum.s = lo_of(s2) + hi_of(s2);
+      }
+      if (top == 0) continue;
+
+      if (base == w0 && pass == 0) {
+        // A first bound: the `top`-th of the warps' best lane maxima.
+        unsigned mine = order_of(most);
+        const int lists = (top + kWarps - 1) / kWarps;
+        for (int i = 0; i < lists; ++i) {
+          const unsigned best = __reduce_max_sync(0xffffffffu, mine);
+          if (lane == 0) sh.maxima[warp * lists + i] = best;
+          const unsigned has = __ballot_sync(0xffffffffu, mine == best);
+          if (lane == __ffs(has) - 1) mine = 0;
+        }
+        __syncthreads();
+        const int n = kWarps * lists;
+        if (tid < n) {
+          const unsigned x0 = sh.maxima[tid];
+          int better = 0;
+          for (int i = 0; i < n; ++i) better += sh.maxima[i] > x0 || (sh.maxima[i] == x0 && i < tid);
+          // Entries equal to it count, whatever their index; -inf bounds nothing
+          // (lanes without an entry have it, too).
+          if (better == top - 1 && value_of(x0) > -INFINITY) sh.bound = (Key)x0 << 32;
+        }
+        __syncthreads();
+      }
+      // Entries that reach the bound.  It rises after 1, 2, 4, .. batches.
+      const bool apart = base > w0 && pass == 0;           // no barriers
+      if (apart && !(batch & (batch - 1))) {
+        __syncthreads();
+        const bool cut = sh.count <= kList;
+        __syncthreads();
+        if (cut) refine(sh, top);
+      }
+      Key bound = sh.bound;
+      float least = bound ? value_of((unsigned)(bound >> 32)) : -INFINITY;
+      auto entry = [&](int u, int i) -> Key {              // 0: none
+        const int k = base + u * kThreads + tid;
+        const long long j = (long long)k * V + i - lead;
+        const float xv = v[u][i];
+        if (!(xv >= least) || k >= w1 || j < 0 || j >= a.vocab) return 0;
+        const Key key = key_of(xv, (int)j);
+        return key > bound ? key : 0;
+      };
+      int before = 0;
+      if (!apart) {
+        before = sh.count;
+        __syncthreads();                                   // all have read the count
+      }
+      if (most >= least) {
+        unsigned reach = 0;
+#pragma unroll
+        for (int u = 0; u < kWords; ++u)
+#pragma unroll
+          for (int i = 0; i < V; ++i) reach |= (unsigned)(v[u][i] >= least) << (u * V + i);
+        while (reach) {                                    // few: read again from the row
+          const int e = __ffs(reach) - 1, k = base + e / V * kThreads + tid;
+          reach &= reach - 1;
+          const long long j = (long long)k * V + e % V - lead;
+          if (k >= w1 || j < 0 || j >= a.vocab) continue;
+          const Key key = key_of((float)x[j], (int)j);
+          if (key <= bound) continue;
+          const int at = atomicAdd(&sh.count, 1);
+          if (at < kList) sh.list[at] = key;
+        }
+      }
+      if (apart) continue;
+      __syncthreads();
+      if (sh.count > kList) {
+        // Taken again, one word and entry at a time, the list cut in between.
+        __syncthreads();
+        if (tid == 0) sh.count = before;                   // at most kRefine
+        __syncthreads();
+#pragma unroll 1
+        for (int u = 0; u < kWords; ++u)
+#pragma unroll 1
+          for (int i = 0; i < V; ++i) {
+            Key key = 0;
+#pragma unroll
+            for (int u1 = 0; u1 < kWords; ++u1)            // v stays in registers
+#pragma unroll
+              for (int i1 = 0; i1 < V; ++i1)
+                if (u1 == u && i1 == i) key = entry(u1, i1);
+            if (__syncthreads_or(key != 0)) {
+              if (key) sh.list[atomicAdd(&sh.count, 1)] = key;
+              refine(sh, top);
+              bound = sh.bound;
+              least = bound ? value_of((unsigned)(bound >> 32)) : -INFINITY;
+            }
+          }
+      } else if (sh.count > kRefine || base == w0) {
+        refine(sh, top);
+      }
     }
     __syncthreads();
-    if (sh.count > kList) {
-      __syncthreads();
-      if (tid == 0) sh.count = before;                 // at most kRefine
-      __syncthreads();
-#pragma unroll
-      for (int u = 0; u < kWords; ++u)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const Key key = entry(u, i);
-          if (__syncthreads_or(key != 0)) {
-            if (key) sh.list[atomicAdd(&sh.count, 1)] = key;
-            refine(sh, top);
-            bound = sh.bound;
-            least = bound ? value_of((unsigned)(bound >> 32)) : -INFINITY;
-          }
-        }
-    } else if (sh.count > kRefine) {
-      refine(sh, top);
+    const bool again = pass == 0 && sh.count > kList;
+    if (top > 0) refine(sh, top);
+    if (!again) break;
+    // A second pass: the bound is kept, the list is not.
+    if (tid == 0) {
+      sh.bound = sh.best[top - 1] - 1;                     // reached by that one, too
+      sh.count = 0;
     }
+    __syncthreads();
   }
-  if (top > 0) refine(sh, top);
 
   // Sums: lanes, warps, CTAs.
 #pragma unroll
