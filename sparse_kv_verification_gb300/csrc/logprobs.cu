@@ -44,7 +44,7 @@ __device__ unsigned int g_logprobs_dev_flags;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kEntries = 16;                // of a thread per batch
+constexpr int kWords = 4;                   // 16-byte words of a thread per batch
 constexpr int kTop = kLogprobsMaxTop;
 constexpr int kLists = (kTop + kWarps - 1) / kWarps;   // lane maxima a warp gives
 constexpr int kList = 1024;
@@ -164,10 +164,42 @@ __device__ __forceinline__ float element(const uint4& w, int i) {
   return __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
 }
 
+// Makes an entry -inf.
+template <typename T>
+__device__ __forceinline__ void forget(uint4& w, int i) {
+  uint32_t* u = &w.x;
+  if constexpr (sizeof(T) == 4)
+    u[i] = 0xff800000u;
+  else
+    u[i / 2] = i & 1 ? (u[i / 2] & 0xffffu) | 0xff800000u : (u[i / 2] & 0xffff0000u) | 0xff80u;
+}
+// The largest entry that is not NaN, or -inf.
+template <typename T>
+__device__ __forceinline__ float largest(const uint4 (&w)[kWords]) {
+  if constexpr (sizeof(T) == 4) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kWords; ++u) {
+      m = max3(m, __uint_as_float(w[u].x), __uint_as_float(w[u].y));
+      m = max3(m, __uint_as_float(w[u].z), __uint_as_float(w[u].w));
+    }
+    return m;
+  } else {
+    uint32_t m = 0xff80ff80u;                            // two -inf
+#pragma unroll
+    for (int u = 0; u < kWords; ++u) {
+      const uint32_t x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) asm("max.bf16x2 %0, %0, %1;\n" : "+r"(m) : "r"(x[i]));
+    }
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2)
     logprobs_kernel(const __grid_constant__ LogprobArgs a) {
-  constexpr int V = 16 / sizeof(T), kWords = kEntries / V;   // of 16 bytes: their entries, a batch's
+  constexpr int V = 16 / sizeof(T);                    // entries of 16 bytes
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
@@ -214,23 +246,21 @@ __global__ void __launch_bounds__(kThreads, 2)
     load(w0);
     __syncthreads();
     for (int base = w0, batch = 0; base < w1; base += kStep, ++batch) {
-      float v[kWords][V];
-      float most = -INFINITY;
+      uint4 cur[kWords];
+      auto v = [&](int u, int i) { return element<T>(cur[u], i); };
 #pragma unroll
       for (int u = 0; u < kWords; ++u) {
         const int k = base + u * kThreads + tid;
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[u][i] = element<T>(next[u], i);
+        cur[u] = next[u];
         if (k == 0 || k >= last || k >= w1) {            // entries beside the row, or none
           const long long j0 = (long long)k * V - lead;
 #pragma unroll
           for (int i = 0; i < V; ++i)
-            if (k >= w1 || j0 + i < 0 || j0 + i >= a.vocab) v[u][i] = -INFINITY;
+            if (k >= w1 || j0 + i < 0 || j0 + i >= a.vocab) forget<T>(cur[u], i);
         }
-#pragma unroll
-        for (int i = 0; i < V; i += 2) most = max3(most, v[u][i], v[u][i + 1]);
       }
       load(base + kStep);
+      const float most = largest<T>(cur);
       if (pass == 0) {
         if (most > sum.m) {
         const float t = fmaxf(exponent(sum.m, -0.5f * most, c2), kLeast), f = ex2(t);
@@ -246,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int i = 0; i < V; i += 2) {
           // exponent(), two entries at a time
-          const uint64_t t = mul2(fma2(pack2(v[u][i], v[u][i + 1]), point5, half2), scale2);
+          const uint64_t t = mul2(fma2(pack2(v(u, i), v(u, i + 1)), point5, half2), scale2);
           const uint64_t e = pack2(ex2(lo_of(t)), ex2(hi_of(t)));
           l2 = add2(l2, e);
           s2 = fma2(e, pack2(fmaxf(lo_of(t), kLeast), fmaxf(hi_of(t), kLeast)), s2);
@@ -280,19 +310,16 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       // Entries that reach the bound.  It rises after 1, 2, 4, .. batches.
       const bool apart = base > w0 && pass == 0;           // no barriers
-      if (apart && !(batch & (batch - 1))) {
-        __syncthreads();
-        const bool cut = sh.count <= kList;
-        __syncthreads();
-        if (cut) refine(sh, top);
-      }
+      if (apart && !(batch & (batch - 1)) && __syncthreads_or(sh.count > top)) refine(sh, top);
       Key bound = sh.bound;
       float least = bound ? value_of((unsigned)(bound >> 32)) : -INFINITY;
-      auto entry = [&](int u, int i) -> Key {              // 0: none
-        const int k = base + u * kThreads + tid;
-        const long long j = (long long)k * V + i - lead;
-        const float xv = v[u][i];
-        if (!(xv >= least) || k >= w1 || j < 0 || j >= a.vocab) return 0;
+      // Entry e of the thread's, read again from the row; 0: none that counts.
+      auto entry = [&](int e) -> Key {
+        const int k = base + e / V * kThreads + tid;
+        const long long j = (long long)k * V + e % V - lead;
+        if (k >= w1 || j < 0 || j >= a.vocab) return 0;
+        const float xv = (float)x[j];
+        if (!(xv >= least)) return 0;
         const Key key = key_of(xv, (int)j);
         return key > bound ? key : 0;
       };
@@ -306,54 +333,47 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int u = 0; u < kWords; ++u)
 #pragma unroll
-          for (int i = 0; i < V; ++i) reach |= (unsigned)(v[u][i] >= least) << (u * V + i);
-        while (reach) {                                    // few: read again from the row
-          const int e = __ffs(reach) - 1, k = base + e / V * kThreads + tid;
+          for (int i = 0; i < V; ++i) reach |= (unsigned)(v(u, i) >= least) << (u * V + i);
+        while (reach) {                                  // few
+          const Key key = entry(__ffs(reach) - 1);
           reach &= reach - 1;
-          const long long j = (long long)k * V + e % V - lead;
-          if (k >= w1 || j < 0 || j >= a.vocab) continue;
-          const Key key = key_of((float)x[j], (int)j);
-          if (key <= bound) continue;
+          if (!key) continue;
           const int at = atomicAdd(&sh.count, 1);
-          if (at < kList) sh.list[at] = key;
+          if (at < kList)
+            sh.list[at] = key;
+          else
+            sh.over = 1;
         }
       }
       if (apart) continue;
       __syncthreads();
-      if (sh.count > kList) {
+      if (sh.over) {
         // Taken again, one word and entry at a time, the list cut in between.
         __syncthreads();
-        if (tid == 0) sh.count = before;                   // at most kRefine
+        if (tid == 0) sh.count = before, sh.over = 0;      // at most kRefine
         __syncthreads();
 #pragma unroll 1
-        for (int u = 0; u < kWords; ++u)
-#pragma unroll 1
-          for (int i = 0; i < V; ++i) {
-            Key key = 0;
-#pragma unroll
-            for (int u1 = 0; u1 < kWords; ++u1)            // v stays in registers
-#pragma unroll
-              for (int i1 = 0; i1 < V; ++i1)
-                if (u1 == u && i1 == i) key = entry(u1, i1);
-            if (__syncthreads_or(key != 0)) {
-              if (key) sh.list[atomicAdd(&sh.count, 1)] = key;
-              refine(sh, top);
-              bound = sh.bound;
-              least = bound ? value_of((unsigned)(bound >> 32)) : -INFINITY;
-            }
+        for (int e = 0; e < kWords * V; ++e) {
+          const Key key = entry(e);
+          if (__syncthreads_or(key != 0)) {
+            if (key) sh.list[atomicAdd(&sh.count, 1)] = key;
+            refine(sh, top);
+            bound = sh.bound;
+            least = bound ? value_of((unsigned)(bound >> 32)) : -INFINITY;
           }
+        }
       } else if (sh.count > kRefine || base == w0) {
         refine(sh, top);
       }
     }
     __syncthreads();
-    const bool again = pass == 0 && sh.count > kList;
+    const bool again = sh.over;                          // in the first pass only
     if (top > 0) refine(sh, top);
     if (!again) break;
     // A second pass: the bound is kept, the list is not.
     if (tid == 0) {
       sh.bound = sh.best[top - 1] - 1;                     // reached by that one, too
-      sh.count = 0;
+      sh.count = sh.over = 0;
     }
     __syncthreads();
   }
