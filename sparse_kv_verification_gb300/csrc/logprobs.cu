@@ -129,7 +129,8 @@ __device__ __forceinline__ Sums join(const Sums& a, const Sums& b, float c2) {
 }
 
 struct Shared {
-  Key list[kList], best[kTop];
+  alignas(16) Key list[kList];
+  Key best[kTop];
   unsigned maxima[kWarps * kLists];
   Sums part[kWarps], all;
   Key bound;
@@ -307,6 +308,24 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (better == top - 1 && value_of(x0) > -INFINITY) sh.bound = (Key)x0 << 32;
         }
         __syncthreads();
+        // Rows with few words leave warps with too few: of all lanes, then.
+        if (sh.bound == 0) {
+          unsigned* lanes = reinterpret_cast<unsigned*>(sh.list);   // still empty
+          const unsigned x0 = order_of(most);
+          lanes[tid] = x0;
+          __syncthreads();
+          int better = 0;
+          for (int i = 0; i < kThreads; i += 4) {
+            const uint4 y = *reinterpret_cast<const uint4*>(lanes + i);
+            better += y.x > x0 || (y.x == x0 && i < tid);
+            better += y.y > x0 || (y.y == x0 && i + 1 < tid);
+            better += y.z > x0 || (y.z == x0 && i + 2 < tid);
+            better += y.w > x0 || (y.w == x0 && i + 3 < tid);
+          }
+          __syncthreads();                               // the list may be filled
+          if (better == top - 1 && value_of(x0) > -INFINITY) sh.bound = (Key)x0 << 32;
+          __syncthreads();
+        }
       }
       // Entries that reach the bound.  It rises after 1, 2, 4, .. batches.
       const bool apart = base > w0 && pass == 0;           // no barriers

@@ -788,7 +788,9 @@ def kv4_desc(cache: torch.Tensor, page_table: Optional[torch.Tensor] = None,
     if cache.dtype != torch.uint8 or len(strides) != 4 or strides[3] != 1:
         raise ValueError("a 4-bit cache must be a uint8 4-D tensor with a contiguous last dim")
     table, page_size, pages_per_seq, num_pages = None, 0, 0, 0
-    index = _one_device(cache, page_table)
+    index = cache.get_device() if page_table is None else _one_device(cache, page_table)
+    if index < 0:
+        raise ValueError("tensors must live on a CUDA device")
     if page_table is not None:
         rows = page_table.stride()
         if page_table.dtype != torch.int32 or len(rows) != 2:

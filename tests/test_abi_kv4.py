@@ -111,12 +111,16 @@ def test_logprobs_refusals(lib):
     assert call(b=0, x=None) == 0 and call(w=0, x=None) == 0
 
 
-def test_binding_refusals(calls):  # noqa: F811
+def test_binding_refusals(calls, monkeypatch):  # noqa: F811
     N = native
     u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
     i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
     bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
     cache = u8(2, 2, 32, 144)
+    with pytest.raises(ValueError, match="CUDA"):
+        N.kv4_desc(cache)                                # on the CPU
+    real = torch.Tensor.get_device
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0 if t.device.type == "cpu" else real(t))
     for bad in (cache.int(), cache[0], cache[..., ::2]):
         with pytest.raises(ValueError, match="uint8"):
             N.kv4_desc(bad)
