@@ -4,7 +4,7 @@
 // Mathematics: S = scale q K^T, O = softmax(S) V with K and V from records
 // (kv4.cuh), by a running reference m per query row: p = 2^(s - m), l = sum p,
 // O = sum p v.  m is not the maximum but a number 8 below the largest score seen
-// when it was set; it moves only where a weight would reach 2^15 (weights are f16).
+// when it was set; it moves only where a weight would pass 2^15 (weights are f16).
 // Weights 2^-33 of the largest still round relative to it, and most tiles need
 // no maximum at all.
 //
@@ -14,22 +14,34 @@
 //   O^T [channel][row]  += V^T [channel][position] P^T      A in tensor memory
 // A step has 8 to 64 rows to a kv head: as M they would be padded to 128 (40 rows:
 // 1024 cycles of tensor core per tile, where the bytes of a tile take 800); as N
-// they are padded to the next 16.  And K and V, whose 4-bit codes pass through
-// registers anyway, go from there to tensor memory; only Q and P are operands in
-// shared memory, whose bandwidth 32 KB tiles of K and V in f16 would take up.
+// they are padded to the next 16, and a product with A in tensor memory takes N / 2
+// cycles per 16 deep (measured: 9.2 at N 16, 24.2 at 48; with A in shared memory 39
+// and 44).  And K and V, whose 4-bit codes pass through registers anyway, go from
+// there to tensor memory; only Q and P are operands in shared memory.
 //
-// f16 holds every cached value exactly (6 bits, 2^-11 .. 2688), and a q row scaled
+// f16 holds every cached value exactly (6 bits, 2^-10 .. 2688), and a q row scaled
 // by a power of two.
 //
 // One persistent CTA per SM.  The tiles of all units (sequence, kv head, block of
 // rows) lie on a line that the CTAs share in equal ranges; a CTA's part of a unit
 // is a segment.  Its even and odd tiles are two streams, each with an m, l and O of
 // its own, so that one's chain (scores, softmax, weights, product) hides the
-// other's; the streams' O, m and l go to the workspace.  Roles of the 20 warps: 0
-// issues the products, 1 (and 3, where rows are gathered) loads records, 2 walks the
-// CTA's range and prepares Q; 4-7 and 8-11 take a stream's K and V to tensor memory
-// (K: a thread has a position; V: a warp has 32 channels, bytes transposed by
-// ldmatrix); 12-15 and 16-19 are a stream's softmax.
+// other's; the streams' O, m and l go to the workspace.  Roles of the 28 warps: 0
+// and 3 issue a stream's products each, 1 loads records, 2 walks the CTA's range;
+// 4-11 take the first stream's K and V to tensor memory (K: a thread has a position;
+// V: a warp has 32 channels, bytes transposed by ldmatrix), 12-19 the second's;
+// 20-23 and 24-27 are a stream's softmax and bring Q.  Where records are gathered
+// (idx, or records apart) 4-11 load them and 12-15, 16-19 convert a stream's K and V.
+//
+// Measured (16 sequences x 32768 positions, 8 kv heads, D 128; bytes alone take 89
+// us): 194 us with 40 rows to a kv head, 134 with 8, 261 with 64; D 64 160; 2048
+// gathered positions each 38.  Parts left out of an earlier form of 28 warps (190 us
+// whole): without V's conversion 175, without K's 179, without both 164, without the
+// softmax 161; without all of these and the products 122: what is left looks like
+// the chain of waits between the roles.  How it got here: one stream 251 us; two
+// streams 187.  Weights in two buffers, K and V by warps of their own, Q brought by the
+// softmax warps and light first tiles read 171, but two waits were missing then (see
+// pv_ready and the wait at a segment's last tile); with them it is 194.
 #pragma once
 
 #include <cstddef>
@@ -82,9 +94,6 @@ __device__ __forceinline__ int kv4_cta(int tile, int total, int g) {
 }
 
 #ifdef DUSTIN_KV4_KERNEL
-#ifndef GAVE_UP
-#define GAVE_UP(b)
-#endif
 
 namespace {
 
@@ -127,7 +136,7 @@ constexpr float kMostWeight = 15.f;   // log2
 template <int D>
 struct Cfg {
   static constexpr int STAGE = kTile * Rec<D>::BYTES;
-  static constexpr int PN = 2, STAGES = D == 128 ? 6 : 12;   // buffers of P per stream; tiles in flight
+  static constexpr int PN = 2 /* pv_ready has as many */, STAGES = D == 128 ? 6 : 12;   // buffers of P per stream; tiles in flight
   static constexpr int P = kTile * 128;             // bytes: 64 rows of f16 per position
   static constexpr int Q = D / 64 * kKv4Rows * 128; // 64-channel halves behind one another
 };
@@ -140,8 +149,13 @@ struct Seg {
 
 struct Control {
   unsigned long long full[12], empty[12];
-  // Of a stream: K there and S free; V and P there; each product done.
-  unsigned long long qk_ready[2], pv_ready[2], s_full[2], pv_done[2];
+  // Of a stream: K there and S free; each product done.
+  unsigned long long qk_ready[2], s_full[2], pv_done[2];
+  // V and P there, by buffer of P.  With a buffer more than that the softmax may be
+  // a tile ahead of V, whose own warps K does not wait for; on one barrier its
+  // arrivals would stand in for V's.  On a buffer's, the next are two tiles on, whose
+  // scores are asked for after this product.
+  unsigned long long pv_ready[2][2];
   unsigned long long q_full[2], q_empty[2], seg_full[kSegRing], seg_empty[kSegRing];
   unsigned long long drain[2];
   Seg seg[kSegRing];
@@ -186,7 +200,6 @@ __device__ __forceinline__ bool pwait(unsigned long long* bar, uint32_t parity) 
       : "memory");
   if (__all_sync(0xffffffffu, ok)) return true;
   raise_flag(DUSTIN_DEVFLAG_WAIT_TIMEOUT);
-  GAVE_UP(smem_u32(bar));
   return false;
 }
 // Whether any thread of a warpgroup says so (named barrier `id`).
@@ -366,7 +379,8 @@ __device__ __forceinline__ void products(Control& sh, uint32_t p_buf, uint32_t q
   int i = 0, scored = 0, done = 0;         // tiles of the CTA, of the stream
   auto pv = [&](bool fresh) {
     const uint64_t pd = pd0 + (done & (C::PN - 1)) * (C::P >> 4);
-    if (!pwait(&sh.pv_ready[BUF], done++ & 1)) return false;
+    if (!pwait(&sh.pv_ready[BUF][done & 1], done >> 1 & 1)) return false;
+    ++done;
     tc_fence_after();
 #pragma unroll
     for (int k = 0; k < kTile / 16; ++k)
@@ -420,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     init(sh.full, GATHER ? 4 * (32 + 1) : 1, STAGES);
     init(sh.empty, GATHER ? 4 : 8, STAGES);
     init(sh.qk_ready, 4 + 1, 2);
-    init(sh.pv_ready, 4 + 4, 2);
+    init(sh.pv_ready[0], 4 + 4, 4);
     init(sh.s_full, 1, 2);
     init(sh.pv_done, 1, 2);
     init(sh.q_full, 8, 2);
@@ -578,9 +592,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     cp_async_wait<0>();
   } else if (warp == kMmaWarp || warp == kMmaWarp2) {
     // ------------------------------------------------ a stream's products
-    // The whole warp walks, one lane issues.  A warp per stream: a tile takes it
-    // through two waits and 16 products, and one warp for both streams was what
-    // bounded all others.
+    // A warp per stream: a tile takes it through two waits and 16 products, and the
+    // streams do not wait for each other here.
     if (warp == kMmaWarp)
       products<D, NC, 0>(sh, p_buf, q_buf);
     else
@@ -655,6 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               vscale[0][p] = __ushort_as_half((unsigned short)s);
               vscale[1][p] = __ushort_as_half((unsigned short)(s >> 16));
             }
+            __syncwarp();
           }
           ok = pwait(&sh.pv_done[buf], phase);
           if (!ok) break;
@@ -685,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           arrive(&sh.empty[st]);
           tc_wait_st();
           tc_fence_before();
-          arrive(&sh.pv_ready[buf]);
+          arrive(&sh.pv_ready[buf][x >> 1 & 1]);
         }
       }
       i = end;
@@ -696,8 +710,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A thread has 4 positions (8 k + lane / 4 of the warp's 32, k = 0 .. 3) and two
     // rows of each 8 (2 (lane % 4), + 1): the rows' factors, references and sums are
     // a quarter of what a position's whole line of rows would take, so that they
-    // stay in registers (read from shared memory for every tile they took 384 of its
-    // cycles), and the weights leave by stmatrix.
+    // stay in registers (from shared memory, at 4 cycles per broadcast of 16 bytes,
+    // they would take 384 of its cycles per tile: by count, not timed), and the
+    // weights leave by stmatrix.
     constexpr int G = NC / 8;                          // groups of 8 rows
     const int buf = (warp - kSoftmaxWarp) >> 2, q = warp & 3;
     const int bar = 1 + buf;                           // named barrier of the warpgroup
@@ -919,7 +934,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        arrive(&sh.pv_ready[buf]);
+        // At the segment's last tile the product before is waited for here, while this
+        // one cannot be done: the wait behind the loop goes by parity, and would take
+        // one that is two products back for the last.
+        if (j + 2 >= n) ok = pwait(&sh.pv_done[buf], phase ^ 1) && ok;
+        arrive(&sh.pv_ready[buf][phase]);
         last = i;
       }
       // The rows' sums over positions.

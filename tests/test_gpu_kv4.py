@@ -420,6 +420,19 @@ def test_nothing_to_see():
     assert not o.any() and torch.isneginf(lse).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("idx", [None, "any"])
+@pytest.mark.parametrize("n,rows", [(40000, 1), (57000, 5), (9000, 3)])
+def test_equal_calls_give_equal_bits(d, n, rows, idx):
+    """A few tiles per SM, taken while the code is still being fetched: the warps of
+    K, V and the softmax are then the furthest apart."""
+    c = Case(1, 8, 1, d, rows, n, idx=idx, win=False, seed=n)
+    o, lse = c.check()
+    for _ in range(40):
+        again = c.run()
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
 @pytest.mark.parametrize("b,hkv,n,lens", [(300, 2, 130, None), (1, 1, 40000, None), (3, 2, 5000, None),
                                           (90, 1, 600, "ragged"), (2, 4, 9000, [8999, 1])])
 def test_shares_of_the_line(b, hkv, n, lens):
