@@ -613,7 +613,10 @@ int dustin_kv4_read(int n_layers, int b, int h_kv, int d, int n, int k,
  * largest are rounded); scores, maxima, sums and partial results are fp32.  A
  * weight of a cached position is rounded to f16 for its product with V (by 2^-11,
  * or by 2^-33 of the row's largest weight so far), and o to bf16 once.
- * Limits: as dustin_sparse_verify_attn; k <= n without idx; k <= 2^27; b <= 2^20;
+ * Where a row's largest |q| * scale * 2^k_exp passes 2^140, its scores are those of
+ * 2^140 (they may still be infinite).
+ * Limits: as dustin_sparse_verify_attn; with k > 0, scale * 2^k_exp in [2^-120, 2^126]
+ * (DUSTIN_ERR_SHAPE); k <= n without idx; k <= 2^27; b <= 2^20;
  * (b * h_kv * blocks of 64 query rows) * (k / 128 + 1) <= 2^30; a workspace of 2^35
  * bytes.
  * Workspace: dustin_kv4_verify_attn_workspace_size (with or without win, idx);

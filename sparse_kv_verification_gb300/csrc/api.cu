@@ -1274,6 +1274,12 @@ int dustin_kv4_verify_attn(int b, int h_q, int h_kv, int d, int w, int n, int k,
   if (flags & ~DUSTIN_ATTN_KV_READY)
     return fail(DUSTIN_ERR_INVALID_ARG, "%s: unknown flags 0x%x", what, flags);
   if (k > 0 && (rc = check_kv4(kv, n, d, what))) return rc;
+  if (k > 0) {
+    // The kernel's factor is their product, in fp32: neither infinite nor subnormal.
+    const double unit = std::ldexp((double)scale, kv->k_exp);
+    if (unit < 0x1p-120 || unit > 0x1p126)
+      return fail(DUSTIN_ERR_SHAPE, "%s: scale * 2^k_exp = %g (2^-120 .. 2^126)", what, unit);
+  }
   if (win && (rc = check_win(win, d, what))) return rc;
   Kv4AttnArgs a = kv4_attn_args(b, h_q, h_kv, d, w, k);
   const size_t need = attn_kv4_workspace(a, sm_count());

@@ -79,6 +79,14 @@ def test_attention_refusals(lib):
     assert call(q=None) == 1 and call(o=None) == 1 and call(lse=None) == 1 and call(kv=None) == 1
     assert call(q=FAKE + 8) == 5 and call(idx=FAKE + 2) == 5 and call(k_len=FAKE + 1) == 5
     assert call(scale=0.0) == 1 and call(scale=float("nan")) == 1 and call(flags=2) == 1
+    # scale * 2^k_exp within [2^-120, 2^126]; a call in range gets as far as its workspace.
+    low, high = desc4(k_exp=-64), desc4(k_exp=64)
+    assert call(scale=2.0 ** 127) == 2 and call(scale=1e20, kv=high) == 2
+    assert call(scale=2.0 ** -121) == 2 and call(scale=2.0 ** -57, kv=low) == 2
+    for kw in (dict(scale=2.0 ** 126), dict(scale=2.0 ** -120), dict(scale=2.0 ** 62, kv=high),
+               dict(scale=2.0 ** -56, kv=low)):
+        assert call(ws=None, **kw) == 4
+    assert call(scale=2.0 ** 127, k=0, kv=None, ws=None) == 4                   # no cache, no such product
     assert call(kv=desc4(stride_n=100)) == 2 and call(kv=desc4(k_exp=-70)) == 2
     assert call(kv=desc4(True, pages_per_seq=15)) == 2 and call(kv=desc4(True, page_size=8)) == 3
     assert call(win=desc(True)) == 3 and call(win=desc(k=None)) == 1
