@@ -34,14 +34,14 @@
 // (idx, or records apart) 4-11 load them and 12-15, 16-19 convert a stream's K and V.
 //
 // Measured (16 sequences x 32768 positions, 8 kv heads, D 128; bytes alone take 89
-// us): 194 us with 40 rows to a kv head, 134 with 8, 261 with 64; D 64 160; 2048
-// gathered positions each 38.  Parts left out of an earlier form of 28 warps (190 us
+// us): 184 us with 40 rows to a kv head, 135 with 8, 241 with 64; D 64 156; 2048
+// gathered positions each 37.  Parts left out of an earlier form of 28 warps (190 us
 // whole): without V's conversion 175, without K's 179, without both 164, without the
 // softmax 161; without all of these and the products 122: what is left looks like
 // the chain of waits between the roles.  How it got here: one stream 251 us; two
 // streams 187.  Weights in two buffers, K and V by warps of their own, Q brought by the
 // softmax warps and light first tiles read 171, but two waits were missing then (see
-// pv_ready and the wait at a segment's last tile); with them it is 194.
+// pv_ready and o_done); with a wait at each segment's last tile 194, with o_done 184.
 #pragma once
 
 #include <cstddef>
@@ -151,6 +151,9 @@ struct Control {
   unsigned long long full[12], empty[12];
   // Of a stream: K there and S free; each product done.
   unsigned long long qk_ready[2], s_full[2], pv_done[2];
+  // A stream's last product of a segment done.  (The softmax may be two products ahead
+  // of pv_done, whose parity then says nothing.)
+  unsigned long long o_done[2];
   // V and P there, by buffer of P.  With a buffer more than that the softmax may be
   // a tile ahead of V, whose own warps K does not wait for; on one barrier its
   // arrivals would stand in for V's.  On a buffer's, the next are two tiles on, whose
@@ -407,7 +410,10 @@ __device__ __forceinline__ void products(Control& sh, uint32_t p_buf, uint32_t q
       if (x > first) ok = pv(x == first + 2);
     }
     mma_commit(on, smem_u32(&sh.q_empty[at & 1]));     // also where the stream has none
-    if (ok && first < end) ok = pv(first + 2 >= end);
+    if (ok && first < end) {
+      ok = pv(first + 2 >= end);
+      mma_commit(on, smem_u32(&sh.o_done[BUF]));
+    }
     i = end;
   }
   // The products in flight end before tensor memory is freed.
@@ -437,6 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     init(sh.pv_ready[0], 4 + 4, 4);
     init(sh.s_full, 1, 2);
     init(sh.pv_done, 1, 2);
+    init(sh.o_done, 1, 2);
     init(sh.q_full, 8, 2);
     init(sh.q_empty, 2 + 8, 2);
     init(sh.seg_full, 1, kSegRing);
@@ -768,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       arrive(&sh.q_full[at & 1]);
       return true;
     };
-    int i = 0, turn = 0;
+    int i = 0, turn = 0, segs = 0;                     // segs: with tiles of the stream
     if (q == 0) arrive(&sh.qk_ready[buf]);             // S is free
     bool ok = bring(0);
     for (int at = 0;; ++at) {
@@ -934,10 +941,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        // At the segment's last tile the product before is waited for here, while this
-        // one cannot be done: the wait behind the loop goes by parity, and would take
-        // one that is two products back for the last.
-        if (j + 2 >= n) ok = pwait(&sh.pv_done[buf], phase ^ 1) && ok;
         arrive(&sh.pv_ready[buf][phase]);
         last = i;
       }
@@ -957,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (q == 0) *reinterpret_cast<uint64_t*>(&sh.minus[buf][8 * g + col]) = minus[g];
         }
       }
-      if (ok && last >= 0) ok = pwait(&sh.pv_done[buf], last >> 1 & 1);
+      if (ok && last >= 0) ok = pwait(&sh.o_done[buf], segs++ & 1);
       tc_fence_after();
       if (vote(bar, !ok)) break;
       const long long place = ((long long)slot * 2 + buf) * a.rows;
