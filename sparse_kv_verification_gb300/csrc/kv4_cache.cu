@@ -16,7 +16,13 @@
 //
 // A lane has 8 channels of a record, two lanes share a scale: 16-byte loads of
 // bf16, and a record of D 128 is written (or read) by one warp as 128 + 16 bytes in
-// one piece.  Bound by HBM: 4 D bytes of bf16 and one record per row.
+// one piece.  Traffic is 4 D bytes of bf16 and one record per row, but writing is
+// bound by its arithmetic (a prompt's rows: issue 79 %, arithmetic 74 %, DRAM 59 %),
+// and gathered reads by the latency of their loads (issue 61 %, DRAM 48 %).
+//
+// Measured: a prompt's rows written and read back (1375 MB) 244 us, 5.6 TB/s;
+// gathered rows read (172 MB) 44 us, 3.9 TB/s; a single row written and
+// read back 4.0 us.
 #include <algorithm>
 
 #include "dustin.h"
