@@ -232,11 +232,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ float lo_of(uint64_t x) { return __uint_as_float((uint32_t)x); }
 __device__ __forceinline__ float hi_of(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -880,11 +875,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             float by[2] = {1.f, 1.f};
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
+              // Rounded down: where neighbouring scores are 16 apart, 8 - top is a tie,
+              // and rounded up it would make this very score's exponent 16, past f16.
+              const float to_be = __fsub_rd(kBelow, top[y]);
               if (fresh) {
-                old[y] = top[y] == -INFINITY ? 0.f : kBelow - top[y];
+                old[y] = top[y] == -INFINITY ? 0.f : to_be;
               } else if (top[y] + old[y] > kBelow) {
-                by[y] = ex2(kBelow - top[y] - old[y]);
-                old[y] = kBelow - top[y];
+                by[y] = ex2(to_be - old[y]);
+                old[y] = to_be;
                 moves = true;
               }
             }
@@ -912,12 +910,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_wait_st();
           }
-          // The scaled score rounded as the maximum was: a weight is at most
-          // 2^8 here, whatever the size of the scores.
+          // The scaled score rounded as the maximum was, the reference down: a weight is
+          // at most 2^8 here, whatever the size of the scores.  (Not in pairs: a product
+          // and a sum of pairs become one operation, .rn or not, whose product is not
+          // rounded: half a step of a score past 2^28 takes the weight out of f16.)
 #pragma unroll
           for (int g = 0; g < G; ++g)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[g][k] = add2(mul2(x[g][k], qs[g]), minus[g]);
+            for (int k = 0; k < 4; ++k)
+              x[g][k] = pack2(__fadd_rn(__fmul_rn(lo_of(x[g][k]), lo_of(qs[g])), lo_of(minus[g])),
+                              __fadd_rn(__fmul_rn(hi_of(x[g][k]), hi_of(qs[g])), hi_of(minus[g])));
           if ((dead.x & dead.y & dead.z & dead.w) != ~0u) fresh = false;
         }
         // All have read S: they have voted since.

@@ -599,3 +599,33 @@ def test_streams_workspaces_and_graphs():
     for (_, o, lse), want in zip(made, alone):
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
     assert flags() == 0
+
+
+@pytest.mark.parametrize("idx", [None, "some"])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_weights_stay_finite_where_scores_are_far_apart_in_fp32(sign, idx):
+    """Row maxima of either sign up to 2^29 and more (log2 units), where 8 is half of
+    what neighbouring fp32 numbers are apart, or less: no weight leaves f16, and the
+    largest score takes all.  A score is off by 128 * 2^-23 of sum |q k| scale, here less
+    than four times the score: by less than 2^-14 of it; a gap of 10^-4 is clear."""
+    c = Case(4, 8, 1, 64, 2, 900, idx=idx, win=False, seed=17)
+    c.rec[:, :, :, 0] = 0x22                                 # K channels 0, 1 are positive
+    c.q[..., 0] = 512.0 * sign
+    k, v = Q.dequantise(c.rec, 64)
+    clear = ties = 0
+    for scale in np.geomspace(2e5, 6e6, 14):
+        c.scale = float(np.float32(scale))
+        o, lse = (f64(x) for x in c.run())
+        assert np.isfinite(o).all() and np.isfinite(lse).all()
+        for i, at in enumerate(c.seen()):
+            s = np.einsum("htd,nd->htn", f64(c.q[i]), k[i, 0, at]) * c.scale
+            best, order = s.argmax(-1), np.sort(s, -1)
+            assert (order[..., -1] * sign > 0).all()
+            ties += (np.abs(order[..., -1]) * np.log2(np.e) // 2 ** 27 == 1).sum()
+            np.testing.assert_allclose(lse[i], order[..., -1], rtol=1e-4)
+            gap = order[..., -1] - order[..., -2] > 1e-4 * np.abs(order[..., -1])
+            for h, t in zip(*np.nonzero(gap)):
+                np.testing.assert_allclose(o[i, h, t], v[i, 0, at[best[h, t]]], rtol=2.0 ** -8, atol=0)
+                clear += 1
+    assert clear > 500 and ties > 100
+    assert flags() == 0
