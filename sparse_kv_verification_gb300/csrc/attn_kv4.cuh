@@ -44,6 +44,7 @@
 // pv_ready and o_done); with a wait at each segment's last tile 194, with o_done 184.
 #pragma once
 
+#include <cfloat>
 #include <cstddef>
 
 #include "dustin.h"
@@ -834,6 +835,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           float (&to)[4][kKv4Rows] = sh.exchange[buf][turn];
           turn ^= 1;
           load();
+          // Scaled here, one by one, and rounded: a product and a sum of pairs are fused,
+          // .rn or not, and half a step of a score past 2^28 takes its weight out of f16.
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              x[g][k] = pack2(__fmul_rn(lo_of(x[g][k]), lo_of(qs[g])), __fmul_rn(hi_of(x[g][k]), hi_of(qs[g])));
           if (dead.x | dead.y | dead.z | dead.w) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -852,8 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, d));
             }
             if (lane < 4)
-              *reinterpret_cast<float2*>(&to[q][8 * g + col]) =
-                  make_float2(__fmul_rn(t0, lo_of(qs[g])), __fmul_rn(t1, hi_of(qs[g])));
+              *reinterpret_cast<float2*>(&to[q][8 * g + col]) = make_float2(t0, t1);
           }
           tc_fence_before();
           if (vote(bar, !ok)) {
@@ -865,7 +872,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool moves = false;
 #pragma unroll
           for (int g = 0; g < G; ++g) {
-            float top[2] = {-INFINITY, -INFINITY}, old[2] = {lo_of(minus[g]), hi_of(minus[g])};
+            // A row without a score above -inf gets the reference of -3.4e38, which any
+            // other score moves; its O and sum are 0.
+            float top[2] = {-FLT_MAX, -FLT_MAX}, old[2] = {lo_of(minus[g]), hi_of(minus[g])};
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
               const float2 t = *reinterpret_cast<const float2*>(&to[w][8 * g + col]);
@@ -879,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               // and rounded up it would make this very score's exponent 16, past f16.
               const float to_be = __fsub_rd(kBelow, top[y]);
               if (fresh) {
-                old[y] = top[y] == -INFINITY ? 0.f : to_be;
+                old[y] = to_be;
               } else if (top[y] + old[y] > kBelow) {
                 by[y] = ex2(to_be - old[y]);
                 old[y] = to_be;
@@ -910,16 +919,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_wait_st();
           }
-          // The scaled score rounded as the maximum was, the reference down: a weight is
-          // at most 2^8 here, whatever the size of the scores.  (Not in pairs: a product
-          // and a sum of pairs become one operation, .rn or not, whose product is not
-          // rounded: half a step of a score past 2^28 takes the weight out of f16.)
+          // As the maximum was rounded, and the reference down: a weight is at most 2^8
+          // here, whatever the size of the scores.
 #pragma unroll
           for (int g = 0; g < G; ++g)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              x[g][k] = pack2(__fadd_rn(__fmul_rn(lo_of(x[g][k]), lo_of(qs[g])), lo_of(minus[g])),
-                              __fadd_rn(__fmul_rn(hi_of(x[g][k]), hi_of(qs[g])), hi_of(minus[g])));
+            for (int k = 0; k < 4; ++k) x[g][k] = add2(x[g][k], minus[g]);
           if ((dead.x & dead.y & dead.z & dead.w) != ~0u) fresh = false;
         }
         // All have read S: they have voted since.

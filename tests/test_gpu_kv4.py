@@ -629,3 +629,58 @@ def test_weights_stay_finite_where_scores_are_far_apart_in_fp32(sign, idx):
                 clear += 1
     assert clear > 500 and ties > 100
     assert flags() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("idx", [None, "first"])
+def test_tiles_without_a_finite_score_before_others(idx, d):
+    """Scores of -6 * 2^126 are beyond fp32 and so -inf, those of -0.25 * 2^126 are not: a
+    row that meets only the first in a segment's first tiles sees the others all the same,
+    beside rows that have finite scores everywhere; and a row that sees none is empty."""
+    b, hkv, n = 76, 2, 1024                                  # eight tiles a unit, one unit a CTA of 152
+    c = Case(b, 6 * hkv, hkv, d, 1, n, win=False, seed=d,
+             idx=None if idx is None else torch.arange(n).expand(b, n))
+    c.scale = 2.0 ** 126
+    far = torch.arange(n).view(1, n) < torch.arange(b).view(b, 1) % 7 * 128 + 128
+    far[3] = True                                            # nothing else
+    far = far.numpy()[:, None].repeat(hkv, 1)
+    c.rec[..., 0] = np.where(far, 0xf, 0x9)                  # K channels 0, 1: code -6 or -0.5, and 0
+    c.rec[..., d] = np.where(far, 0x38, 0x30)                # of scale 1 or 0.5
+    c.q = c.q * 2.0 ** -128
+    c.q[:, ::2] = 0
+    c.q[:, ::2, :, 0] = 1.0                                  # every other row: the score is K's channel 0
+    o, lse = c.run()
+    ro, rl, spread = c.oracle()
+    none = np.broadcast_to((far.all(-1).repeat(6, 1) & (np.arange(6 * hkv) % 2 == 0))[..., None], rl.shape)
+    ro[none], rl[none] = 0, -np.inf
+    with np.errstate(invalid="ignore"):
+        large = rl < -1e30                                   # held to 2^-20 of themselves
+    assert none.sum() == 6 and large.sum() == 6 * b
+    got, finite = f64(lse), large & ~none
+    np.testing.assert_allclose(got[finite], rl[finite], rtol=2.0 ** -20)
+    fill = torch.from_numpy(np.where(finite, rl, got))
+    check(o, fill, (ro, rl, spread))
+    assert flags() == 0
+
+
+@pytest.mark.parametrize("idx", [None, "first"])
+def test_scores_past_fp32_are_infinite(idx):
+    """6 * 2^126 in the first tile, in a later one or in the last position of all: NaN, for
+    the rows that meet it only."""
+    b, n = 152, 1024                                         # eight tiles a unit, one unit a CTA of 152
+    c = Case(b, 4, 1, 64, 1, n, win=False, seed=8, idx=None if idx is None else torch.arange(n).expand(b, n))
+    c.scale = 2.0 ** 126
+    c.rec[..., 0], c.rec[..., 64] = 0x09, 0x30               # K channels 0, 1: -0.25 and 0
+    at = [0, 100, 300, 600, 1023, None]
+    for i in range(b):
+        if at[i % 6] is not None:
+            c.rec[i, 0, at[i % 6], 0], c.rec[i, 0, at[i % 6], 64] = 0x07, 0x38   # 6
+    c.q = c.q * 2.0 ** -128
+    c.q[:, ::2] = 0
+    c.q[:, ::2, :, 0] = 1.0
+    o, lse = (f64(x) for x in c.run())
+    want = np.zeros(lse.shape, bool)
+    want[np.arange(b) % 6 != 5, ::2] = True
+    np.testing.assert_array_equal(np.isnan(lse), want)
+    np.testing.assert_array_equal(np.isnan(o), np.broadcast_to(want[..., None], o.shape))
+    assert np.isfinite(lse[~want]).all() and flags() == 0
