@@ -1296,7 +1296,7 @@ int dustin_kv4_verify_attn(int b, int h_q, int h_kv, int d, int w, int n, int k,
   a.idx = idx;
   a.k_len = k_len;
   a.n = n;
-  a.scale_log2 = scale * kLog2e;
+  a.scale = scale;
   cudaError_t e = launch_attn_kv4(a, sm_count(), ws, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, what);
   return DUSTIN_OK;

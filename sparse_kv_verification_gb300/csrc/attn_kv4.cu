@@ -9,6 +9,7 @@
 //   l = sum_i 2^(m_i - M) l_i + sum_t 2^(s_t - M),  lse = ln 2 (M + log2 l),
 // in a fixed order.
 #include <algorithm>
+#include <cmath>
 
 #include "attn_kv4.cuh"
 
@@ -25,7 +26,7 @@ struct JoinArgs {
   float* lse;
   KvView win;
   int has_win, w, rows;          // rows: b * h_q * w
-  float scale_log2, v_unit;      // scale_log2 without 2^k_exp
+  float scale, v_unit;
 };
 
 // Weighted sums by a running maximum.
@@ -108,7 +109,8 @@ __global__ void __launch_bounds__(kJoinThreads, 8)
 #pragma unroll
       for (int i = 0; i < kInFlight; ++i) {
         if (t0 + i * W > last) s[i] = -INFINITY;
-        s[i] *= c.scale_log2;
+        // One after the other: scale * log2 e may be no fp32 number.
+        s[i] = __fmul_rn(s[i], c.scale) * kLog2e;
         part.raise(s[i]);
       }
 #pragma unroll
@@ -244,7 +246,8 @@ cudaError_t launch_attn_kv4(const Kv4AttnArgs& p, int sms, void* ws, cudaStream_
     a.run = kKv4Tile;
     if (p.kv.page_table)         // the largest power of two that divides page and tile
       while (p.kv.page_size % a.run) a.run >>= 1;
-    a.scale_log2 = ldexpf(p.scale_log2, p.kv.k_exp);
+    // Of 64 bits: the product is an ordinary fp32 number, scale * log2 e need not be.
+    a.scale_log2 = (float)std::ldexp((double)p.scale * 1.4426950408889634, p.kv.k_exp);
     cudaError_t e = p.d == 64 ? launch_attn_kv4_d64(a, gather, st) : launch_attn_kv4_d128(a, gather, st);
     if (e != cudaSuccess) return e;
   }
@@ -254,7 +257,7 @@ cudaError_t launch_attn_kv4(const Kv4AttnArgs& p, int sms, void* ws, cudaStream_
   c.has_win = p.has_win;
   c.w = p.w;
   c.rows = p.b * p.hq * p.w;
-  c.scale_log2 = p.scale_log2;
+  c.scale = p.scale;
   c.v_unit = ldexpf(1.f, p.kv.v_exp);
   return p.d == 64 ? join<64>(c, st) : join<128>(c, st);
 }

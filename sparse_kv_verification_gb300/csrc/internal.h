@@ -182,7 +182,7 @@ struct Kv4AttnArgs {
   const int* idx;           // [b][k] or null
   const int* k_len;         // [b] or null
   int b, hq, hkv, d, w, n, k, has_win;
-  float scale_log2;
+  float scale;
 };
 size_t attn_kv4_workspace(const Kv4AttnArgs& a, int sms);
 cudaError_t launch_attn_kv4(const Kv4AttnArgs& a, int sms, void* ws, cudaStream_t st);

@@ -684,3 +684,22 @@ def test_scores_past_fp32_are_infinite(idx):
     np.testing.assert_array_equal(np.isnan(lse), want)
     np.testing.assert_array_equal(np.isnan(o), np.broadcast_to(want[..., None], o.shape))
     assert np.isfinite(lse[~want]).all() and flags() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("idx", [None, "some"])
+@pytest.mark.parametrize("scale,k_exp,q_exp", [(2.0 ** 127.9, -64, -66), (3 * 2.0 ** -149, 64, 81),
+                                               (2.0 ** -149, 64, 83)])
+def test_scales_at_the_ends_of_fp32(scale, k_exp, q_exp, idx, d):
+    """scale * log2 e is no fp32 number, or one of few bits, while scale * 2^k_exp and the
+    scores are ordinary; and no cache at all, where a window alone meets the scale."""
+    c = Case(2, 8, 2, d, 2, 260, idx=idx, win=scale > 1, k_exp=k_exp, seed=9)
+    c.scale = float(np.float32(scale))
+    c.q = c.q * 2.0 ** q_exp                                 # |q| scale 2^k_exp is 1/4 or so
+    if c.win:
+        c.win[0] = c.win[0] * 2.0 ** k_exp
+    c.check(large=4)
+    if c.win:
+        c.k, c.idx = 0, None
+        c.check(large=4)
+    assert flags() == 0
