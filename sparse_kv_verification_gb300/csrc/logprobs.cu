@@ -134,6 +134,15 @@ __device__ __forceinline__ Sums join(const Sums& a, const Sums& b, float c2) {
   return r;
 }
 
+// sum += x, with what the roundings so far have added too much in `over` (Kahan): a
+// thread of a long row adds thousands of batches, each of which may be less than half a
+// step of the sum.  (One sum over all entries lost 2e-4 of 2^26 of them, 3e-3 of 2^30.)
+__device__ __forceinline__ void add_up(float& sum, float& over, float x) {
+  const float y = __fsub_rn(x, over), t = __fadd_rn(sum, y);
+  over = __fsub_rn(__fsub_rn(t, sum), y);
+  sum = t;
+}
+
 struct Shared {
   alignas(16) Key list[kList];
   Key best[kTop];
@@ -240,6 +249,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int last = (int)all - 1;
 
   Sums sum{-INFINITY, 0.f, 0.f};
+  float l_over = 0.f, s_over = 0.f;                    // what their roundings added
   uint4 next[kWords];
   auto load = [&](int base) {
 #pragma unroll
@@ -270,26 +280,28 @@ __global__ void __launch_bounds__(kThreads, 2)
       const float most = largest<T>(cur);
       if (pass == 0) {
         if (most > sum.m) {
-        const float t = fmaxf(exponent(sum.m, -0.5f * most, c2), kLeast), f = ex2(t);
-        sum.s = f * fmaf(sum.l, t, sum.s);
-        sum.l *= f;
-        sum.m = most;
-      }
-      const float half = sum.m == -INFINITY ? 0.f : -0.5f * sum.m;
-      const uint64_t half2 = pack2(half, half), scale2 = pack2(c2, c2), point5 = pack2(0.5f, 0.5f);
-      uint64_t l2 = pack2(sum.l, 0.f), s2 = pack2(sum.s, 0.f);
-#pragma unroll
-      for (int u = 0; u < kWords; ++u)
-#pragma unroll
-        for (int i = 0; i < V; i += 2) {
-          // exponent(), two entries at a time
-          const uint64_t t = mul2(fma2(pack2(v(u, i), v(u, i + 1)), point5, half2), scale2);
-          const uint64_t e = pack2(ex2(lo_of(t)), ex2(hi_of(t)));
-          l2 = add2(l2, e);
-          s2 = fma2(e, pack2(fmaxf(lo_of(t), kLeast), fmaxf(hi_of(t), kLeast)), s2);
+          const float t = fmaxf(exponent(sum.m, -0.5f * most, c2), kLeast), f = ex2(t);
+          sum.s = f * fmaf(sum.l, t, sum.s);
+          sum.l *= f;
+          sum.m = most;
+          l_over *= f;
+          s_over *= f;
         }
-      sum.l = lo_of(l2) + hi_of(l2);
-      sum.s = lo_of(s2) + hi_of(s2);
+        const float half = sum.m == -INFINITY ? 0.f : -0.5f * sum.m;
+        const uint64_t half2 = pack2(half, half), scale2 = pack2(c2, c2), point5 = pack2(0.5f, 0.5f);
+        uint64_t l2 = 0, s2 = 0;
+#pragma unroll
+        for (int u = 0; u < kWords; ++u)
+#pragma unroll
+          for (int i = 0; i < V; i += 2) {
+            // exponent(), two entries at a time
+            const uint64_t t = mul2(fma2(pack2(v(u, i), v(u, i + 1)), point5, half2), scale2);
+            const uint64_t e = pack2(ex2(lo_of(t)), ex2(hi_of(t)));
+            l2 = add2(l2, e);
+            s2 = fma2(e, pack2(fmaxf(lo_of(t), kLeast), fmaxf(hi_of(t), kLeast)), s2);
+          }
+        add_up(sum.l, l_over, lo_of(l2) + hi_of(l2));
+        add_up(sum.s, s_over, lo_of(s2) + hi_of(s2));
       }
       if (top == 0) continue;
 
@@ -404,6 +416,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 
   // Sums: lanes, warps, CTAs.
+  sum.l -= l_over;
+  sum.s -= s_over;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) {
     const Sums o{__shfl_xor_sync(0xffffffffu, sum.m, d), __shfl_xor_sync(0xffffffffu, sum.l, d),

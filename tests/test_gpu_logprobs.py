@@ -188,3 +188,25 @@ def test_equal_calls_give_equal_bits_and_peaks_are_exact():
     tokens[0, 0, 0] = 77
     lp, ent, lse, ids, _ = check(x, tokens, 3)
     assert lp[0, 0, 0] == 0 and ent[0, 0] == 0 and ids[0, 0, 0] == 77
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_small_weights_behind_large_ones(dtype):
+    """2^26 logits of which each thread of eight CTAs meets one of 0 first and 2^14 of
+    -17.5 after it: each of these is less than half a step of the sum so far, together
+    they are 4e-4 of it."""
+    vocab, v = 1 << 26, 4 if dtype == torch.float32 else 8
+    j = torch.arange(vocab, device=DEV)
+    first = (j % (vocab // 8) < 512 * v) & (j % v == 0)
+    n = int(first.sum())
+    x = torch.where(first, 0.0, -17.5).to(dtype).view(1, 1, vocab)
+    tokens = torch.tensor([[[0, 1, vocab - 1]]], dtype=torch.int32)
+    lp, ent, lse, ids, best = run(x, tokens, 2)
+    small = math.exp(-17.5)
+    total = n + (vocab - n) * small
+    r_lse, r_ent = math.log(total), math.log(total) + (vocab - n) * small * 17.5 / total
+    assert n == 4096 and abs(math.log(n) - r_lse) > 4e-4
+    close(lse, [[r_lse]], 4e-5)
+    close(lp, [[[-r_lse, -17.5 - r_lse, -17.5 - r_lse]]], 4e-5 + 2.0 ** -22 * 30)
+    close(ent, [[r_ent]], 4e-5 * (1 + r_ent))
+    np.testing.assert_array_equal(ids, [[[0, v]]])
