@@ -617,8 +617,9 @@ int dustin_kv4_read(int n_layers, int b, int h_kv, int d, int n, int k,
  * 2^140 (they may still be infinite).
  * Limits: as dustin_sparse_verify_attn; with k > 0, scale * 2^k_exp in [2^-120, 2^126]
  * (DUSTIN_ERR_SHAPE); k <= n without idx; k <= 2^27; b <= 2^20;
- * (b * h_kv * blocks of 64 query rows) * (k / 128 + 1) <= 2^30; a workspace of 2^35
- * bytes.
+ * (b * h_kv * blocks of 64 query rows) * (k / 128 + 1) <= 2^30, and with k > 2^25 at
+ * most 256 such blocks (an SM's share of longer ones could outlast a wait's second); a
+ * workspace of 2^35 bytes.
  * Workspace: dustin_kv4_verify_attn_workspace_size (with or without win, idx);
  * its content need not be kept, and calls that may run at the same time (two
  * streams, two captured graphs) have one each. */

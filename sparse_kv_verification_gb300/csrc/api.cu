@@ -1231,6 +1231,12 @@ static int check_kv4_shape(int b, int h_q, int h_kv, int d, int w, int k, const 
   const double units = (double)b * h_kv * (((double)(h_q / h_kv) * w + 63) / 64 + 1);
   if (b > (1 << 20) || k > (1 << 27) || units * (k / 128 + 1.0) > (double)(1 << 30))
     return fail(DUSTIN_ERR_SHAPE, "%s: problem too large", what);
+  // A CTA that has five units or more (so 3 to an SM) waits for whole ones of k / 128
+  // tiles, each taking up to 2 us, and a wait ends after a second.
+  const long long blocks = (long long)b * h_kv * (((long long)(h_q / h_kv) * w + 63) / 64);
+  if (k > (1 << 25) && blocks > 256)
+    return fail(DUSTIN_ERR_SHAPE, "%s: k=%d with %lld blocks of rows (256 past 2^25 positions)", what,
+                k, blocks);
   return DUSTIN_OK;
 }
 

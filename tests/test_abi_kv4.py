@@ -179,3 +179,17 @@ def test_caches_of_two_devices_are_refused(calls):  # noqa: F811
     with pytest.raises(ValueError, match="one device"):
         native.dustin_kv4_write([rows, rows], [a, b], 1, 1, 64, 4, 1)
     assert not calls
+
+
+def test_attention_refuses_parts_longer_than_a_wait(lib):
+    """Where a CTA has five units or more, the warp that deals them out waits for whole
+    ones, at most 2^18 tiles of 128 positions."""
+    def call(hkv, k, w=1):
+        kv = desc4()
+        return lib.dustin_kv4_verify_attn(1, hkv, hkv, 64, w, 1, k, FAKE, ctypes.byref(kv), FAKE, None,
+                                          None, 0.1, FAKE, FAKE, None, 0, 0, None)
+    size = lib.dustin_kv4_verify_attn_workspace_size
+    assert call(760, 1 << 26) == 2 and call(257, (1 << 25) + 1) == 2 and call(3, 1 << 26, w=64 * 86) == 2
+    assert size(1, 257, 257, 64, 1, 1 << 26) == 0 and size(257, 1, 1, 64, 1, 1 << 26) == 0
+    for hkv, k, w in ((256, 1 << 26, 1), (760, 1 << 25, 1), (3, 1 << 26, 64 * 85)):
+        assert call(hkv, k, w) == 4 and size(1, hkv, hkv, 64, w, k) > 0      # as far as the workspace
