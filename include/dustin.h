@@ -529,7 +529,9 @@ int dustin_kv_resize(int n_seqs, int pages_per_seq, int page_size, int num_pages
  * A value is e2m1(code) * e4m3(scale) * 2^exp, with k_exp for K and v_exp for V;
  * e2m1 has the values 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign (bit 3), e4m3 finite ones
  * up to 448, NaN (0x7f) and a sign that writing never sets.  All of it is exact in
- * bf16.
+ * bf16.  Scoring, page statistics, compaction and the copies of dustin_kv_resize take
+ * bf16 rows only: what they are to see of such a cache is read back first, and a forked
+ * page of it is copied by the caller.
  *
  * Contiguous layout (page_table == NULL): the record of (b, kv head h, position
  * j) is at data + b*stride_b + h*stride_h + j*stride_n.  Paged: position j of
@@ -606,8 +608,9 @@ int dustin_kv4_read(int n_layers, int b, int h_kv, int d, int n, int k,
  *   k_len  int32 [b], device, or NULL (k each); clamped to [0, k]
  * Records behind the lengths are never used, whatever they hold.  A row that sees
  * no position, or only scores of -inf, gives o = 0, lse = -inf.  A row with a
- * score that is NaN or +inf gives NaN, o and lse (scores beyond fp32 count as
- * infinite).  DUSTIN_ATTN_KV_READY is accepted, without effect.  Sums are taken in a
+ * score that is NaN or +inf gives NaN, o and lse (scores beyond fp32, in units of
+ * log 2, count as infinite, and so do products q . K of the window).
+ * DUSTIN_ATTN_KV_READY is accepted, without effect.  Sums are taken in a
  * fixed order: equal calls give equal bits.
  * Precision: cached values enter exactly, q as well (entries 2^-37 below their row's
  * largest are rounded); scores, maxima, sums and partial results are fp32.  A
@@ -658,6 +661,11 @@ int dustin_kv4_verify_attn(int b, int h_q, int h_kv, int d, int w, int n, int k,
  *   top_ids int32 [b][w][top];  top_logprobs fp32 [b][w][top]  (NULL if top is 0)
  * Rows may start at any element; they are read in aligned words of 16 bytes, so
  * bytes beside a row may be read too (never used).  Equal calls give equal bits.
+ * Precision: weights and sums are fp32.  lse and the log probabilities are off by 4e-5
+ * + 2^-22 of their size at most, the entropy by 4e-5 (1 + entropy), mostly by some 1e-7;
+ * 2^-22 more for each 16384 entries (8192 in fp32) at whose end a thread's largest has
+ * grown, which matters for rows of millions that rise all along.  These are absolute:
+ * of a token with probability 1 - 1e-9 the log probability may be 0, and the entropy.
  * b == 0 or w == 0 is a no-op.  Limits: 1 <= vocab <= 2^30, b * w <= 2^27; m <= 512;
  * top <= min(vocab, 64); 0 < scale <= 2^100.  No workspace. */
 int dustin_token_logprobs(int b, int w, int vocab, int dtype, const void* logits,

@@ -34,14 +34,19 @@
 // (idx, or records apart) 4-11 load them and 12-15, 16-19 convert a stream's K and V.
 //
 // Measured (16 sequences x 32768 positions, 8 kv heads, D 128; bytes alone take 89
-// us): 184 us with 40 rows to a kv head, 135 with 8, 241 with 64; D 64 156; 2048
-// gathered positions each 37.  Parts left out of an earlier form of 28 warps (190 us
+// us): 177 us with 40 rows to a kv head, 135 with 8, 241 with 64, 466 with 128 (two
+// blocks, each of which reads and converts the cache); D 64 157; 2048 gathered positions
+// each 37, of which the join takes 8.  The instance of 49 to 64 rows spills (386 bytes of
+// stores; 2.7 % of its warps' instructions are such accesses, 0.1 % at 40 rows): its
+// softmax has 64 scores and 48 row factors to hold in 136 registers.  Parts left out of an earlier form of 28 warps (190 us
 // whole): without V's conversion 175, without K's 179, without both 164, without the
 // softmax 161; without all of these and the products 122: what is left looks like
 // the chain of waits between the roles.  How it got here: one stream 251 us; two
 // streams 187.  Weights in two buffers, K and V by warps of their own, Q brought by the
 // softmax warps and light first tiles read 171, but two waits were missing then (see
-// pv_ready and o_done); with a wait at each segment's last tile 194, with o_done 184.
+// pv_ready and o_done); with a wait at each segment's last tile 194, with o_done 184,
+// with the slow path's scores scaled as they are read 177.  (Such changes of rare code
+// move the whole by 10 %, either way: the fast path's registers change with it.)
 #pragma once
 
 #include <cfloat>

@@ -20,9 +20,10 @@
 // bound by its arithmetic (a prompt's rows: issue 79 %, arithmetic 74 %, DRAM 59 %),
 // and gathered reads by the latency of their loads (issue 61 %, DRAM 48 %).
 //
-// Measured: a prompt's rows written and read back (1375 MB) 244 us, 5.6 TB/s;
-// gathered rows read (172 MB) 44 us, 3.9 TB/s; a single row written and
-// read back 4.0 us.
+// Measured: a prompt's rows written and read back (1375 MB) 243 us, 5.7 TB/s (written
+// alone 139, read alone 106); gathered rows read (172 MB) 44 us, 3.9 TB/s; a single row
+// written and read back 4.0 us, up to 5 rows of 16 sequences in 16 layers 11: two
+// launches each, with the descriptors of 128 layers, 16 KB, as parameters.
 #include <algorithm>
 
 #include "dustin.h"

@@ -17,20 +17,25 @@
 // last of which is the next bound: some top * ln(row / batch) entries follow, taken
 // without a barrier.  (That and entries taken in pairs: 249 -> 191 us for a prompt's
 // rows; batches kept as they are read and the bound raised only where the list grew:
-// 176.)  Should
-// they not fit (rows that rise, or have few values above many equal ones), the list's
-// own `top`-th is a bound for a second pass, which cuts the list as it fills.  An
-// entry that equals a bound counts if its index is lower, so ties go to the lowest
-// index and equal entries (banned tokens at -inf) do not fill the list.  Places come
-// from counting better entries: no order of atomics shows.
+// 176.)  Should they not fit (rows that rise, or have few values above many equal
+// ones), the list's own `top`-th is a bound for a second pass, which cuts the list as it
+// fills.  An entry that equals a bound counts if its index is lower, so ties go to the
+// lowest index and equal entries (banned tokens at -inf) do not fill the list.  But each
+// of them is read again and compared by its index, one at a time: where the bound is
+// -inf or a value that most of the row has, that is most of the time (a prompt's rows with
+// all but 10 tokens banned: 565 us with one alternative, 1107 with 20; with all but
+// 1000 banned as without).  Places come from counting better entries: no order of
+// atomics shows.
 //
 // One cluster of C CTAs per row (C by the number of rows); rank 0 joins the parts
 // through distributed shared memory.  No workspace.  Many rows: no
-// pipe is full (issue 63 %, arithmetic 47 %, DRAM 44 %; stalls: barriers, waits of a
-// few cycles).  Few: the latency of a load batch, three barriers, the cluster's.
+// pipe is full (issue 65 %, arithmetic 42 %, DRAM 45 %; 14.6 instructions a logit, of
+// which the sums need some 6; stalls: barriers, waits of a few cycles).  Few: the
+// latency of a load batch, three barriers, the cluster's.
 //
-// Measured (2048 rows of 152064 in bf16, 623 MB): 176 us with one alternative, 3.5
-// TB/s; 136 without any, 4.6 TB/s; 221 with 20.  4 rows of 32000 in fp32: 9.1 us.
+// Measured (2048 rows of 152064 in bf16, 623 MB): 173 us with one alternative, 3.6
+// TB/s; 136 without any, 4.6 TB/s; 217 with 20; in fp32 212 and 198, 5.9 and 6.3 TB/s.
+// 4 rows of 32000 in fp32: 9.2 us.
 #include <algorithm>
 #include <climits>
 #include <cooperative_groups.h>
@@ -371,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int u = 0; u < kWords; ++u)
 #pragma unroll
           for (int i = 0; i < V; ++i) reach |= (unsigned)(v(u, i) >= least) << (u * V + i);
-        while (reach) {                                  // few
+        while (reach) {          // few, unless the bound is a value of most entries
           const Key key = entry(__ffs(reach) - 1);
           reach &= reach - 1;
           if (!key) continue;
