@@ -109,8 +109,9 @@ __global__ void __launch_bounds__(kJoinThreads, 8)
 #pragma unroll
       for (int i = 0; i < kInFlight; ++i) {
         if (t0 + i * W > last) s[i] = -INFINITY;
-        // One after the other: scale * log2 e may be no fp32 number.
-        s[i] = __fmul_rn(s[i], c.scale) * kLog2e;
+        // One after the other: scale * log2 e may be no fp32 number.  Rounded, not part of
+        // the difference below, or large scores would pass their own maximum.
+        s[i] = __fmul_rn(__fmul_rn(s[i], c.scale), kLog2e);
         part.raise(s[i]);
       }
 #pragma unroll

@@ -703,3 +703,31 @@ def test_scales_at_the_ends_of_fp32(scale, k_exp, q_exp, idx, d):
         c.k, c.idx = 0, None
         c.check(large=4)
     assert flags() == 0
+
+
+@pytest.mark.parametrize("k", [0, 200])
+def test_huge_scores_of_the_window(k):
+    """Scores of a window from 2^20 to past 2^100 (log2 units): the largest takes all, alone and
+    beside a cache."""
+    c = Case(4, 8, 1, 64, 12, 200, k=k, seed=23)
+    c.win[0] = c.win[0] * 4                                  # the window has the largest scores, mostly
+    keys, values = Q.dequantise(c.rec, 64)
+    clear = 0
+    for scale in np.geomspace(1e4, 1e32, 30):
+        c.scale = float(np.float32(scale))
+        o, lse = (f64(x) for x in c.run())
+        assert np.isfinite(o).all() and np.isfinite(lse).all()
+        for i in range(4):
+            for t in range(12):
+                a = np.concatenate([keys[i, 0, :k], f64(c.win[0][i, 0, :t + 1])])
+                v = np.concatenate([values[i, 0, :k], f64(c.win[1][i, 0, :t + 1])])
+                s = f64(c.q[i, :, t]) @ a.T * c.scale
+                size = (np.abs(f64(c.q[i, :, t])) @ np.abs(a).T).max(-1) * c.scale
+                order = np.sort(np.concatenate([s, np.full((8, 1), -np.inf)], -1), -1)
+                assert np.all(np.abs(lse[i, :, t] - order[:, -1]) <= 2.0 ** -14 * size + 6)
+                # Off by 128 * 2^-23 of sum |q k| scale at most.
+                for h in np.nonzero(order[:, -1] - order[:, -2] > 2.0 ** -13 * size + 100)[0]:
+                    np.testing.assert_allclose(o[i, h, t], v[s[h].argmax()], rtol=2.0 ** -8, atol=1e-25)
+                    clear += 1
+    assert clear > 5000
+    assert flags() == 0
